@@ -104,6 +104,9 @@ typedef struct {
 #define DA_DEV_NEG_LEN         4   /* cache_seqlens[b] < 0: treated as 0 */
 #define DA_DEV_TIMEOUT         8   /* a pipeline wait ran out of time: work unit abandoned */
 #define DA_DEV_META_MISMATCH  16   /* sched_meta was built for another desc */
+#define DA_DEV_BAD_TOKEN      32   /* a draft token >= vocab: taken as the end of its chain */
+#define DA_DEV_BAD_PROBS      64   /* a row without a positive probability: the next token is -1 */
+#define DA_DEV_BAD_REQUEST   128   /* a request index outside [0, B): the token's K and V are skipped */
 
 /*
  * Library plumbing from here to decode_attn_num_parts: no page defines these
@@ -263,6 +266,166 @@ int decode_attn_fwd_ex(const da_desc *desc, const void *q, const void *k_pool, c
 int decode_attn_append_kv(const da_desc *desc, const void *k_new, const void *v_new, int64_t new_row_stride,
                           const int32_t *positions, const int32_t *block_table, void *k_pool, void *v_pool,
                           const float *k_scale, const float *v_scale, int32_t *device_error, cudaStream_t stream);
+
+/* Rotary positions with one or several axes (host struct, passed by pointer,
+ * not retained). */
+typedef struct {
+    int32_t rot_dim;      /* rotated values per head: a multiple of 16 in [16, min(D_qk, 512)]; on the 656-byte
+                             format at most 64, the first rot_dim of the 64 RoPE values */
+    int32_t n_axes;       /* 1..4 (time, height, width, ...) */
+    int32_t sections[4];  /* pairs per axis, >= 0; the first n_axes sum to rot_dim / 2, the others are 0 */
+    int32_t interleaved;  /* 0: pairs in blocks, the first sections[0] follow axis 0, the next sections[1] axis 1, ...;
+                             1: alternating, pair i follows axis a = i mod n_axes while i / n_axes < sections[a],
+                             else axis 0 */
+    int32_t adjacent;     /* 0: pair i = values (i, i + rot_dim / 2); 1: values (2 i, 2 i + 1) */
+} da_rope;
+
+/*
+ * Rotary positions and KV append in one pass: rotates the queries and keys of
+ * new tokens and writes their K and V into the pool, any number of tokens per
+ * request (a draft chain, ragged prompts). With theta = rope_positions[axis(i)][n]
+ * * inv_freq[i], pair i of token n goes (x, y) -> (x cos theta - y sin theta,
+ * x sin theta + y cos theta) in every query and key head; values past rot_dim
+ * pass through. (No counterpart on the source pages, which append finished
+ * rows.)
+ *   desc: as for decode_attn_append_kv, and G (H_q = H_kv * G).
+ *   n_tokens: N >= 0 (0: nothing is launched). Token n belongs to request
+ *     requests[n]; requests = NULL: to request n / s_q, and N must be B * s_q.
+ *   q: bf16, token n's [H_q][D_qk] at q + n * q_stride. k_new, v_new: likewise
+ *     [H_kv][D]; on the 656-byte format k_new holds the 576 values of the latent
+ *     vector and v_new is NULL. Strides count bf16 elements (0: packed rows;
+ *     else at least the row and a multiple of 8), so the three may be slices of
+ *     one projection output.
+ *   inv_freq: fp32 [rot_dim / 2], radians per position. Angles are exact to
+ *     about 2^-31 of a turn at any int32 position.
+ *   rope_positions: int32 [n_axes][N]. positions: int32 [N], the token's index
+ *     in its request's cache (slot t % page_size of page block_table[b][t /
+ *     page_size]); negative: the token is skipped, its q_out row left as it was.
+ *   q_out: bf16 [N][H_q][D_qk], the q of decode_attn_fwd when the tokens come
+ *     request by request. It may be q itself (packed rows); else the two must
+ *     not overlap (DA_ERR_UNSUPPORTED).
+ *   k_pool, v_pool, k_scale, v_scale, device_error: as for decode_attn_append_kv.
+ *     Besides its bits, DA_DEV_BAD_REQUEST; such a token's q is still rotated.
+ * Products and sums are fp32; each value is rounded once, K to the pool's format
+ * from its fp32 value by the rules of decode_attn_append_kv. Two tokens that
+ * address the same slot race. Launches one kernel on `stream`. No allocation,
+ * no sync.
+ */
+int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_tokens, const void *q,
+                            int64_t q_stride, const void *k_new, int64_t k_stride, const void *v_new,
+                            int64_t v_stride, const float *inv_freq, const int32_t *rope_positions,
+                            const int32_t *requests, const int32_t *positions, const int32_t *block_table,
+                            void *q_out, void *k_pool, void *v_pool, const float *k_scale, const float *v_scale,
+                            int32_t *device_error, cudaStream_t stream);
+
+/*
+ * Attention weight gathered by cached tokens, the measure by which
+ * decode_attn_evict keeps them. After a decode step, for every token t < L_b of
+ * request b and KV head h,
+ *     w[t] <- (t < weighted_lens[b] ? decay * w[t] : 0)
+ *             + sum_j sum_g exp(sigma * q_{b,j,hG+g} . k_t - lse[b,j,hG+g])
+ * over the query tokens j <= num_accepted[b] that see t (t <= L_b - s_q + j).
+ * (No counterpart on the source pages.) bf16 and e4m3 formats, no sliding
+ * window (DA_ERR_UNSUPPORTED otherwise).
+ *   desc, q, k_pool, k_scale, block_table, cache_seqlens, sched_meta, lse: those
+ *     of the step's decode_attn_fwd call, with the same requirements; sinks
+ *     need no argument (they are in lse). Page errors go to sched_meta's word.
+ *   num_accepted: device int32 [B] or NULL (all s_q count): of a draft chain
+ *     whose verification accepted a drafts, query tokens 0..a count; negative:
+ *     none does.
+ *   weighted_lens: device int32 [B] or NULL (all of L_b): the tokens that have
+ *     a weight already; the others (this step's, a prompt's at the first call)
+ *     start from 0, whatever their slot held.
+ *   decay: finite, >= 0.
+ *   weights: device fp32 [num_pages][H_kv][page_size], written in place; only
+ *     slots of tokens t < L_b change. A page that two requests share would be
+ *     updated by both: give every request pages of its own.
+ * A query row whose lse is -inf adds nothing. Each weight is summed in fp32 in
+ * a fixed order. Launches one kernel on `stream`. No allocation, no sync.
+ */
+int decode_attn_accum_weights(const da_desc *desc, const void *q, const void *k_pool, const float *k_scale,
+                              const int32_t *block_table, const int32_t *cache_seqlens, void *sched_meta,
+                              size_t sched_meta_bytes, const float *lse, const int32_t *num_accepted,
+                              const int32_t *weighted_lens, float decay, float *weights, cudaStream_t stream);
+
+/*
+ * Eviction: cuts every request's cache down to `budget` tokens per KV head,
+ * copied in their order to the pages of a second block table. (No counterpart
+ * on the source pages.) For request b and KV head h: all tokens when L_b <=
+ * budget; else the first keep_first, the last keep_last, and of those between
+ * them the heaviest by `weights`, budget tokens in all. Equal weights (-0 = +0):
+ * the lower position is kept; a NaN weighs more than any number. Heads choose
+ * independently, so slot i of a page may hold different tokens of different
+ * heads: positions have to be in the keys already (rotated).
+ *   desc: B, H_kv, D_qk, D_v, page_size, max_pages_per_seq, num_pages and
+ *     kv_dtype are used. bf16 pools need D_qk == D_v, a multiple of 8, e4m3 pools
+ *     a multiple of 16; the 656-byte token as for decode_attn_append_kv.
+ *   budget >= 1, at most max_pages_per_seq * page_size; keep_first, keep_last >=
+ *     0 with keep_first + keep_last <= budget.
+ *   block_table, dst_block_table: device int32 [B][max_pages_per_seq]; entries
+ *     past ceil(L_b / P) and past ceil(min(L_b, budget) / P) are never read. The
+ *     pages of dst_block_table must be distinct and hold no token that this call
+ *     reads. Afterwards dst_block_table is the requests' block table.
+ *   k_pool, v_pool (NULL or k_pool for the 656-byte token), weights (fp32
+ *     [num_pages][H_kv][page_size]): written in the kept tokens' new slots only.
+ *   kept: device int32 [B][H_kv][budget], the kept positions in ascending order,
+ *     then -1. new_seqlens: device int32 [B], min(L_b, budget); not
+ *     cache_seqlens itself (DA_ERR_UNSUPPORTED).
+ *   device_error: device int32 or NULL; DA_DEV_NEG_LEN (taken as 0),
+ *     DA_DEV_SEQ_TOO_LONG (clamped) and DA_DEV_BAD_PAGE (a token on a page
+ *     outside [0, num_pages) weighs less than any other; its row, or one whose
+ *     new page is outside, is not copied) are OR-ed into it.
+ * Launches two kernels on `stream`. No allocation, no sync.
+ */
+int decode_attn_evict(const da_desc *desc, int32_t budget, int32_t keep_first, int32_t keep_last,
+                      const int32_t *cache_seqlens, const int32_t *block_table, const int32_t *dst_block_table,
+                      void *k_pool, void *v_pool, float *weights, int32_t *kept, int32_t *new_seqlens,
+                      int32_t *device_error, cudaStream_t stream);
+
+/* Types of the probabilities of decode_attn_verify_drafts. */
+typedef enum {
+    DA_PROB_F32 = 0,
+    DA_PROB_BF16 = 1,
+    DA_PROB_F16 = 2
+} da_prob_dtype;
+
+/*
+ * Verification of a chain of drafted tokens against the target's probabilities,
+ * from given random numbers: the step after a decode call with s_q = n_draft + 1
+ * query tokens (XQA page, section "投机解码:XQA 的第二个工作负载", ends at the
+ * attention; the rule is not there). Request b has K = n_draft drafts x_0 ..
+ * x_{K-1}, the target's probabilities p_0 .. p_K (p_j after the first j drafts)
+ * and the draft model's q_0 .. q_{K-1}. Draft j is accepted when u_j * q_j(x_j)
+ * < p_j(x_j), compared exactly, and all before it were. With a drafts accepted,
+ * the next token is drawn from max(p_a - q_a, 0) where draft a was refused, from
+ * p_a where the chain had ended: the first v for which the sum of the weights up
+ * to v exceeds floor(u_K * total), each weight its fp32 value rounded to a whole
+ * number of steps of 2^-44. The sums are exact integers.
+ *   B >= 1, n_draft in [0, 63] (0: draws one token per request), vocab V in
+ *     [1, 2^20], prob_dtype: of both probabilities.
+ *   target_probs: device, row j of request b at (b * (n_draft + 1) + j) *
+ *     target_stride elements; draft_probs: (b * n_draft + j) * draft_stride, or
+ *     NULL for drafts that are certain (q_j(x_j) = 1). Strides: 0 for V, else >= V;
+ *     aligned to their type only.
+ *   draft_tokens: device int32 [B][n_draft]; a negative one ends its chain (ragged
+ *     chains), one >= V too (DA_DEV_BAD_TOKEN).
+ *   uniform: device fp32 [B][n_draft + 1] in [0, 1); u_K is clamped into it.
+ *   Probabilities that are NaN or negative count as 0 in the draw, above 1 as 1; a
+ *     comparison with NaN refuses the draft. Where no weight of p_a - q_a is left,
+ *     p_a is drawn from; where none of p_a either, the token is -1 (DA_DEV_BAD_PROBS).
+ *   num_accepted: device int32 [B], a. out_tokens: device int32 [B][n_draft + 1]:
+ *     the accepted drafts, the next token, then -1.
+ *   cache_seqlens, new_seqlens: device int32 [B], both or neither; new = L_b -
+ *     n_draft + a, the length that keeps the accepted drafts. They may be the same
+ *     buffer.
+ *   device_error: device int32 or NULL.
+ * Launches one kernel on `stream`. No allocation, no sync.
+ */
+int decode_attn_verify_drafts(int32_t B, int32_t n_draft, int32_t vocab, int32_t prob_dtype,
+                              const void *target_probs, int64_t target_stride, const void *draft_probs,
+                              int64_t draft_stride, const int32_t *draft_tokens, const float *uniform,
+                              const int32_t *cache_seqlens, int32_t *num_accepted, int32_t *out_tokens,
+                              int32_t *new_seqlens, int32_t *device_error, cudaStream_t stream);
 
 /*
  * Reads the device error word of sched_meta into *device_error (host int32).

@@ -22,6 +22,10 @@ KV_BF16 = 0
 KV_FP8 = 1
 KV_MLA656 = 2
 
+PROB_F32 = 0
+PROB_BF16 = 1
+PROB_F16 = 2
+
 DA_OK = 0
 DA_ERR_NULL = -1
 DA_ERR_DIMS = -2
@@ -37,6 +41,9 @@ DA_DEV_SEQ_TOO_LONG = 2
 DA_DEV_NEG_LEN = 4
 DA_DEV_TIMEOUT = 8
 DA_DEV_META_MISMATCH = 16
+DA_DEV_BAD_TOKEN = 32
+DA_DEV_BAD_PROBS = 64
+DA_DEV_BAD_REQUEST = 128
 
 LIB_PATH = _build_mod.LIB_PATH
 
@@ -59,6 +66,20 @@ class Desc(ctypes.Structure):
 class LaunchOpts(ctypes.Structure):
     _fields_ = [("use_pdl", ctypes.c_int32), ("main_begin", ctypes.c_void_p), ("main_end", ctypes.c_void_p),
                 ("sinks", ctypes.c_void_p), ("indices", ctypes.c_void_p)]
+
+
+class Rope(ctypes.Structure):
+    """Rotary positions with one or several axes (da_rope in the header)."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+                ("interleaved", ctypes.c_int32), ("adjacent", ctypes.c_int32)]
+
+    @classmethod
+    def make(cls, rot_dim, sections=None, interleaved=False, adjacent=False):
+        """``sections``: pairs per axis (default: one axis with all of them)."""
+        sections = [rot_dim // 2] if sections is None else [int(x) for x in sections]
+        if not 1 <= len(sections) <= 4:
+            raise DecodeAttnError("1 to 4 axes are supported")
+        return cls(rot_dim, len(sections), (ctypes.c_int32 * 4)(*sections), int(interleaved), int(adjacent))
 
 
 class DecodeAttnError(RuntimeError):
@@ -87,11 +108,18 @@ def load_library(path: str = LIB_PATH):
     lib.decode_attn_fwd_ex.argtypes = [DP, P, P, P, P, P, P, P, P, SZ, P, P, ctypes.POINTER(LaunchOpts), P]
     lib.decode_attn_get_error.argtypes = [P, ctypes.POINTER(I32), P]
     lib.decode_attn_append_kv.argtypes = [DP, P, P, ctypes.c_int64, P, P, P, P, P, P, P, P]
+    I64, F32 = ctypes.c_int64, ctypes.c_float
+    lib.decode_attn_rope_append.argtypes = [DP, ctypes.POINTER(Rope), I32, P, I64, P, I64, P, I64, P, P, P, P, P, P,
+                                            P, P, P, P, P, P]
+    lib.decode_attn_accum_weights.argtypes = [DP, P, P, P, P, P, P, SZ, P, P, P, F32, P, P]
+    lib.decode_attn_evict.argtypes = [DP, I32, I32, I32, P, P, P, P, P, P, P, P, P, P]
+    lib.decode_attn_verify_drafts.argtypes = [I32, I32, I32, I32, P, I64, P, I64, P, P, P, P, P, P, P, P]
     lib.decode_attn_strerror.argtypes = [ctypes.c_int]
     lib.decode_attn_strerror.restype = ctypes.c_char_p
     for f in ("decode_attn_sched_meta_bytes", "decode_attn_meta_offsets", "decode_attn_num_parts",
               "decode_attn_sched_meta", "decode_attn_fwd", "decode_attn_fwd_ex", "decode_attn_get_error",
-              "decode_attn_append_kv"):
+              "decode_attn_append_kv", "decode_attn_rope_append", "decode_attn_accum_weights", "decode_attn_evict",
+              "decode_attn_verify_drafts"):
         getattr(lib, f).restype = ctypes.c_int
     _libs[path] = lib
     return lib
@@ -189,6 +217,151 @@ def append_kv(desc: Desc, k_new, v_new, positions, block_table, k_pool, v_pool, 
         _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(device_error), _stream(stream)))
 
 
+def _device():
+    """The current CUDA device's index (one that no tensor has, before CUDA is in use)."""
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _need(dev, name, t, dtype, shape=None):
+    """A contiguous tensor of this dtype (and shape) on device ``dev``; its address."""
+    if not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape)):
+        want = "" if shape is None else f" of shape {tuple(shape)}"
+        raise DecodeAttnError(f"{name}: want a contiguous {dtype} tensor{want} on the current CUDA device, "
+                              f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _opt(dev, name, t, dtype, shape=None):
+    return None if t is None else _need(dev, name, t, dtype, shape)
+
+
+def _rows(dev, name, t, dtype, n, width):
+    """n rows of `width` contiguous values; their address and the distance between rows."""
+    d = t.dim()
+    if not (t.dtype is dtype and t.get_device() == dev and d in (2, 3) and t.shape[0] == n and t.numel() == n * width
+            and t.stride(d - 1) == 1 and (d == 2 or t.stride(1) == t.shape[2])):
+        raise DecodeAttnError(f"{name}: want a {dtype} tensor of {n} rows of {width} contiguous values on the current "
+                              f"CUDA device, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+    return t.data_ptr(), (t.stride(0) if n > 1 else width)
+
+
+def _pool(dev, name, t, desc):
+    """A pool of this desc, given by its bytes ([num_pages][page_size][H_kv][row]); its address."""
+    row = 656 if desc.kv_dtype == KV_MLA656 else desc.D_qk * (2 if desc.kv_dtype == KV_BF16 else 1)
+    if not (t.get_device() == dev and t.is_contiguous()
+            and t.numel() * t.element_size() == desc.num_pages * desc.page_size * desc.H_kv * row):
+        raise DecodeAttnError(f"{name}: not a pool of this desc on the current CUDA device "
+                              f"({t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()})")
+    return t.data_ptr()
+
+
+def rope_append(desc: Desc, rope: Rope, q, k_new, v_new, inv_freq, rope_positions, positions, block_table, q_out,
+                k_pool, v_pool, k_scale=None, v_scale=None, requests=None, device_error=None, stream=None, lib=None):
+    """Rotate the new tokens' q and K by their positions (one or several axes)
+    and write K and V into the pool, any number of tokens per request; see
+    decode_attn_rope_append in the header. ``q`` [N, H_q * D] (or [N, H_q, D]),
+    ``k_new`` and ``v_new`` [N, H_kv * D] (v_new None and k_new [N, 576] for the
+    656-byte token) may be column slices of one projection output;
+    ``rope_positions`` int32 [n_axes, N], ``positions`` and ``requests`` int32
+    [N]. ``q_out`` bf16 [N, H_q, D] may be ``q``."""
+    import torch
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    dev, n, D, heads = _device(), positions.numel(), desc.D_qk, (desc.H_kv,)
+    q_len, kv_len = desc.H_kv * desc.G * D, desc.H_kv * D
+    qp, qs = _rows(dev, "q", q, bf16, n, q_len)
+    kp, ks = _rows(dev, "k_new", k_new, bf16, n, kv_len)
+    vp, vs = (None, 0) if v_new is None else _rows(dev, "v_new", v_new, bf16, n, kv_len)
+    if q_out.numel() != n * q_len:
+        raise DecodeAttnError(f"q_out: want {n} rows of {q_len} values, got {tuple(q_out.shape)}")
+    _check((lib or load_library()).decode_attn_rope_append(
+        ctypes.byref(desc), ctypes.byref(rope), n, qp, qs, kp, ks, vp, vs,
+        _need(dev, "inv_freq", inv_freq, f32, (rope.rot_dim // 2,)),
+        _need(dev, "rope_positions", rope_positions, i32, (rope.n_axes, n)),
+        _opt(dev, "requests", requests, i32, (n,)), _need(dev, "positions", positions, i32),
+        _need(dev, "block_table", block_table, i32, (desc.B, desc.max_pages_per_seq)),
+        _need(dev, "q_out", q_out, bf16), _pool(dev, "k_pool", k_pool, desc),
+        None if v_pool is None else _pool(dev, "v_pool", v_pool, desc), _opt(dev, "k_scale", k_scale, f32, heads),
+        _opt(dev, "v_scale", v_scale, f32, heads), _opt(dev, "device_error", device_error, i32), _stream(stream)))
+
+
+def accum_weights(desc: Desc, q, k_pool, k_scale, block_table, cache_seqlens, meta, lse, weights, num_accepted=None,
+                  weighted_lens=None, decay=1.0, stream=None, lib=None):
+    """Add the softmax weights of the step's attention call to ``weights`` (fp32
+    [num_pages, H_kv, page_size]); q, block_table, cache_seqlens, meta and lse are
+    that call's. ``num_accepted`` int32 [B]: query tokens 0..a of a verified chain
+    count; ``weighted_lens`` int32 [B]: tokens past it start from 0. See
+    decode_attn_accum_weights in the header."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    dev, B = _device(), desc.B
+    rows = B * max(1, desc.s_q) * desc.H_kv * desc.G
+    if q.numel() != rows * desc.D_qk or lse.numel() != rows:
+        raise DecodeAttnError(f"q {tuple(q.shape)} and lse {tuple(lse.shape)} are not of this desc")
+    _check((lib or load_library()).decode_attn_accum_weights(
+        ctypes.byref(desc), _need(dev, "q", q, torch.bfloat16), _pool(dev, "k_pool", k_pool, desc),
+        _opt(dev, "k_scale", k_scale, f32, (desc.H_kv,)),
+        _need(dev, "block_table", block_table, i32, (B, desc.max_pages_per_seq)),
+        _need(dev, "cache_seqlens", cache_seqlens, i32, (B,)), _need(dev, "meta", meta, meta.dtype),
+        meta.numel() * meta.element_size(), _need(dev, "lse", lse, f32),
+        _opt(dev, "num_accepted", num_accepted, i32, (B,)), _opt(dev, "weighted_lens", weighted_lens, i32, (B,)),
+        decay, _need(dev, "weights", weights, f32, (desc.num_pages, desc.H_kv, desc.page_size)), _stream(stream)))
+
+
+def evict(desc: Desc, budget, cache_seqlens, block_table, dst_block_table, k_pool, v_pool, weights, kept, new_seqlens,
+          keep_first=0, keep_last=0, device_error=None, stream=None, lib=None):
+    """Cut every request's cache to ``budget`` tokens per KV head (the first
+    ``keep_first``, the last ``keep_last`` and the heaviest between them by
+    ``weights``), copied in their order to the pages of ``dst_block_table``;
+    ``kept`` int32 [B, H_kv, budget] gets their positions, ``new_seqlens`` the
+    lengths. See decode_attn_evict in the header."""
+    import torch
+    i32, dev, B = torch.int32, _device(), desc.B
+    table = (B, desc.max_pages_per_seq)
+    _check((lib or load_library()).decode_attn_evict(
+        ctypes.byref(desc), budget, keep_first, keep_last, _need(dev, "cache_seqlens", cache_seqlens, i32, (B,)),
+        _need(dev, "block_table", block_table, i32, table), _need(dev, "dst_block_table", dst_block_table, i32, table),
+        _pool(dev, "k_pool", k_pool, desc), None if v_pool is None else _pool(dev, "v_pool", v_pool, desc),
+        _need(dev, "weights", weights, torch.float32, (desc.num_pages, desc.H_kv, desc.page_size)),
+        _need(dev, "kept", kept, i32, (B, desc.H_kv, budget)), _need(dev, "new_seqlens", new_seqlens, i32, (B,)),
+        _opt(dev, "device_error", device_error, i32), _stream(stream)))
+
+
+def _prob_rows(dev, name, t, dtype, shape):
+    """Probabilities [B, rows, V], the rows evenly spaced; their address and the distance between rows."""
+    B, rows, V = shape
+    if not (t.dtype is dtype and t.get_device() == dev and t.shape == shape and (V == 1 or t.stride(2) == 1)
+            and (B == 1 or rows == 1 or t.stride(0) == rows * t.stride(1))):
+        raise DecodeAttnError(f"{name}: want a {dtype} tensor of shape {shape} with evenly spaced rows on the current "
+                              f"CUDA device, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+    return t.data_ptr(), (t.stride(1) if rows > 1 else t.stride(0) if B > 1 else V)
+
+
+def verify_drafts(target_probs, draft_probs, draft_tokens, uniform, num_accepted, out_tokens, cache_seqlens=None,
+                  new_seqlens=None, device_error=None, stream=None, lib=None):
+    """Accept or refuse the drafts of every request and draw its next token:
+    ``target_probs`` [B, K + 1, V], ``draft_probs`` [B, K, V] of the same dtype
+    (None: certain drafts), ``draft_tokens`` int32 [B, K] (None for K = 0),
+    ``uniform`` fp32 [B, K + 1]; ``num_accepted`` int32 [B], ``out_tokens`` int32
+    [B, K + 1] and, with ``cache_seqlens``, ``new_seqlens`` int32 [B] are written.
+    See decode_attn_verify_drafts in the header."""
+    import torch
+    i32, dev, dtype = torch.int32, _device(), target_probs.dtype
+    if target_probs.dim() != 3 or target_probs.shape[1] < 1:
+        raise DecodeAttnError(f"target_probs: want [B, K + 1, V], got {tuple(target_probs.shape)}")
+    B, rows, V = target_probs.shape
+    K = rows - 1
+    kind = {torch.float32: PROB_F32, torch.bfloat16: PROB_BF16, torch.float16: PROB_F16}.get(dtype, -1)
+    tp, ts = _prob_rows(dev, "target_probs", target_probs, dtype, (B, rows, V))
+    dp, ds = (None, 0) if draft_probs is None else _prob_rows(dev, "draft_probs", draft_probs, dtype, (B, K, V))
+    _check((lib or load_library()).decode_attn_verify_drafts(
+        B, K, V, kind, tp, ts, dp, ds, _opt(dev, "draft_tokens", draft_tokens, i32, (B, K)),
+        _need(dev, "uniform", uniform, torch.float32, (B, rows)), _opt(dev, "cache_seqlens", cache_seqlens, i32, (B,)),
+        _need(dev, "num_accepted", num_accepted, i32, (B,)), _need(dev, "out_tokens", out_tokens, i32, (B, rows)),
+        _opt(dev, "new_seqlens", new_seqlens, i32, (B,)), _opt(dev, "device_error", device_error, i32),
+        _stream(stream)))
+
+
 def get_error(meta, stream=None) -> int:
     e = ctypes.c_int32(0)
     _check(load_library().decode_attn_get_error(_ptr(meta), ctypes.byref(e), _stream(stream)))
@@ -196,4 +369,6 @@ def get_error(meta, stream=None) -> int:
 
 
 __all__ = ["Desc", "LaunchOpts", "DecodeAttnError", "load_library", "strerror", "sched_meta_bytes",
-           "meta_offsets", "num_parts", "sched_meta", "fwd", "fwd_static_scratch", "append_kv", "get_error", "KV_BF16", "KV_FP8", "KV_MLA656"]
+           "meta_offsets", "num_parts", "sched_meta", "fwd", "fwd_static_scratch", "append_kv", "rope_append",
+           "accum_weights", "evict", "verify_drafts", "get_error", "Rope", "KV_BF16", "KV_FP8", "KV_MLA656", "PROB_F32",
+           "PROB_BF16", "PROB_F16"]

@@ -17,6 +17,10 @@ cudaError_t launch_gqa(int D, bool fp8, const CUtensorMap &tkv, const CUtensorMa
 cudaError_t launch_mla(const MlaParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_combine(int DV, const CombineParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_append(int kv_dtype, const AppendParams &p, cudaStream_t stream, bool pdl);
+cudaError_t launch_rope(int kv_dtype, RopeParams p, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_accum(int D, bool fp8, const AccumParams &p, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_verify(int prob_dtype, const VerifyParams &p, int num_sms, cudaStream_t stream, bool pdl);
 int mla_ctas_per_part(int s_q);
 bool mla_kernel_available();
 int mla_max_parts(int s_q);
@@ -98,6 +102,54 @@ int resolve_sms(const da_desc *d, int *nsm) {
         *nsm *= gqa_ctas_per_sm(d->D_qk, d->kv_dtype == DA_KV_FP8_PER_TENSOR, sq_of(d));
     }
     return DA_OK;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// SMs of the current device (0: the query failed)
+int current_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return n;
+}
+
+// log2 of a page size that is a power of two, else -1
+int log2_of(int v) {
+    for (int k = 0; k < 31; ++k)
+        if (v == (1 << k)) return k;
+    return -1;
+}
+
+// The sizes of a pool and its block table, for the calls that write K and V:
+// DA_OK, and the bf16 values of a token's new K row.
+int check_pool_desc(const da_desc *d, int64_t *row_len) {
+    if (d->B < 1 || d->B > (1 << 24) || d->H_kv < 1 || d->H_kv > 4096 || d->page_size < 1 ||
+        d->max_pages_per_seq < 1 || d->num_pages < 1 || d->D_qk < 1 || d->D_v < 1 || d->D_qk > 4096 ||
+        d->D_v > 4096)
+        return DA_ERR_DIMS;
+    if ((int64_t)d->max_pages_per_seq * d->page_size > (int64_t)INT32_MAX) return DA_ERR_DIMS;
+    if ((int64_t)d->B * d->max_pages_per_seq > (int64_t)INT32_MAX) return DA_ERR_DIMS;
+    switch (d->kv_dtype) {
+        case DA_KV_BF16:
+        case DA_KV_FP8_PER_TENSOR:
+            if (d->D_qk != d->D_v || (d->D_qk % 8) != 0) return DA_ERR_UNSUPPORTED;
+            *row_len = (int64_t)d->H_kv * d->D_qk;
+            return DA_OK;
+        case DA_KV_FP8_MLA656:
+            if (d->H_kv != 1 || d->D_qk != 576 || d->D_v != 512) return DA_ERR_UNSUPPORTED;
+            *row_len = 576;
+            return DA_OK;
+        default:
+            return DA_ERR_UNSUPPORTED;
+    }
+}
+
+// A row stride in bf16 elements: 0 stands for packed rows
+int check_stride(int64_t *stride, int64_t row_len) {
+    if (*stride == 0) *stride = row_len;
+    return (*stride < row_len || (*stride % 8) != 0 || *stride > ((int64_t)1 << 40)) ? DA_ERR_DIMS : DA_OK;
 }
 
 // Page-trace test build: where the kernels record the pool rows they read,
@@ -432,9 +484,7 @@ int decode_attn_fwd_ex(const da_desc *desc, const void *q, const void *k_pool, c
         p.topk = desc->topk;
         p.s_q = sq_of(desc);
         p.debug_stall = g_debug_stall;
-        p.log2_page = -1;
-        for (int k = 0; k < 31; ++k)
-            if (desc->page_size == (1 << k)) p.log2_page = k;
+        p.log2_page = log2_of(desc->page_size);
         if (ev_begin && cudaEventRecord(ev_begin, stream) != cudaSuccess) return DA_ERR_CUDA;
         if (launch_mla(p, stream, pdl) != cudaSuccess) return DA_ERR_CUDA;
     }
@@ -472,30 +522,11 @@ int decode_attn_append_kv(const da_desc *desc, const void *k_new, const void *v_
                           const float *k_scale, const float *v_scale, int32_t *device_error, cudaStream_t stream) {
     if (!desc) return DA_ERR_NULL;
     const da_desc *d = desc;
-    if (d->B < 1 || d->B > (1 << 24) || d->H_kv < 1 || d->H_kv > 4096 || d->page_size < 1 ||
-        d->max_pages_per_seq < 1 || d->num_pages < 1 || d->D_qk < 1 || d->D_v < 1 || d->D_qk > 4096 ||
-        d->D_v > 4096)
-        return DA_ERR_DIMS;
-    if ((int64_t)d->max_pages_per_seq * d->page_size > (int64_t)INT32_MAX) return DA_ERR_DIMS;
-    if ((int64_t)d->B * d->max_pages_per_seq > (int64_t)INT32_MAX) return DA_ERR_DIMS;
-    const bool mla = is_mla(d);
     int64_t row_len = 0;  // bf16 values of one request's new K (or V) row
-    switch (d->kv_dtype) {
-        case DA_KV_BF16:
-        case DA_KV_FP8_PER_TENSOR:
-            if (d->D_qk != d->D_v || (d->D_qk % 8) != 0) return DA_ERR_UNSUPPORTED;
-            row_len = (int64_t)d->H_kv * d->D_qk;
-            break;
-        case DA_KV_FP8_MLA656:
-            if (d->H_kv != 1 || d->D_qk != 576 || d->D_v != 512) return DA_ERR_UNSUPPORTED;
-            row_len = 576;
-            break;
-        default:
-            return DA_ERR_UNSUPPORTED;
-    }
-    if (new_row_stride == 0) new_row_stride = row_len;
-    if (new_row_stride < row_len || (new_row_stride % 8) != 0 || new_row_stride > ((int64_t)1 << 40))
-        return DA_ERR_DIMS;
+    int rc = check_pool_desc(d, &row_len);
+    if (rc) return rc;
+    const bool mla = is_mla(d);
+    if ((rc = check_stride(&new_row_stride, row_len))) return rc;
     if (!k_new || !positions || !block_table || !k_pool) return DA_ERR_NULL;
     if (mla) {
         if (v_new) return DA_ERR_UNSUPPORTED;
@@ -530,6 +561,238 @@ int decode_attn_append_kv(const da_desc *desc, const void *k_new, const void *v_
     p.max_pages = d->max_pages_per_seq;
     p.num_pages = d->num_pages;
     if (launch_append(d->kv_dtype, p, stream, true) != cudaSuccess) return DA_ERR_CUDA;
+    return DA_OK;
+}
+
+int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_tokens, const void *q,
+                            int64_t q_stride, const void *k_new, int64_t k_stride, const void *v_new,
+                            int64_t v_stride, const float *inv_freq, const int32_t *rope_positions,
+                            const int32_t *requests, const int32_t *positions, const int32_t *block_table,
+                            void *q_out, void *k_pool, void *v_pool, const float *k_scale, const float *v_scale,
+                            int32_t *device_error, cudaStream_t stream) {
+    if (!desc || !rope) return DA_ERR_NULL;
+    int64_t row_len = 0;
+    int rc = check_pool_desc(desc, &row_len);
+    if (rc) return rc;
+    const bool mla = is_mla(desc);
+    if (desc->G < 1 || desc->G > 1024 || n_tokens < 0 || desc->s_q < 0 || desc->s_q > 64) return DA_ERR_DIMS;
+    const int64_t H_q = (int64_t)desc->H_kv * desc->G, q_len = H_q * desc->D_qk;
+    if (rope->rot_dim < 16 || rope->rot_dim % 16 != 0 || rope->rot_dim > 512 || rope->rot_dim > (mla ? 64 : desc->D_qk) ||
+        rope->n_axes < 1 || rope->n_axes > 4)
+        return DA_ERR_DIMS;
+    int64_t pairs = 0;
+    for (int a = 0; a < 4; ++a) {
+        if (rope->sections[a] < 0 || (a >= rope->n_axes && rope->sections[a] != 0)) return DA_ERR_DIMS;
+        pairs += rope->sections[a];
+    }
+    if (pairs != rope->rot_dim / 2) return DA_ERR_DIMS;
+    if (!requests && n_tokens != (int64_t)desc->B * sq_of(desc)) return DA_ERR_DIMS;
+    if ((rc = check_stride(&q_stride, q_len)) || (rc = check_stride(&k_stride, row_len))) return rc;
+    if (!mla && (rc = check_stride(&v_stride, row_len))) return rc;
+    if (n_tokens == 0) return DA_OK;
+    if (!q || !k_new || !inv_freq || !rope_positions || !positions || !block_table || !q_out || !k_pool)
+        return DA_ERR_NULL;
+    if (mla) {
+        if (v_new || (v_pool && v_pool != k_pool)) return DA_ERR_UNSUPPORTED;
+    } else if (!v_new || !v_pool) {
+        return DA_ERR_NULL;
+    }
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q_out) || !aligned16(k_pool) ||
+        !aligned16(v_pool) || !aligned4(inv_freq) || !aligned4(rope_positions) || !aligned4(requests) ||
+        !aligned4(positions) || !aligned4(block_table) || !aligned4(device_error))
+        return DA_ERR_ALIGN;
+    if (desc->kv_dtype == DA_KV_FP8_PER_TENSOR) {
+        if (!k_scale || !v_scale) return DA_ERR_SCALE;
+        if (!aligned4(k_scale) || !aligned4(v_scale)) return DA_ERR_ALIGN;
+    }
+    // q_out is q, row for row, or does not touch it
+    const bool in_place = q == q_out && q_stride == q_len;
+    if (!in_place) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(q), b = reinterpret_cast<uintptr_t>(q_out);
+        const uint64_t a_len = 2ull * ((uint64_t)(n_tokens - 1) * q_stride + q_len), b_len = 2ull * n_tokens * q_len;
+        // byte ranges from the first row's start to the last row's end
+        if (a < b + b_len && b < a + a_len) return DA_ERR_UNSUPPORTED;
+    }
+    const int sms = current_sms();
+    if (!sms) return DA_ERR_CUDA;
+    RopeParams p = {};
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(k_new);
+    p.v = static_cast<const uint16_t *>(v_new);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.inv_freq = inv_freq;
+    p.rope_pos = rope_positions;
+    p.requests = requests;
+    p.positions = positions;
+    p.block_table = block_table;
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.k_pool = static_cast<uint8_t *>(k_pool);
+    p.v_pool = static_cast<uint8_t *>(mla ? k_pool : v_pool);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.error = device_error;
+    p.N = n_tokens;
+    p.B = desc->B;
+    p.H_q = (int32_t)H_q;
+    p.H_kv = desc->H_kv;
+    p.D = desc->D_qk;
+    p.s_q = sq_of(desc);
+    p.page_size = desc->page_size;
+    p.max_pages = desc->max_pages_per_seq;
+    p.num_pages = desc->num_pages;
+    p.rot = rope->rot_dim;
+    for (int a = 0; a < 4; ++a) p.sections[a] = rope->sections[a];
+    p.n_axes = rope->n_axes;
+    p.interleaved = rope->interleaved != 0;
+    p.adjacent = rope->adjacent != 0;
+    p.in_place = in_place;
+    if (launch_rope(desc->kv_dtype, p, sms, stream, true) != cudaSuccess) return DA_ERR_CUDA;
+    return DA_OK;
+}
+
+int decode_attn_accum_weights(const da_desc *desc, const void *q, const void *k_pool, const float *k_scale,
+                              const int32_t *block_table, const int32_t *cache_seqlens, void *sched_meta,
+                              size_t sched_meta_bytes, const float *lse, const int32_t *num_accepted,
+                              const int32_t *weighted_lens, float decay, float *weights, cudaStream_t stream) {
+    MetaLayout L;
+    const int rc = make_layout(desc, &L);
+    if (rc) return rc;
+    if (is_mla(desc) || desc->window != 0 || desc->topk != 0) return DA_ERR_UNSUPPORTED;
+    if (!(decay >= 0.f) || std::isinf(decay)) return DA_ERR_DIMS;
+    const bool fp8 = desc->kv_dtype == DA_KV_FP8_PER_TENSOR;
+    if (!q || !k_pool || !block_table || !cache_seqlens || !sched_meta || !lse || !weights) return DA_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k_pool) || !aligned16(block_table) || !aligned16(cache_seqlens) ||
+        !aligned16(sched_meta) || !aligned16(lse) || !aligned16(weights) || !aligned4(num_accepted) ||
+        !aligned4(weighted_lens))
+        return DA_ERR_ALIGN;
+    if (fp8 && !k_scale) return DA_ERR_SCALE;
+    if (!aligned4(k_scale)) return DA_ERR_ALIGN;
+    if (sched_meta_bytes < L.total) return DA_ERR_META_SIZE;
+    if ((int64_t)desc->page_size * desc->num_pages > (int64_t)INT32_MAX) return DA_ERR_DIMS;
+    const int sms = current_sms();
+    if (!sms) return DA_ERR_CUDA;
+    AccumParams p = {};
+    p.q = q;
+    p.k_pool = static_cast<const uint8_t *>(k_pool);
+    p.k_scale = k_scale;
+    p.block_table = block_table;
+    p.seqlens = cache_seqlens;
+    p.meta = meta_view(sched_meta, L);
+    p.lse = lse;
+    p.accepted = num_accepted;
+    p.weighted = weighted_lens;
+    p.weights = weights;
+    p.decay = decay;
+    p.scale_log2 = (desc->softmax_scale > 0.f ? desc->softmax_scale : 1.0f / std::sqrt((float)desc->D_qk)) * kLog2eF;
+    p.B = desc->B;
+    p.H_kv = desc->H_kv;
+    p.G = desc->G;
+    p.H_q = desc->H_kv * desc->G;
+    p.s_q = sq_of(desc);
+    p.page_size = desc->page_size;
+    p.log2_page = log2_of(desc->page_size);
+    p.max_pages = desc->max_pages_per_seq;
+    p.num_pages = desc->num_pages;
+    p.splits = desc->splits;
+    p.num_parts = L.num_parts;
+    if (launch_accum(desc->D_qk, fp8, p, sms, stream, true) != cudaSuccess) return DA_ERR_CUDA;
+    return DA_OK;
+}
+
+int decode_attn_evict(const da_desc *desc, int32_t budget, int32_t keep_first, int32_t keep_last,
+                      const int32_t *cache_seqlens, const int32_t *block_table, const int32_t *dst_block_table,
+                      void *k_pool, void *v_pool, float *weights, int32_t *kept, int32_t *new_seqlens,
+                      int32_t *device_error, cudaStream_t stream) {
+    if (!desc) return DA_ERR_NULL;
+    int64_t row_len = 0;
+    const int rc = check_pool_desc(desc, &row_len);
+    if (rc) return rc;
+    const bool mla = is_mla(desc);
+    const int64_t row_bytes = mla ? 656 : (int64_t)desc->D_qk * (desc->kv_dtype == DA_KV_BF16 ? 2 : 1);
+    if (row_bytes % 16 != 0) return DA_ERR_UNSUPPORTED;
+    if (budget < 1 || budget > (int64_t)desc->max_pages_per_seq * desc->page_size || keep_first < 0 || keep_last < 0 ||
+        (int64_t)keep_first + keep_last > budget)
+        return DA_ERR_DIMS;
+    // rows of the selection, and tiles of the copy (at least one token each), index the grids
+    if ((int64_t)desc->B * desc->H_kv > (INT32_MAX >> 3) || (int64_t)desc->B * budget > (int64_t)INT32_MAX)
+        return DA_ERR_DIMS;
+    if (!cache_seqlens || !block_table || !dst_block_table || !k_pool || !weights || !kept || !new_seqlens)
+        return DA_ERR_NULL;
+    if (mla) {
+        if (v_pool && v_pool != k_pool) return DA_ERR_UNSUPPORTED;
+    } else if (!v_pool) {
+        return DA_ERR_NULL;
+    }
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned4(cache_seqlens) || !aligned4(block_table) ||
+        !aligned4(dst_block_table) || !aligned4(weights) || !aligned4(kept) || !aligned4(new_seqlens) ||
+        !aligned4(device_error))
+        return DA_ERR_ALIGN;
+    if (new_seqlens == cache_seqlens || block_table == dst_block_table) return DA_ERR_UNSUPPORTED;
+    const int sms = current_sms();
+    if (!sms) return DA_ERR_CUDA;
+    EvictParams p = {};
+    p.seqlens = cache_seqlens;
+    p.src_table = block_table;
+    p.dst_table = dst_block_table;
+    p.k_pool = static_cast<uint8_t *>(k_pool);
+    p.v_pool = mla ? nullptr : static_cast<uint8_t *>(v_pool);
+    p.weights = weights;
+    p.kept = kept;
+    p.new_seqlens = new_seqlens;
+    p.error = device_error;
+    p.B = desc->B;
+    p.H_kv = desc->H_kv;
+    p.page_size = desc->page_size;
+    p.log2_page = log2_of(desc->page_size);
+    p.max_pages = desc->max_pages_per_seq;
+    p.num_pages = desc->num_pages;
+    p.row_bytes = (int32_t)row_bytes;
+    p.budget = budget;
+    p.first = keep_first;
+    p.last = keep_last;
+    if (launch_evict(p, sms, stream, true) != cudaSuccess) return DA_ERR_CUDA;
+    return DA_OK;
+}
+
+int decode_attn_verify_drafts(int32_t B, int32_t n_draft, int32_t vocab, int32_t prob_dtype,
+                              const void *target_probs, int64_t target_stride, const void *draft_probs,
+                              int64_t draft_stride, const int32_t *draft_tokens, const float *uniform,
+                              const int32_t *cache_seqlens, int32_t *num_accepted, int32_t *out_tokens,
+                              int32_t *new_seqlens, int32_t *device_error, cudaStream_t stream) {
+    if (B < 1 || B > (1 << 20) || n_draft < 0 || n_draft > 63 || vocab < 1 || vocab > (1 << 20)) return DA_ERR_DIMS;
+    if (prob_dtype < DA_PROB_F32 || prob_dtype > DA_PROB_F16) return DA_ERR_UNSUPPORTED;
+    if (target_stride == 0) target_stride = vocab;
+    if (draft_stride == 0) draft_stride = vocab;
+    if (target_stride < vocab || draft_stride < vocab || target_stride > ((int64_t)1 << 34) ||
+        draft_stride > ((int64_t)1 << 34))
+        return DA_ERR_DIMS;
+    if (!target_probs || !uniform || !num_accepted || !out_tokens || (n_draft > 0 && !draft_tokens)) return DA_ERR_NULL;
+    if ((cache_seqlens == nullptr) != (new_seqlens == nullptr)) return DA_ERR_NULL;
+    const uintptr_t es = prob_dtype == DA_PROB_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(target_probs) % es || reinterpret_cast<uintptr_t>(draft_probs) % es ||
+        !aligned4(draft_tokens) || !aligned4(uniform) || !aligned4(cache_seqlens) || !aligned4(num_accepted) ||
+        !aligned4(out_tokens) || !aligned4(new_seqlens) || !aligned4(device_error))
+        return DA_ERR_ALIGN;
+    const int sms = current_sms();
+    if (!sms) return DA_ERR_CUDA;
+    VerifyParams p = {};
+    p.target = target_probs;
+    p.draft = n_draft > 0 ? draft_probs : nullptr;
+    p.target_stride = target_stride;
+    p.draft_stride = draft_stride;
+    p.tokens = draft_tokens;
+    p.uniform = uniform;
+    p.seqlens = cache_seqlens;
+    p.accepted = num_accepted;
+    p.out = out_tokens;
+    p.new_seqlens = new_seqlens;
+    p.error = device_error;
+    p.B = B;
+    p.K = n_draft;
+    p.V = vocab;
+    if (launch_verify(prob_dtype, p, sms, stream, true) != cudaSuccess) return DA_ERR_CUDA;
     return DA_OK;
 }
 

@@ -158,4 +158,73 @@ struct AppendParams {
     int32_t B, H_kv, D, page_size, max_pages, num_pages;
 };
 
+// Rotary positions + append (rope.cu).
+struct RopeParams {
+    const uint16_t *q, *k, *v;     // bf16 rows, token n at + n * stride
+    int64_t q_stride, k_stride, v_stride;
+    const float *inv_freq;         // [rot / 2]
+    const int32_t *rope_pos;       // [n_axes][N]
+    const int32_t *requests;       // [N] or null: n / s_q
+    const int32_t *positions;      // [N] slot in the request; < 0: token skipped
+    const int32_t *block_table;    // [B][max_pages]
+    uint16_t *q_out;               // bf16 [N][H_q][D]
+    uint8_t *k_pool, *v_pool;
+    const float *k_scale, *v_scale;
+    int32_t *error;
+    int32_t N, B, H_q, H_kv, D, s_q, page_size, max_pages, num_pages;
+    int32_t rot;                   // rotated values per head, a multiple of 16
+    int32_t sections[4];           // pairs per axis
+    int32_t n_axes, interleaved, adjacent;
+    int32_t in_place;              // q_out is q: values that are not rotated stay where they are
+    int32_t items;                 // 16-value items per head
+    int32_t heads;                 // head slots per token: q heads, then K and V heads (not for the 656-byte token)
+    int32_t tokens;                // tokens a block works on at a time
+    int32_t q_blocks;              // 656-byte token: blocks before this one rotate q, the others write tokens
+};
+
+// Attention weight gathered by cached tokens (accum.cu).
+struct AccumParams {
+    const void *q;                 // bf16 [B][s_q][H_q][D]
+    const uint8_t *k_pool;
+    const float *k_scale;          // [H_kv], e4m3 pools only
+    const int32_t *block_table;
+    const int32_t *seqlens;
+    MetaView meta;
+    const float *lse;              // [B][s_q][H_q]
+    const int32_t *accepted;       // [B] or null: query tokens 0..accepted[b] count
+    const int32_t *weighted;       // [B] or null: tokens whose weight is valid (the others start from 0)
+    float *weights;                // [num_pages][H_kv][page_size]
+    float decay, scale_log2;
+    int32_t B, H_kv, G, H_q, s_q, page_size, log2_page, max_pages, num_pages, splits, num_parts;
+};
+
+// Eviction by weight (evict.cu).
+struct EvictParams {
+    const int32_t *seqlens;        // [B]
+    const int32_t *src_table, *dst_table;  // [B][max_pages]
+    uint8_t *k_pool, *v_pool;      // v_pool null: one pool (656-byte token)
+    float *weights;                // [num_pages][H_kv][page_size]
+    int32_t *kept;                 // [B][H_kv][budget]
+    int32_t *new_seqlens;          // [B]
+    int32_t *error;                // may be null
+    int32_t B, H_kv, page_size, log2_page, max_pages, num_pages;
+    int32_t row_bytes;             // of one token and head, a multiple of 16
+    int32_t budget, first, last;
+};
+
+// Verification of drafted tokens (verify.cu).
+struct VerifyParams {
+    const void *target;            // [B][K + 1] rows of V probabilities
+    const void *draft;             // [B][K] rows, or null: the drafts are certain
+    int64_t target_stride, draft_stride;  // elements between consecutive rows
+    const int32_t *tokens;         // [B][K]
+    const float *uniform;          // [B][K + 1]
+    const int32_t *seqlens;        // [B] or null
+    int32_t *accepted;             // [B]
+    int32_t *out;                  // [B][K + 1]
+    int32_t *new_seqlens;          // [B] or null
+    int32_t *error;                // may be null
+    int32_t B, K, V;
+};
+
 }  // namespace da

@@ -1,0 +1,345 @@
+// Rotary positions with several axes, fused with the KV append.
+//
+// Pair i of the rotated values of a head turns by the angle
+//     theta = pos[axis(i)][n] * inv_freq[i],
+//     (x, y) -> (x cos theta - y sin theta, x sin theta + y cos theta),
+// where a token has one position per axis (time, height, width) and axis(i)
+// comes from the sections: in blocks (the first sections[0] pairs follow axis
+// 0, the next sections[1] axis 1, ...) or alternating. q goes rotated to
+// q_out, K rotated and V as it is into the page slot of the token, in the
+// pool's format (bf16, e4m3 with one scale per head, the 656-byte token, whose
+// last 64 values are the rotated ones). Products and sums are fp32, each value
+// is rounded once.
+//
+// The angle: positions reach far beyond what an fp32 product keeps of an angle
+// (position 10^6 has an ulp of 0.06 rad), so the phase is kept in turns as a
+// 64-bit fraction, F = inv_freq / (2 pi) mod 1 in units of 2^-64 from the fp32
+// bits of inv_freq, and pos * F wraps modulo one turn in integer arithmetic:
+// the phase error is below |pos| * 2^-63 turns. The top 32 bits, as a signed
+// fraction of half a turn, go to sincospif.
+//
+// Bound by HBM: every value is read and written once. Work item = 16 values of
+// a head (two 16-byte vectors, the two halves of eight pairs); a thread keeps
+// the same place in a head and walks over the heads of a token, so cos and sin
+// of its eight pairs are read from shared memory, where each angle is computed
+// once per token.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "decode_attn.h"
+#include "layout.h"
+#include "quant.cuh"
+
+namespace da {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 8;  // tokens a block works on at a time
+
+// inv_freq / (2 pi) mod 1, in units of 2^-64, from the fp32 bits: mantissa
+// (24 bits) times floor(2^64 / (2 pi)), shifted by the exponent. Finite input.
+__device__ __forceinline__ uint64_t turns_of(float f) {
+    constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull;  // floor(2^64 / (2 pi))
+    const uint32_t u = __float_as_uint(f);
+    const int ex = (int)((u >> 23) & 255u);
+    const uint64_t m = (u & 0x7FFFFFu) | (ex ? 0x800000u : 0u);
+    const int e = (ex ? ex : 1) - 150;  // f = m 2^e
+    const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+    uint64_t r = 0;
+    if (e >= 0) {
+        if (e < 64) r = lo << e;
+    } else if (e > -64) {
+        r = (lo >> -e) | (hi << (64 + e));
+    } else if (e > -128) {
+        r = hi >> (-e - 64);
+    }
+    return (u >> 31) ? 0ull - r : r;
+}
+
+// cos and sin of pos * F turns
+__device__ __forceinline__ float2 cos_sin(int32_t pos, uint64_t F, bool finite) {
+    const uint64_t phase = (uint64_t)(int64_t)pos * F;
+    const float half_turns = (float)(int32_t)(phase >> 32) * 0x1p-31f;
+    float s, c;
+    sincospif(half_turns, &s, &c);
+    return finite ? make_float2(c, s) : make_float2(NAN, NAN);
+}
+
+__device__ __forceinline__ int axis_of(const RopeParams &p, int i) {
+    if (p.interleaved) {
+        const int a = i % p.n_axes;
+        return i / p.n_axes < p.sections[a] ? a : 0;
+    }
+    int a = 0, end = p.sections[0];
+    while (a + 1 < p.n_axes && i >= end) end += p.sections[++a];
+    return a;
+}
+
+constexpr int64_t kSkip = -2;    // negative position: the token is skipped
+constexpr int64_t kNowhere = -1;  // invalid request, position or page: no K / V row is written
+
+// Pool slot of token n (page * page_size + slot), or one of the above.
+__device__ __forceinline__ int64_t slot_of(const RopeParams &p, int n, bool reporter) {
+    const int t = __ldg(p.positions + n);
+    if (t < 0) return kSkip;
+    const int b = p.requests ? __ldg(p.requests + n) : n / p.s_q;
+    if (b < 0 || b >= p.B) {
+        if (reporter && p.error) atomicOr(p.error, DA_DEV_BAD_REQUEST);
+        return kNowhere;
+    }
+    if ((int64_t)t >= (int64_t)p.max_pages * p.page_size) {
+        if (reporter && p.error) atomicOr(p.error, DA_DEV_SEQ_TOO_LONG);
+        return kNowhere;
+    }
+    const int page = __ldg(p.block_table + (int64_t)b * p.max_pages + t / p.page_size);
+    if (page < 0 || page >= p.num_pages) {
+        if (reporter && p.error) atomicOr(p.error, DA_DEV_BAD_PAGE);
+        return kNowhere;
+    }
+    return (int64_t)page * p.page_size + t % p.page_size;
+}
+
+// 16-byte load of q, K or V rows: plain (q may be rotated in place)
+__device__ __forceinline__ uint4 ld_row(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void unpack8(uint4 x, float *v) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float *v) {
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
+// Rotates the eight pairs of an item; cs: their (cos, sin).
+template <bool kAdjacent>
+__device__ __forceinline__ void rotate16(float (&x)[16], const float2 *cs) {
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+        const float4 c2 = *reinterpret_cast<const float4 *>(cs + k);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float c = u ? c2.z : c2.x, s = u ? c2.w : c2.y;
+            const int i = kAdjacent ? 2 * (k + u) : k + u, j = kAdjacent ? i + 1 : i + 8;
+            const float a = x[i], b = x[j];
+            x[i] = a * c - b * s;
+            x[j] = a * s + b * c;
+        }
+    }
+}
+
+// One token's latent row, by one warp: NoPE quantised as the append does, the
+// RoPE part rotated, lane l its pair l (or the two values that pass through).
+template <bool kAdjacent>
+__device__ __forceinline__ void latent_token(const RopeParams &p, int n, int lane, uint64_t F, bool finite, int axis) {
+    const uint16_t *src = p.k + (int64_t)n * p.k_stride;
+    LatentIn x;
+    x.a0 = ld_stream_v4(src + lane * 16);
+    x.a1 = ld_stream_v4(src + lane * 16 + 8);
+    const int half = p.rot / 2;
+    const bool turn = lane < half;
+    const int i = kAdjacent || !turn ? 2 * lane : lane, j = kAdjacent || !turn ? i + 1 : lane + half;
+    const float a = __uint_as_float((uint32_t)__ldg(src + kLatentNope + i) << 16);
+    const float b = __uint_as_float((uint32_t)__ldg(src + kLatentNope + j) << 16);
+    const float2 cs = turn ? cos_sin(__ldg(p.rope_pos + (int64_t)axis * p.N + n), F, finite) : make_float2(1.f, 0.f);
+    const int64_t slot = slot_of(p, n, lane == 0);  // uniform over the warp
+    if (slot < 0) return;
+    uint8_t *row = p.k_pool + slot * kLatentRow;
+    latent_store_nope(row, lane, x);
+    uint16_t *out = reinterpret_cast<uint16_t *>(row + kLatentRope);
+    const uint32_t ab = turn ? pack_bf16(a * cs.x - b * cs.y, a * cs.y + b * cs.x)
+                             : (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xFFFF0000u);
+    if (kAdjacent || !turn) {
+        *reinterpret_cast<uint32_t *>(out + i) = ab;
+    } else {
+        out[i] = (uint16_t)(ab & 0xFFFFu);
+        out[j] = (uint16_t)(ab >> 16);
+    }
+}
+
+template <int kKv, bool kAdjacent>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+    extern __shared__ float4 smem[];
+    __shared__ int64_t s_slot[2][kMaxTokens];
+    constexpr bool kLatent = kKv == DA_KV_FP8_MLA656;
+    const int tid = threadIdx.x, pairs = p.rot / 2;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    if (kLatent && (int)blockIdx.x >= p.q_blocks) {
+        const int lane = tid & 31;
+        const bool turn = lane < pairs;
+        const float f = turn ? __ldg(p.inv_freq + lane) : 0.f;
+        const bool finite = fabsf(f) < INFINITY;
+        const uint64_t F = finite ? turns_of(f) : 0;
+        const int axis = turn ? axis_of(p, lane) : 0;
+        const int64_t step = (int64_t)(gridDim.x - p.q_blocks) * (kThreads / 32);
+        for (int64_t n = (int64_t)(blockIdx.x - p.q_blocks) * (kThreads / 32) + (tid >> 5); n < p.N; n += step)
+            latent_token<kAdjacent>(p, (int)n, lane, F, finite, axis);
+        return;
+    }
+
+    // angles: thread (ta, ia) computes pair ia of tokens ta, ta + at, ...
+    const int at = kThreads / pairs, ta = tid / pairs, ia = tid - ta * pairs;
+    uint64_t F = 0;
+    bool finite = true;
+    const int32_t *apos = p.rope_pos;
+    if (ta < at) {
+        const float f = __ldg(p.inv_freq + ia);
+        finite = fabsf(f) < INFINITY;
+        F = finite ? turns_of(f) : 0;
+        apos += (int64_t)axis_of(p, ia) * p.N;
+    }
+    // items: thread (head slot, j) holds 16-value item j of a head
+    const int per_pass = kThreads / p.items, hs = tid / p.items, j = tid - hs * p.items;
+    const int ts = p.tokens > 1 ? hs / p.heads : 0, h_first = hs - ts * p.heads;
+    const bool mine = hs < per_pass && ts < p.tokens;
+    const int h_step = p.tokens > 1 ? p.heads : per_pass;
+    const int turned = p.rot / 16;                     // items j < turned are rotated (q and K)
+    const int base = kLatent && j < turned ? kLatentNope : 0;
+    const int jo = kLatent && j >= turned ? j - turned : j;   // copied items: their place in the head
+    const bool in_rot = j < turned;
+    const int r0 = in_rot && !kAdjacent ? 8 * j : 16 * jo;    // the item's two vectors in q and K heads
+    const int r1 = in_rot && !kAdjacent ? pairs + 8 * j : 16 * jo + 8;
+    const bool has1 = in_rot || 16 * jo + 8 < p.D;            // D = 8 mod 16: the last item has one vector
+    const int hq = p.H_q, hk = kLatent ? 0 : p.H_kv;
+
+    const int tiles = (p.N + p.tokens - 1) / p.tokens;
+    const int blocks = kLatent ? p.q_blocks : gridDim.x;
+    int buf = 0;
+    for (int tile = blockIdx.x; tile < tiles; tile += blocks, buf ^= 1) {
+        const int n0 = tile * p.tokens, nt = min(p.tokens, p.N - n0);
+        const int n = n0 + ts;
+        const bool work = mine && ts < nt;
+        // the source of this thread's item of head h
+        auto src_of = [&](int h) -> const uint16_t * {
+            if (h < hq) return p.q + (int64_t)n * p.q_stride + (int64_t)h * p.D + base;
+            if (h < hq + hk) return p.k + (int64_t)n * p.k_stride + (int64_t)(h - hq) * p.D;
+            return p.v + (int64_t)n * p.v_stride + (int64_t)(h - hq - hk) * p.D;
+        };
+        auto load = [&](int h, uint4 &x0, uint4 &x1) {
+            if (h < hq && p.in_place && !in_rot) return;
+            const bool is_v = !kLatent && h >= hq + hk;
+            const uint16_t *s = src_of(h);
+            x0 = ld_row(s + (is_v ? 16 * j : r0));
+            if (has1 && (!is_v || 16 * j + 8 < p.D)) x1 = ld_row(s + (is_v ? 16 * j + 8 : r1));
+        };
+        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+        if (work && h_first < p.heads) load(h_first, x0, x1);
+        float2 *cs = reinterpret_cast<float2 *>(smem) + (size_t)buf * p.tokens * pairs;
+        if (ta < at)
+            for (int t = ta; t < nt; t += at) cs[t * pairs + ia] = cos_sin(__ldg(apos + n0 + t), F, finite);
+        if (tid >= kThreads - 32 && tid - (kThreads - 32) < nt) {
+            const int t = tid - (kThreads - 32);
+            s_slot[buf][t] = kLatent ? (__ldg(p.positions + n0 + t) < 0 ? kSkip : kNowhere) : slot_of(p, n0 + t, true);
+        }
+        __syncthreads();
+        if (!work) continue;
+        const int64_t slot = s_slot[buf][ts];
+        if (slot == kSkip) continue;
+        for (int h = h_first; h < p.heads; h += h_step) {
+            uint4 y0 = make_uint4(0u, 0u, 0u, 0u), y1 = y0;
+            if (h + h_step < p.heads && p.tokens == 1) load(h + h_step, y0, y1);
+            const bool is_q = h < hq, is_k = !is_q && h < hq + hk, is_v = !is_q && !is_k;
+            const bool turn = in_rot && !is_v;
+            if (is_q) {
+                if (!(p.in_place && !in_rot)) {
+                    if (turn) {
+                        float x[16];
+                        unpack8(x0, x);
+                        unpack8(x1, x + 8);
+                        rotate16<kAdjacent>(x, cs + ts * pairs + 8 * j);
+                        x0 = pack8(x);
+                        x1 = pack8(x + 8);
+                    }
+                    uint16_t *o = p.q_out + ((int64_t)n * hq + h) * p.D + base;
+                    st_v4(o + r0, x0);
+                    if (has1) st_v4(o + r1, x1);
+                }
+            } else if (!kLatent && slot >= 0) {
+                const int hh = is_k ? h - hq : h - hq - hk;
+                const int o0 = is_v ? 16 * j : r0, o1 = is_v ? 16 * j + 8 : r1;
+                const bool two = is_v ? 16 * j + 8 < p.D : has1;
+                const int64_t row = (slot * p.H_kv + hh) * p.D;
+                uint8_t *pool = is_k ? p.k_pool : p.v_pool;
+                if (kKv == DA_KV_BF16) {
+                    if (turn) {
+                        float x[16];
+                        unpack8(x0, x);
+                        unpack8(x1, x + 8);
+                        rotate16<kAdjacent>(x, cs + ts * pairs + 8 * j);
+                        x0 = pack8(x);
+                        x1 = pack8(x + 8);
+                    }
+                    st_v4(pool + (row + o0) * 2, x0);
+                    if (two) st_v4(pool + (row + o1) * 2, x1);
+                } else {
+                    float x[16], q[16];
+                    unpack8(x0, x);
+                    unpack8(x1, x + 8);
+                    if (turn) rotate16<kAdjacent>(x, cs + ts * pairs + 8 * j);
+                    quot_rn(x, recip_of(__ldg((is_k ? p.k_scale : p.v_scale) + hh)), q);
+                    uint32_t c[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) c[i] = e4m3x2(q[2 * i], q[2 * i + 1]);
+                    st_v2(pool + row + o0, make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16)));
+                    if (two) st_v2(pool + row + o1, make_uint2(c[4] | (c[5] << 16), c[6] | (c[7] << 16)));
+                }
+            }
+            x0 = y0;
+            x1 = y1;
+        }
+    }
+}
+
+template <int kKv>
+cudaError_t launch(const cudaLaunchConfig_t &cfg, const RopeParams &p) {
+    return p.adjacent ? cudaLaunchKernelEx(&cfg, rope_kernel<kKv, true>, p)
+                      : cudaLaunchKernelEx(&cfg, rope_kernel<kKv, false>, p);
+}
+
+}  // namespace
+
+// Fills in p.items, heads, tokens and q_blocks and launches.
+cudaError_t launch_rope(int kv_dtype, RopeParams p, int num_sms, cudaStream_t stream, bool pdl) {
+    const bool latent = kv_dtype == DA_KV_FP8_MLA656;
+    p.items = latent && p.in_place ? p.rot / 16 : (p.D + 15) / 16;
+    p.heads = p.H_q + (latent ? 0 : 2 * p.H_kv);
+    const int per_pass = kThreads / p.items;
+    const int t = per_pass / p.heads;
+    p.tokens = t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t;
+    const int64_t tiles = ((int64_t)p.N + p.tokens - 1) / p.tokens;
+    const int64_t most = (int64_t)num_sms * 8;  // resident blocks; each walks over the tiles beyond
+    int64_t blocks = tiles < most ? tiles : most;
+    p.q_blocks = (int32_t)blocks;
+    if (latent) {
+        const int64_t lt = ((int64_t)p.N + kThreads / 32 - 1) / (kThreads / 32);
+        blocks += lt < most ? lt : most;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)2 * p.tokens * (p.rot / 2) * sizeof(float2);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    if (latent) return launch<DA_KV_FP8_MLA656>(cfg, p);
+    return kv_dtype == DA_KV_FP8_PER_TENSOR ? launch<DA_KV_FP8_PER_TENSOR>(cfg, p) : launch<DA_KV_BF16>(cfg, p);
+}
+
+}  // namespace da
