@@ -402,7 +402,7 @@ typedef enum {
  * to v exceeds floor(u_K * total), each weight its fp32 value rounded to a whole
  * number of steps of 2^-44. The sums are exact integers.
  *   B >= 1, n_draft in [0, 63] (0: draws one token per request), vocab V in
- *     [1, 2^20], prob_dtype: of both probabilities.
+ *     [1, 2^20), prob_dtype: of both probabilities.
  *   target_probs: device, row j of request b at (b * (n_draft + 1) + j) *
  *     target_stride elements; draft_probs: (b * n_draft + j) * draft_stride, or
  *     NULL for drafts that are certain (q_j(x_j) = 1). Strides: 0 for V, else >= V;

@@ -586,7 +586,7 @@ int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_
         pairs += rope->sections[a];
     }
     if (pairs != rope->rot_dim / 2) return DA_ERR_DIMS;
-    if (!requests && n_tokens != (int64_t)desc->B * sq_of(desc)) return DA_ERR_DIMS;
+    if (!requests && n_tokens != 0 && n_tokens != (int64_t)desc->B * sq_of(desc)) return DA_ERR_DIMS;
     if ((rc = check_stride(&q_stride, q_len)) || (rc = check_stride(&k_stride, row_len))) return rc;
     if (!mla && (rc = check_stride(&v_stride, row_len))) return rc;
     if (n_tokens == 0) return DA_OK;
@@ -761,7 +761,7 @@ int decode_attn_verify_drafts(int32_t B, int32_t n_draft, int32_t vocab, int32_t
                               int64_t draft_stride, const int32_t *draft_tokens, const float *uniform,
                               const int32_t *cache_seqlens, int32_t *num_accepted, int32_t *out_tokens,
                               int32_t *new_seqlens, int32_t *device_error, cudaStream_t stream) {
-    if (B < 1 || B > (1 << 20) || n_draft < 0 || n_draft > 63 || vocab < 1 || vocab > (1 << 20)) return DA_ERR_DIMS;
+    if (B < 1 || B > (1 << 20) || n_draft < 0 || n_draft > 63 || vocab < 1 || vocab >= (1 << 20)) return DA_ERR_DIMS;
     if (prob_dtype < DA_PROB_F32 || prob_dtype > DA_PROB_F16) return DA_ERR_UNSUPPORTED;
     if (target_stride == 0) target_stride = vocab;
     if (draft_stride == 0) draft_stride = vocab;

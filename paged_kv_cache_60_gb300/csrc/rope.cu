@@ -208,12 +208,19 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const bool mine = hs < per_pass && ts < p.tokens;
     const int h_step = p.tokens > 1 ? p.heads : per_pass;
     const int turned = p.rot / 16;                     // items j < turned are rotated (q and K)
-    const int base = kLatent && j < turned ? kLatentNope : 0;
-    const int jo = kLatent && j >= turned ? j - turned : j;   // copied items: their place in the head
     const bool in_rot = j < turned;
-    const int r0 = in_rot && !kAdjacent ? 8 * j : 16 * jo;    // the item's two vectors in q and K heads
-    const int r1 = in_rot && !kAdjacent ? pairs + 8 * j : 16 * jo + 8;
-    const bool has1 = in_rot || 16 * jo + 8 < p.D;            // D = 8 mod 16: the last item has one vector
+    // the item's two vectors in q and K heads; on the 656-byte format the rotated values start at 512, and the
+    // copied items are those before them, then what is left behind them
+    int r0, r1;
+    if (in_rot) {
+        r0 = (kLatent ? kLatentNope : 0) + (kAdjacent ? 16 * j : 8 * j);
+        r1 = r0 + (kAdjacent ? 8 : pairs);
+    } else {
+        const int c = 16 * (j - turned);
+        r0 = !kLatent || c >= kLatentNope ? c + p.rot : c;
+        r1 = r0 + 8;
+    }
+    const bool has1 = in_rot || r1 < p.D;                     // D = 8 mod 16: the last item has one vector
     const int hq = p.H_q, hk = kLatent ? 0 : p.H_kv;
 
     const int tiles = (p.N + p.tokens - 1) / p.tokens;
@@ -225,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         const bool work = mine && ts < nt;
         // the source of this thread's item of head h
         auto src_of = [&](int h) -> const uint16_t * {
-            if (h < hq) return p.q + (int64_t)n * p.q_stride + (int64_t)h * p.D + base;
+            if (h < hq) return p.q + (int64_t)n * p.q_stride + (int64_t)h * p.D;
             if (h < hq + hk) return p.k + (int64_t)n * p.k_stride + (int64_t)(h - hq) * p.D;
             return p.v + (int64_t)n * p.v_stride + (int64_t)(h - hq - hk) * p.D;
         };
@@ -264,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                         x0 = pack8(x);
                         x1 = pack8(x + 8);
                     }
-                    uint16_t *o = p.q_out + ((int64_t)n * hq + h) * p.D + base;
+                    uint16_t *o = p.q_out + ((int64_t)n * hq + h) * p.D;
                     st_v4(o + r0, x0);
                     if (has1) st_v4(o + r1, x1);
                 }

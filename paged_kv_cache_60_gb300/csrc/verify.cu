@@ -12,7 +12,7 @@
 //
 // The weights are counted in whole steps of 2^-44 (their fp32 values rounded to
 // nearest even, at most 2^44 each), so their sums are 64-bit integers: exact,
-// the same in any order and on any split, and never over 2^64 for up to 2^20
+// the same in any order and on any split, and below 2^64 for fewer than 2^20
 // entries. The token is the first v whose running sum exceeds floor(u_K *
 // total). A step is 2^-44: next to an fp32 probability of 1e-6 it is below the
 // rounding of the probability itself.
@@ -34,7 +34,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 1024;                        // entries per tile, one warp each
-constexpr int kMaxVocab = 1 << 20;
+constexpr int kMaxVocab = 1 << 20;                // exclusive
 constexpr int kMaxTiles = kMaxVocab / kTile;
 
 template <typename T>
