@@ -7,14 +7,17 @@
 // heads of h: the softmax weights of the step's attention call, from its lse.
 //
 // Bound by HBM: K is read once (V is not needed), w read and written once.
-// Like the attention kernel it walks the parts of the scheduling metadata; the
-// warps of a part share its tiles round robin and never wait for each other.
-// The K rows go from global memory straight into the A fragments of the warp
-// MMA (K tile as M, the 8 query heads as N): a dot product does not care in
-// which order its terms are added, so the k index of the MMA stands for
-// whichever dims make each lane's share of a row contiguous, in q as in K.
-// Lane (r, c) of a warp reads 16 contiguous bytes of row r at a time, the four
-// lanes of a row 64.
+// The kernel has the attention kernel's shape without its V half: it walks the
+// parts of the scheduling metadata in 64-token chunks, a producer warp brings
+// K pages into a ring of shared-memory stages with one TMA copy per page, and
+// every consumer warp takes whole chunks, round robin, as four 16-token tiles
+// on the M side of a warp MMA with the 8 query heads as N. The lse is final, so
+// a tile's exponentials are the weights themselves: there is no running
+// maximum, no state between chunks and nothing to merge, and the warps of all
+// CTAs write disjoint tokens. Where the metadata has fewer (part, head) pairs
+// than the GPU has room for (a short fixed split), several CTAs share a pair's
+// chunks.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -27,27 +30,52 @@
 namespace da {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-
-// D, e4m3, query tokens held in registers
+// NQ: query tokens held in registers
 template <int D, bool FP8, int NQ>
-struct Cfg {
-    static constexpr int ROW = D * (FP8 ? 1 : 2);      // bytes
-    static constexpr int NV = ROW / 64;                // 16-byte vectors per lane and row
+struct AccumCfg {
+    static constexpr int ROW = D * (FP8 ? 1 : 2);      // bytes of one token's head
+    static constexpr int NX = ROW / 128;
     static constexpr int KS = D / 16;                  // MMA steps
-    static constexpr int MT = ROW == 256 ? 1 : 2;      // 16-token m tiles per warp tile: 4 KB
-    static constexpr int TOK = 16 * MT;
-    static constexpr int TPC = kChunk / TOK;           // tiles per chunk
-    static constexpr int NG = 2 * MT;                  // 8-token groups per tile
+    static constexpr int STAGE = kChunk * ROW;
+    // Consumer warps, and stages (a multiple, so that a stage always belongs to one warp): 192 KB in flight on an SM. A
+    // producer warp issues a chunk in about 0.35 us, which 16 KB chunks (bf16, D = 128) hide behind HBM; 8 KB chunks
+    // take two CTAs, and so two producers, per SM (e4m3: 174 us against 307 with one CTA of twelve consumer warps, for
+    // 64 x 32768 tokens of 4 heads).
+    static constexpr int NCW = 6;
+    static constexpr int NS = 2 * NCW;
+    static constexpr int MIN_BLOCKS = ROW == 128 ? 2 : 1;
+    static constexpr int THREADS = (NCW + 1) * 32;
+    static constexpr int TT = NQ == 1 ? 4 : NQ == 2 ? 2 : 1;   // tiles whose scores are in registers at a time
+    static constexpr int OFF_BAR = NS * STAGE;
+    static constexpr int OFF_PAGE = OFF_BAR + 2 * NS * 8;
+    static constexpr int OFF_FLAG = OFF_PAGE + NS * 8 * 4;
+    static constexpr int SMEM = OFF_FLAG + 16 + 1024;  // + alignment slack
 };
 
 template <int D, bool FP8, int NQ>
-__global__ void __launch_bounds__(kThreads) accum_kernel(const __grid_constant__ AccumParams p) {
-    using C = Cfg<D, FP8, NQ>;
+__global__ void __launch_bounds__(AccumCfg<D, FP8, NQ>::THREADS, AccumCfg<D, FP8, NQ>::MIN_BLOCKS)
+    accum_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ AccumParams p) {
+    using C = AccumCfg<D, FP8, NQ>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *empty = full + C::NS;
+    int32_t *pages = reinterpret_cast<int32_t *>(smem + C::OFF_PAGE);   // [stage][box]: the box's page, -1: none
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r8 = lane >> 2, c4 = lane & 3;
-    const int part = blockIdx.x, h = blockIdx.y;
+    const int part = blockIdx.x, h = blockIdx.y, Z = gridDim.z;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NS; ++i) {
+            mbar_init(&full[i], p.boxes_per_chunk);  // one arrival per producer lane
+            mbar_init(&empty[i], 1);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == C::NCW && lane == 0) prefetch_tmap(&tm_k);
+    __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
 
@@ -63,21 +91,87 @@ __global__ void __launch_bounds__(kThreads) accum_kernel(const __grid_constant__
         }
     }
     const int max_len = p.max_pages * p.page_size;
-    const float sl2 = p.scale_log2 * (FP8 ? __ldg(p.k_scale + h) : 1.f);
-    const int W = kWarps * gridDim.z, w = blockIdx.z * kWarps + warp;  // warps of this part
-
+    // this CTA's chunks of a segment: lc0 + (z - lc0) mod Z, then every Z-th
+    const auto first_chunk = [&](int lc0) { return lc0 + (int)(((int)blockIdx.z + Z - lc0 % Z) % Z); };
     SegWalker wk = make_walker(p.meta, rec0, rec1, p.B, p.seqlens, max_len, p.s_q, 0, 0);
     Seg sg;
-    int done = 0;  // tiles of the part's earlier segments
+    int i = 0;  // this CTA's chunks so far
+
+    if (warp == C::NCW) {
+        // ------------------------------------------------------------ producer
+        // Lane j < boxes_per_chunk owns box j of every chunk and keeps the page ids of its next four chunks in
+        // registers, loaded four chunks ahead.
+        const int nb = p.boxes_per_chunk, bt = p.box_tokens, P = p.page_size;
+        if (lane >= nb) return;
+        const uint64_t pol = policy_evict_first();
+        const uint32_t box_bytes = (uint32_t)bt * C::ROW;
+        bool aborted = false;
+        while (!aborted && wk.next(sg)) {
+            const int32_t *table = p.block_table + (size_t)sg.b * p.max_pages;
+            auto id_of = [&](int lc) -> int {
+                const int tok = lc * kChunk + lane * bt;
+                return (lc < sg.lc1 && tok < sg.L) ? table[tok / P] : -2;
+            };
+            const int lcf = first_chunk(sg.lc0);
+            int ring[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ring[k] = id_of(lcf + k * Z);
+            for (int lc = lcf; lc < sg.lc1 && !aborted; lc += 4 * Z) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int c = lc + k * Z;
+                    if (c >= sg.lc1) break;
+                    int pg = ring[k];
+                    ring[k] = id_of(c + 4 * Z);
+                    const int stage = i % C::NS;
+                    if (!mbar_wait_bounded(&empty[stage], ((i / C::NS) & 1) ^ 1, abort_flag, p.wait_limit_ns)) {
+                        atomicOr(&p.meta.header[kHError], DA_DEV_TIMEOUT);
+                        *abort_flag = 1;
+                        aborted = true;
+                        break;
+                    }
+                    if (pg != -2 && (pg < 0 || pg >= p.num_pages)) {
+                        atomicOr(&p.meta.header[kHError], DA_DEV_BAD_PAGE);
+                        p.meta.header[kHErrorDetail] = pg;
+                        pg = -2;  // skipped: its rows keep stale bytes, its weights stay
+                    }
+                    pages[stage * 8 + lane] = pg < 0 ? -1 : pg;
+                    mbar_arrive_expect_tx(&full[stage], pg < 0 ? 0u : box_bytes);  // (releases the page id too)
+                    if (pg >= 0) {
+                        const int tok = c * kChunk + lane * bt;
+                        const int in_page = (P > kChunk) ? (tok % P) : 0;
+                        tma_load_4d(smem + (size_t)stage * C::STAGE + lane * box_bytes, &tm_k, &full[stage], 0, 0, h,
+                                    pg * P + in_page, pol);
+                    }
+                    ++i;
+                }
+            }
+        }
+        if (aborted) {
+            // let copies already in flight land before the CTA exits (ignoring the abort flag)
+            for (int k = max(0, i - C::NS); k < i; ++k) mbar_wait_timed(&full[k % C::NS], (k / C::NS) & 1, 100000000ull);
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumers
+    const int r8 = lane >> 2, c4 = lane & 3, lrow = lane & 7, lmat = lane >> 3;
+    const float sl2 = p.scale_log2 * (FP8 ? __ldg(p.k_scale + h) : 1.f);
+    const int lbt = p.log2_box_tokens;
+    // tokens whose weights this lane updates: 16 c4 + r8 of a chunk, and the eighth one after it
+    const int own = 16 * c4 + r8;
     while (wk.next(sg)) {
         const int b = sg.b, L = sg.L;
-        const int tiles = min((sg.lc1 - sg.lc0) * C::TPC, (L - sg.lc0 * kChunk + C::TOK - 1) / C::TOK);
-        if (tiles <= 0) continue;
-        const int first = (w + W - done % W) % W;
-        done += tiles;
-        if (first >= tiles) continue;
+        const int lcf = first_chunk(sg.lc0);
+        const int n = lcf < sg.lc1 ? (sg.lc1 - lcf + Z - 1) / Z : 0;   // this CTA's chunks of the segment
+        // the first of them that is this warp's
+        const int skip = (warp + C::NCW - i % C::NCW) % C::NCW;
+        if (skip >= n) {
+            i += n;
+            continue;
+        }
         // q: B fragments, n = query head r8; lse of the two heads whose scores this lane gets
-        uint32_t qf[NQ][C::KS][2];
+        uint32_t qf[C::KS][NQ][2];
         float lse2[NQ][2];
         int last[NQ];  // last token that query token j sees, -1 where it does not count
         const int acc = p.accepted ? p.accepted[b] : p.s_q - 1;
@@ -89,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) accum_kernel(const __grid_constant__
             lse2[j][0] = lse2[j][1] = 0.f;
             if (!on) {
 #pragma unroll
-                for (int k = 0; k < C::KS; ++k) qf[j][k][0] = qf[j][k][1] = 0u;
+                for (int ks = 0; ks < C::KS; ++ks) qf[ks][j][0] = qf[ks][j][1] = 0u;
                 continue;
             }
             const size_t head0 = ((size_t)b * p.s_q + j) * p.H_q + (size_t)h * 8;
@@ -99,165 +193,163 @@ __global__ void __launch_bounds__(kThreads) accum_kernel(const __grid_constant__
             lse2[j][1] = ls.y * kLog2e;
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + (head0 + r8) * D;
             if constexpr (!FP8) {
-                // vector x: dims x 32 + c4 8 .. + 7 feed two MMA steps, four dims each
+                const uint32_t *q32 = reinterpret_cast<const uint32_t *>(q);
 #pragma unroll
-                for (int x = 0; x < C::NV; ++x) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(q + x * 32 + c4 * 8);
-                    qf[j][2 * x][0] = v.x;
-                    qf[j][2 * x][1] = v.y;
-                    qf[j][2 * x + 1][0] = v.z;
-                    qf[j][2 * x + 1][1] = v.w;
+                for (int ks = 0; ks < C::KS; ++ks) {
+                    qf[ks][j][0] = q32[ks * 8 + c4];
+                    qf[ks][j][1] = q32[ks * 8 + 4 + c4];
                 }
             } else {
-                // vector x: dims x 64 + c4 16 .. + 15 feed four steps
 #pragma unroll
-                for (int x = 0; x < C::NV; ++x)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(q + x * 64 + c4 * 16 + y * 8);
-                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            qf[j][4 * x + 2 * y + i / 2][i & 1] =
-                                pack_f16(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
-                    }
+                for (int ks = 0; ks < C::KS; ++ks) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(q + ks * 16 + c4 * 4);
+                    qf[ks][j][0] = pack_f16(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+                    qf[ks][j][1] = pack_f16(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+                }
             }
         }
-        const int32_t *table = p.block_table + (size_t)b * p.max_pages;
-        // page and slot of the 8-token group g of a tile (groups start on multiples of 8, pages are multiples of 8)
-        auto page_of = [&](int t) -> int {
-            if (t >= L) return -2;
-            return table[p.log2_page >= 0 ? t >> p.log2_page : t / p.page_size];
-        };
-        auto slot_of = [&](int t) -> int {
-            return p.log2_page >= 0 ? t & (p.page_size - 1) : t % p.page_size;
-        };
-        const int base0 = sg.lc0 * kChunk;
-        int page[C::NG];
-#pragma unroll
-        for (int g = 0; g < C::NG; ++g) page[g] = page_of(base0 + first * C::TOK + 8 * g);
-        for (int ti = first; ti < tiles; ti += W) {
-            const int t0 = base0 + ti * C::TOK;
-            uint4 kv[C::NG][C::NV];
-            float *wp = nullptr;   // the weight that this lane updates: row r8 of group c4
-            float old = 0.f;
-#pragma unroll
-            for (int g = 0; g < C::NG; ++g) {
-                const int t = t0 + 8 * g;
-                int pg = page[g];
-                if (pg != -2 && (pg < 0 || pg >= p.num_pages)) {
-                    if (lane == 0) {
-                        atomicOr(&p.meta.header[kHError], DA_DEV_BAD_PAGE);
-                        p.meta.header[kHErrorDetail] = pg;
-                    }
-                    pg = -2;
+        const int i1 = i + n;
+        int c = lcf + skip * Z;
+        for (i += skip; i < i1; i += C::NCW, c += C::NCW * Z) {
+            const int stage = i % C::NS;
+            if (!mbar_wait_warp(&full[stage], (i / C::NS) & 1, abort_flag, p.wait_limit_ns)) {
+                if (lane == 0) {
+                    atomicOr(&p.meta.header[kHError], DA_DEV_TIMEOUT);
+                    *abort_flag = 1;
                 }
-                const int slot = slot_of(t);
-                const bool in = pg >= 0 && t + r8 < L;
-                const uint8_t *k = p.k_pool + (((size_t)max(pg, 0) * p.page_size + slot + r8) * p.H_kv + h) * C::ROW;
-#pragma unroll
-                for (int x = 0; x < C::NV; ++x)
-                    kv[g][x] = in ? ldg_stream16(k + x * 64 + c4 * 16) : make_uint4(0u, 0u, 0u, 0u);
-                if (g == c4 && in) {
-                    wp = p.weights + ((size_t)pg * p.H_kv + h) * p.page_size + slot + r8;
-                    old = t + r8 < wl ? *wp * p.decay : 0.f;
-                }
+                return;
             }
-            // the next tile's pages, a tile ahead of their use
-            if (ti + W < tiles) {
+            const int t0 = c * kChunk;
+            // the old weights, loaded under the products
+            float *wp[2];
+            float old[2];
 #pragma unroll
-                for (int g = 0; g < C::NG; ++g) page[g] = page_of(t0 + W * C::TOK + 8 * g);
+            for (int k = 0; k < 2; ++k) {
+                const int u = own + 8 * k, t = t0 + u;
+                const int pg = pages[stage * 8 + (u >> lbt)];
+                const int slot = p.page_size > kChunk ? t % p.page_size : u & (p.page_size - 1);
+                wp[k] = t < L && pg >= 0 ? p.weights + ((size_t)pg * p.H_kv + h) * p.page_size + slot : nullptr;
+                old[k] = 0.f;
+                if (wp[k] && t < wl) old[k] = *wp[k];   // scaled at the end: nothing waits for it here
             }
-            float sum[C::NG];
+            const uint32_t s_base = smem_u32(smem + (size_t)stage * C::STAGE);
+            float add[2] = {0.f, 0.f};
 #pragma unroll
-            for (int m = 0; m < C::MT; ++m) {
-                float s[NQ][4];
+            for (int tt = 0; tt < 4; tt += C::TT) {
+                float s[C::TT][NQ][4];
 #pragma unroll
-                for (int j = 0; j < NQ; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+                for (int t = 0; t < C::TT; ++t)
 #pragma unroll
-                for (int x = 0; x < C::NV; ++x) {
-                    const uint4 lo = kv[2 * m][x], hi = kv[2 * m + 1][x];
-                    if constexpr (!FP8) {
-                        const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+                    for (int j = 0; j < NQ; ++j) s[t][j][0] = s[t][j][1] = s[t][j][2] = s[t][j][3] = 0.f;
+                if constexpr (!FP8) {
 #pragma unroll
-                        for (int j = 0; j < NQ; ++j) {
-                            mma_bf16(s[j], a0, qf[j][2 * x][0], qf[j][2 * x][1]);
-                            mma_bf16(s[j], a1, qf[j][2 * x + 1][0], qf[j][2 * x + 1][1]);
+                    for (int ks = 0; ks < C::KS; ++ks)
+#pragma unroll
+                        for (int t = 0; t < C::TT; ++t) {
+                            const int tok = 16 * (tt + t) + lrow + (lmat & 1) * 8;
+                            const int d = ks * 16 + (lmat >> 1) * 8, x = d >> 6;
+                            const uint32_t addr = s_base + tok * C::ROW + x * 128 +
+                                                  ((((d & 63) >> 3) ^ ((tok * C::NX + x) & 7)) << 4);
+                            uint32_t a[4];
+                            ldsm_x4(addr, a[0], a[1], a[2], a[3]);
+#pragma unroll
+                            for (int j = 0; j < NQ; ++j) mma_bf16(s[t][j], a, qf[ks][j][0], qf[ks][j][1]);
                         }
-                    } else {
-                        const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, u[4] = {hi.x, hi.y, hi.z, hi.w};
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t a[4] = {
-                                e4m3x2_to_f16x2((uint16_t)(l[i] & 0xffff)), e4m3x2_to_f16x2((uint16_t)(u[i] & 0xffff)),
-                                e4m3x2_to_f16x2((uint16_t)(l[i] >> 16)), e4m3x2_to_f16x2((uint16_t)(u[i] >> 16))};
+                    for (int kk = 0; kk < D / 32; ++kk)
 #pragma unroll
-                            for (int j = 0; j < NQ; ++j) mma_f16(s[j], a, qf[j][4 * x + i][0], qf[j][4 * x + i][1]);
+                        for (int t = 0; t < C::TT; ++t) {
+                            const int tok = 16 * (tt + t) + lrow + (lmat & 1) * 8;
+                            const uint32_t addr = s_base + tok * 128 + (((kk * 2 + (lmat >> 1)) ^ (tok & 7)) << 4);
+                            uint32_t R[4];
+                            ldsm_x4(addr, R[0], R[1], R[2], R[3]);
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const uint32_t ra = R[hf * 2], rb = R[hf * 2 + 1];
+                                const uint32_t a[4] = {
+                                    e4m3x2_to_f16x2((uint16_t)(ra & 0xffff)), e4m3x2_to_f16x2((uint16_t)(rb & 0xffff)),
+                                    e4m3x2_to_f16x2((uint16_t)(ra >> 16)), e4m3x2_to_f16x2((uint16_t)(rb >> 16))};
+#pragma unroll
+                                for (int j = 0; j < NQ; ++j)
+                                    mma_f16(s[t][j], a, qf[kk * 2 + hf][j][0], qf[kk * 2 + hf][j][1]);
+                            }
                         }
-                    }
                 }
                 // a row that does not count or see the token adds nothing, whatever its score
-                float e0 = 0.f, e1 = 0.f;
-                const int ta = t0 + 16 * m + r8;
 #pragma unroll
-                for (int j = 0; j < NQ; ++j) {
-                    const bool on0 = lse2[j][0] != -INFINITY, on1 = lse2[j][1] != -INFINITY;
-                    if (ta <= last[j]) {
-                        e0 += on0 ? ex2(fmaf(s[j][0], sl2, -lse2[j][0])) : 0.f;
-                        e0 += on1 ? ex2(fmaf(s[j][1], sl2, -lse2[j][1])) : 0.f;
+                for (int t = 0; t < C::TT; ++t) {
+                    float e0 = 0.f, e1 = 0.f;
+                    const int ta = t0 + 16 * (tt + t) + r8;
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) {
+                        const bool on0 = lse2[j][0] != -INFINITY, on1 = lse2[j][1] != -INFINITY;
+                        if (ta <= last[j]) {
+                            e0 += on0 ? ex2(fmaf(s[t][j][0], sl2, -lse2[j][0])) : 0.f;
+                            e0 += on1 ? ex2(fmaf(s[t][j][1], sl2, -lse2[j][1])) : 0.f;
+                        }
+                        if (ta + 8 <= last[j]) {
+                            e1 += on0 ? ex2(fmaf(s[t][j][2], sl2, -lse2[j][0])) : 0.f;
+                            e1 += on1 ? ex2(fmaf(s[t][j][3], sl2, -lse2[j][1])) : 0.f;
+                        }
                     }
-                    if (ta + 8 <= last[j]) {
-                        e1 += on0 ? ex2(fmaf(s[j][2], sl2, -lse2[j][0])) : 0.f;
-                        e1 += on1 ? ex2(fmaf(s[j][3], sl2, -lse2[j][1])) : 0.f;
+                    e0 += __shfl_xor_sync(0xffffffffu, e0, 1);
+                    e1 += __shfl_xor_sync(0xffffffffu, e1, 1);
+                    e0 += __shfl_xor_sync(0xffffffffu, e0, 2);
+                    e1 += __shfl_xor_sync(0xffffffffu, e1, 2);
+                    if (c4 == tt + t) {
+                        add[0] = e0;
+                        add[1] = e1;
                     }
                 }
-                e0 += __shfl_xor_sync(0xffffffffu, e0, 1);
-                e1 += __shfl_xor_sync(0xffffffffu, e1, 1);
-                e0 += __shfl_xor_sync(0xffffffffu, e0, 2);
-                e1 += __shfl_xor_sync(0xffffffffu, e1, 2);
-                sum[2 * m] = e0;
-                sum[2 * m + 1] = e1;
             }
-            if (wp) {
-                float v = sum[0];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[stage]);  // rows and page ids have been read
 #pragma unroll
-                for (int g = 1; g < C::NG; ++g) v = c4 == g ? sum[g] : v;
-                *wp = old + v;
-            }
+            for (int k = 0; k < 2; ++k)
+                if (wp[k]) *wp[k] = (t0 + own + 8 * k < wl ? old[k] * p.decay : 0.f) + add[k];
         }
+        i = i1;
     }
 }
 
 template <int D, bool FP8, int NQ>
-cudaError_t launch(const AccumParams &p, int num_sms, cudaStream_t stream, bool pdl) {
-    // blocks per (part, head): enough to fill the SMs, two blocks on each
+cudaError_t launch(const CUtensorMap &tk, const AccumParams &p, int num_sms, cudaStream_t stream, bool pdl) {
+    using C = AccumCfg<D, FP8, NQ>;
+    const auto kern = accum_kernel<D, FP8, NQ>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    // CTAs per (part, head): as many as fit the GPU at once
     const int64_t pairs = (int64_t)p.num_parts * p.H_kv;
-    int64_t z = (2 * (int64_t)num_sms + pairs - 1) / pairs;
+    int64_t z = (int64_t)num_sms * C::MIN_BLOCKS / pairs;
     z = z < 1 ? 1 : z > 8 ? 8 : z;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.num_parts, (unsigned)p.H_kv, (unsigned)z);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, accum_kernel<D, FP8, NQ>, p);
+    return cudaLaunchKernelEx(&cfg, kern, tk, p);
 }
 
 template <int D, bool FP8>
-cudaError_t launch_for(const AccumParams &p, int num_sms, cudaStream_t stream, bool pdl) {
-    if (p.s_q == 1) return launch<D, FP8, 1>(p, num_sms, stream, pdl);
-    if (p.s_q == 2) return launch<D, FP8, 2>(p, num_sms, stream, pdl);
-    return launch<D, FP8, 4>(p, num_sms, stream, pdl);
+cudaError_t launch_for(const CUtensorMap &tk, const AccumParams &p, int num_sms, cudaStream_t stream, bool pdl) {
+    if (p.s_q == 1) return launch<D, FP8, 1>(tk, p, num_sms, stream, pdl);
+    if (p.s_q == 2) return launch<D, FP8, 2>(tk, p, num_sms, stream, pdl);
+    return launch<D, FP8, 4>(tk, p, num_sms, stream, pdl);
 }
 
 }  // namespace
 
-cudaError_t launch_accum(int D, bool fp8, const AccumParams &p, int num_sms, cudaStream_t stream, bool pdl) {
-    if (fp8) return launch_for<128, true>(p, num_sms, stream, pdl);
-    return D == 64 ? launch_for<64, false>(p, num_sms, stream, pdl) : launch_for<128, false>(p, num_sms, stream, pdl);
+cudaError_t launch_accum(int D, bool fp8, const CUtensorMap &tk, const AccumParams &p, int num_sms,
+                         cudaStream_t stream, bool pdl) {
+    if (fp8) return launch_for<128, true>(tk, p, num_sms, stream, pdl);
+    return D == 64 ? launch_for<64, false>(tk, p, num_sms, stream, pdl)
+                   : launch_for<128, false>(tk, p, num_sms, stream, pdl);
 }
 
 }  // namespace da

@@ -18,7 +18,8 @@ cudaError_t launch_mla(const MlaParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_combine(int DV, const CombineParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_append(int kv_dtype, const AppendParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_rope(int kv_dtype, RopeParams p, int num_sms, cudaStream_t stream, bool pdl);
-cudaError_t launch_accum(int D, bool fp8, const AccumParams &p, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_accum(int D, bool fp8, const CUtensorMap &tk, const AccumParams &p, int num_sms,
+                         cudaStream_t stream, bool pdl);
 cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_verify(int prob_dtype, const VerifyParams &p, int num_sms, cudaStream_t stream, bool pdl);
 int mla_ctas_per_part(int s_q);
@@ -692,12 +693,18 @@ int decode_attn_accum_weights(const da_desc *desc, const void *q, const void *k_
     p.H_q = desc->H_kv * desc->G;
     p.s_q = sq_of(desc);
     p.page_size = desc->page_size;
-    p.log2_page = log2_of(desc->page_size);
     p.max_pages = desc->max_pages_per_seq;
     p.num_pages = desc->num_pages;
     p.splits = desc->splits;
     p.num_parts = L.num_parts;
-    if (launch_accum(desc->D_qk, fp8, p, sms, stream, true) != cudaSuccess) return DA_ERR_CUDA;
+    p.box_tokens = desc->page_size < kChunk ? desc->page_size : kChunk;
+    p.boxes_per_chunk = kChunk / p.box_tokens;
+    p.log2_box_tokens = log2_of(p.box_tokens);
+    p.wait_limit_ns = g_wait_limit_ns ? g_wait_limit_ns : kWaitLimitNs;
+    CUtensorMap tk;
+    const int mrc = make_kv_map(&tk, k_pool, 0, false, desc, fp8 ? 1 : 2, p.box_tokens, false);
+    if (mrc) return mrc;
+    if (launch_accum(desc->D_qk, fp8, tk, p, sms, stream, true) != cudaSuccess) return DA_ERR_CUDA;
     return DA_OK;
 }
 

@@ -195,7 +195,9 @@ struct AccumParams {
     const int32_t *weighted;       // [B] or null: tokens whose weight is valid (the others start from 0)
     float *weights;                // [num_pages][H_kv][page_size]
     float decay, scale_log2;
-    int32_t B, H_kv, G, H_q, s_q, page_size, log2_page, max_pages, num_pages, splits, num_parts;
+    int32_t B, H_kv, G, H_q, s_q, page_size, max_pages, num_pages, splits, num_parts;
+    int32_t box_tokens, boxes_per_chunk, log2_box_tokens;  // as in GqaParams
+    uint64_t wait_limit_ns;
 };
 
 // Eviction by weight (evict.cu).
