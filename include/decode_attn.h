@@ -360,7 +360,7 @@ int decode_attn_accum_weights(const da_desc *desc, const void *q, const void *k_
  *   desc: B, H_kv, D_qk, D_v, page_size, max_pages_per_seq, num_pages and
  *     kv_dtype are used. bf16 pools need D_qk == D_v, a multiple of 8, e4m3 pools
  *     a multiple of 16; the 656-byte token as for decode_attn_append_kv.
- *   budget >= 1, at most max_pages_per_seq * page_size; keep_first, keep_last >=
+ *   budget >= 1, at most max_pages_per_seq * page_size (itself at most 2^30); keep_first, keep_last >=
  *     0 with keep_first + keep_last <= budget.
  *   block_table, dst_block_table: device int32 [B][max_pages_per_seq]; entries
  *     past ceil(L_b / P) and past ceil(min(L_b, budget) / P) are never read. The

@@ -722,6 +722,8 @@ int decode_attn_evict(const da_desc *desc, int32_t budget, int32_t keep_first, i
     if (budget < 1 || budget > (int64_t)desc->max_pages_per_seq * desc->page_size || keep_first < 0 || keep_last < 0 ||
         (int64_t)keep_first + keep_last > budget)
         return DA_ERR_DIMS;
+    // token indices leave room for a CTA's stride
+    if ((int64_t)desc->max_pages_per_seq * desc->page_size > ((int64_t)1 << 30)) return DA_ERR_DIMS;
     // rows of the selection, and tiles of the copy (at least one token each), index the grids
     if ((int64_t)desc->B * desc->H_kv > (INT32_MAX >> 3) || (int64_t)desc->B * budget > (int64_t)INT32_MAX)
         return DA_ERR_DIMS;

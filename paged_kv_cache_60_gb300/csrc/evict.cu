@@ -23,6 +23,7 @@
 // and written once.
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 
 #include "common.cuh"
@@ -32,16 +33,18 @@
 namespace da {
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kBins = 2048;
-constexpr int kKeyCap = 40960;  // keys a CTA keeps in shared memory (160 KB); later ones are read again from the pool
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;     // of the first two digits (11 bits); the third has 1024
+constexpr int kCopies = 4;      // of the first digit's histogram
+constexpr int kKeyCap = 36864;  // keys a CTA keeps in shared memory (144 KB); later ones are read again from the pool
 
 __device__ __forceinline__ int page_index(int t, int page_size, int log2_page) {
     return log2_page >= 0 ? t >> log2_page : t / page_size;
 }
 
 // Unsigned key in the order of the weights: -inf lowest, -0 = +0, NaN (any)
-// above +inf.
+// above +inf. 0 is below every weight's.
 __device__ __forceinline__ uint32_t key_of(float w) {
     if (w != w) return 0xFFFFFFFFu;
     const uint32_t u = __float_as_uint(w + 0.f);
@@ -53,23 +56,75 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t caddr) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
     return v;
 }
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t caddr) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(caddr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void red_cluster_add(uint32_t caddr, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
+}
+
+// One token's key; 0 for a token on a page outside the pool.
+__device__ __noinline__ uint32_t weight_key(const EvictParams &p, const int32_t *table, int h, int t) {
+    const int pi = page_index(t, p.page_size, p.log2_page), page = __ldg(table + pi);
+    if (page < 0 || page >= p.num_pages) {
+        if (p.error) atomicOr(p.error, DA_DEV_BAD_PAGE);
+        return 0u;
+    }
+    return key_of(__ldg(p.weights + ((int64_t)page * p.H_kv + h) * p.page_size + (t - pi * p.page_size)));
+}
 
 struct SelSmem {
-    uint32_t hist[3][kBins];   // this CTA's counts, one histogram a digit
-    uint32_t warp_sum[32];
-    uint32_t wgt[33], weq[33];
-    uint32_t digit, above;     // the digit found, tokens above it
-    uint32_t gt, eq;           // this CTA's tokens above / at the last kept key
+    // this CTA's counts: the first digit's in kCopies interleaved copies (a warp's lanes spread over them, since
+    // weights crowd into few exponents), then the other digits'
+    uint32_t hist0[kBins * kCopies];
+    uint32_t hist[3][kBins];
+    uint32_t warp_sum[kSelWarps], wgt[kSelWarps], weq[kSelWarps];
+    uint32_t digit, above;         // the digit found, tokens above it
+    uint32_t gt, eq;               // this CTA's tokens above / at the last kept key
 };
+constexpr int kSelBase = (sizeof(SelSmem) + 15) / 16 * 16;
+constexpr int kRowHist = 3 * kBins * 4;   // in a cluster: the whole row's histograms, on rank 0
+constexpr int sel_keys_at(int cluster) { return kSelBase + (cluster > 1 ? kRowHist : 0); }
+
+// sum of one value per warp over the warps below `upto`
+__device__ __forceinline__ uint32_t sum_below(const uint32_t *per_warp, int upto, int lane) {
+    return __reduce_add_sync(0xffffffffu, lane < upto ? per_warp[lane] : 0u);
+}
+
+// Counts one key per lane that is `in`: one add for the whole warp where many of its keys share a bin (equal weights).
+__device__ __forceinline__ void count(uint32_t *hist, uint32_t bin, bool in, int lane) {
+    const uint32_t act = __ballot_sync(0xffffffffu, in);
+    if (__popc(act) >= 8) {
+        const uint32_t b0 = __shfl_sync(0xffffffffu, bin, __ffs(act) - 1);
+        if (__all_sync(0xffffffffu, !in || bin == b0)) {
+            if (lane == 0) atomicAdd(hist + b0, (uint32_t)__popc(act));
+            return;
+        }
+    }
+    if (in) atomicAdd(hist + bin, 1u);
+}
 
 // kC: CTAs per cluster
 template <int kC>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
-    extern __shared__ uint32_t keys[];
-    __shared__ SelSmem s;
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __grid_constant__ EvictParams p) {
+    extern __shared__ __align__(16) uint8_t sel_smem[];
+    SelSmem &s = *reinterpret_cast<SelSmem *>(sel_smem);
+    uint32_t *row_hist = reinterpret_cast<uint32_t *>(sel_smem + kSelBase);
+    uint32_t *keys = reinterpret_cast<uint32_t *>(sel_smem + sel_keys_at(kC));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = kC > 1 ? (int)cluster_ctarank() : 0;
     const int row = blockIdx.x / kC, b = row / p.H_kv, h = row - b * p.H_kv;
+    static_assert(offsetof(SelSmem, hist) == sizeof(s.hist0), "cleared as one");
+    for (int i = tid; i < (kCopies + 3) * kBins / 4; i += kSelThreads)
+        reinterpret_cast<uint4 *>(s.hist0)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (kC > 1)
+        for (int i = tid; i < kRowHist / 16; i += kSelThreads)
+            reinterpret_cast<uint4 *>(row_hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     pdl_wait();
     pdl_launch_dependents();
 
@@ -94,69 +149,112 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     uint32_t want = N - F - R;    // tokens to choose, < M
     if (want == 0) return;        // uniform over the cluster, as every exit above
 
-    // this CTA's share [m0, m1) of the middle, a multiple of 32 tokens
-    const int share = ((M + kC - 1) / kC + 31) / 32 * 32;
-    const int m0 = min(M, rank * share), m1 = min(M, m0 + share), n = m1 - m0;
+    // this CTA's share [m0, m1) of the middle, a multiple of 128 tokens
+    const int share = (int)((((int64_t)M + kC - 1) / kC + 127) / 128 * 128);
+    const int m0 = (int)min((int64_t)M, (int64_t)rank * share), n = min(share, M - m0);
+    const int t0 = F + m0;
     const int32_t *table = p.src_table + (int64_t)b * p.max_pages;
-    auto weight_key = [&](int i) -> uint32_t {
-        const int t = F + m0 + i, pi = page_index(t, p.page_size, p.log2_page);
-        const int page = __ldg(table + pi);
-        if (page < 0 || page >= p.num_pages) {
-            if (p.error) atomicOr(p.error, DA_DEV_BAD_PAGE);
-            return 0u;  // below every weight
-        }
-        return key_of(__ldg(p.weights + ((int64_t)page * p.H_kv + h) * p.page_size + (t - pi * p.page_size)));
-    };
-    for (int i = tid; i < kBins; i += kSelThreads) s.hist[0][i] = s.hist[1][i] = s.hist[2][i] = 0;
+    __syncthreads();  // the histograms are clear
+    // kBatch pages, then their weights: two latencies for kBatch * kSelThreads keys
+    constexpr int kBatch = 8;
     const int nc = min(n, kKeyCap);
-    for (int i = tid; i < nc; i += kSelThreads) keys[i] = weight_key(i);
+    for (int i0 = 0; i0 < nc; i0 += kBatch * kSelThreads) {
+        int page[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = min(i0 + u * kSelThreads + tid, nc - 1);
+            page[u] = __ldg(table + page_index(t0 + i, p.page_size, p.log2_page));
+        }
+        float w[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int t = t0 + min(i0 + u * kSelThreads + tid, nc - 1);
+            const int slot = t - page_index(t, p.page_size, p.log2_page) * p.page_size;
+            const bool ok = page[u] >= 0 && page[u] < p.num_pages;
+            w[u] = ok ? __ldg(p.weights + ((int64_t)page[u] * p.H_kv + h) * p.page_size + slot) : 0.f;
+            if (!ok) page[u] = -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * kSelThreads + tid;
+            if (i0 + u * kSelThreads >= nc) break;
+            const uint32_t k = page[u] < 0 ? 0u : key_of(w[u]);
+            if (i < nc) {
+                keys[i] = k;
+                if (page[u] < 0 && p.error) atomicOr(p.error, DA_DEV_BAD_PAGE);
+            }
+            count(s.hist0 + (lane & (kCopies - 1)), (k >> 21) * kCopies, i < nc, lane);
+        }
+    }
+    for (int i0 = nc; i0 < n; i0 += kSelThreads) {  // keys beyond shared memory
+        const int i = i0 + tid;
+        count(s.hist0 + (lane & (kCopies - 1)), i < n ? (weight_key(p, table, h, t0 + i) >> 21) * kCopies : 0u, i < n, lane);
+    }
     __syncthreads();
-    auto key = [&](int i) -> uint32_t { return i < kKeyCap ? keys[i] : weight_key(i); };
+    // keys i .. i + 3 (i a multiple of 4); what lies past n is not a key
+    auto keys4 = [&](int i, uint32_t(&k)[4]) {
+        if (i < kKeyCap) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(keys + i);
+            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) k[u] = i + u < n ? weight_key(p, table, h, t0 + i + u) : 0u;
+        }
+    };
 
-    // digits, highest first
+    // digits of 11, 11 and 10 bits, highest first
     uint32_t prefix = 0, mask = 0, local_above = 0;
 #pragma unroll
     for (int d = 0; d < 3; ++d) {
         const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
         const int bins = d == 2 ? 1024 : kBins;
         uint32_t *hist = s.hist[d];
-        for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-            const int i = i0 + tid;
-            const uint32_t k = i < n ? key(i) : 0u;
-            const bool in = i < n && (k & mask) == prefix;
-            const uint32_t bin = (k >> shift) & (bins - 1);
-            // one add per warp where all its keys share a bin (equal weights)
-            const uint32_t act = __ballot_sync(0xffffffffu, in);
-            if (act) {
-                const uint32_t b0 = __shfl_sync(0xffffffffu, bin, __ffs(act) - 1);
-                if (__all_sync(0xffffffffu, !in || bin == b0)) {
-                    if (lane == 0) atomicAdd(hist + b0, (uint32_t)__popc(act));
-                } else if (in) {
-                    atomicAdd(hist + bin, 1u);
-                }
-            }
-        }
-        if (kC > 1)
-            cluster_sync_all();
-        else
-            __syncthreads();
-        // the whole row's counts, two bins a thread from the top, and their suffix sums
-        const int top = bins - 1 - 2 * tid;  // bins top and top - 1
-        uint32_t c0 = 0, c1 = 0;
-        if (top > 0) {
-            const uint32_t a = smem_u32(hist + top - 1);
+        if (d > 0) {
+            for (int i0 = 4 * (tid - lane); i0 < n; i0 += 4 * kSelThreads) {
+                const int i = i0 + 4 * lane;
+                uint32_t k[4] = {0u, 0u, 0u, 0u};
+                if (i < n) keys4(i, k);
 #pragma unroll
-            for (int r = 0; r < kC; ++r) {
-                if (kC > 1) {
-                    c1 += ld_cluster_u32(mapa_shared(a, r));
-                    c0 += ld_cluster_u32(mapa_shared(a + 4, r));
-                } else {
-                    c1 += hist[top - 1];
-                    c0 += hist[top];
+                for (int u = 0; u < 4; ++u) count(hist, (k[u] >> shift) & (bins - 1), i + u < n && (k[u] & mask) == prefix, lane);
+            }
+            __syncthreads();
+        }
+        // four bins a thread, from the top
+        const int base = bins - 4 * (tid + 1);
+        uint32_t c[4] = {0u, 0u, 0u, 0u};
+        if (base >= 0) {
+            if (d == 0) {
+                static_assert(kCopies == 4, "one 16-byte vector of copies per bin");
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(s.hist0 + (base + i) * kCopies);
+                    c[i] = v.x + v.y + v.z + v.w;
                 }
+                if (kC > 1) *reinterpret_cast<uint4 *>(hist + base) = make_uint4(c[0], c[1], c[2], c[3]);
+            } else {
+                const uint4 v = *reinterpret_cast<const uint4 *>(hist + base);
+                c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
             }
         }
-        uint32_t v = c0 + c1;
+        if (kC > 1) {
+            // the whole row's counts: every CTA adds its bins that are not empty to rank 0's, then reads the sums
+            __syncwarp();
+            if (d == 0) cluster_sync_all();  // rank 0's memory is there, and clear
+            const uint32_t a = mapa_shared(smem_u32(row_hist + d * kBins + max(base, 0)), 0);
+            if (base >= 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c[i]) red_cluster_add(a + 4 * i, c[i]);
+            }
+            __syncwarp();
+            cluster_sync_all();
+            if (base >= 0) {
+                const uint4 v = ld_cluster_v4(a);
+                c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
+            }
+        }
+        const uint32_t mine4 = c[0] + c[1] + c[2] + c[3];
+        uint32_t v = mine4;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
@@ -164,46 +262,40 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         }
         if (lane == 31) s.warp_sum[warp] = v;
         __syncthreads();
-        uint32_t before = 0;
-        {
-            uint32_t w = lane < warp ? s.warp_sum[lane] : 0u;
-            before = __reduce_add_sync(0xffffffffu, w);
-        }
-        const uint32_t incl = before + v, excl = incl - c0 - c1;  // counts above these bins
-        if (top > 0) {
-            if (excl < want && want <= excl + c0) {
-                s.digit = top;
-                s.above = excl;
-            } else if (excl + c0 < want && want <= incl) {
-                s.digit = top - 1;
-                s.above = excl + c0;
+        uint32_t above = sum_below(s.warp_sum, warp, lane) + v - mine4;   // tokens above this thread's bins
+        if (base >= 0) {
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                if (above < want && want <= above + c[i]) {
+                    s.digit = base + i;
+                    s.above = above;
+                }
+                above += c[i];
             }
         }
         __syncthreads();
         const uint32_t digit = s.digit;
         want -= s.above;
-        // this CTA's tokens above the digit
-        uint32_t mine = 0;
-        for (int i = digit + 1 + tid; i < bins; i += kSelThreads) mine += hist[i];
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        if (lane == 0) s.wgt[warp] = mine;
-        __syncthreads();
-        local_above += __reduce_add_sync(0xffffffffu, s.wgt[lane]);
-        if (d == 2 && tid == 0) {
-            s.gt = local_above;
-            s.eq = hist[digit];
+        if (kC > 1) {  // this CTA's tokens above the digit
+            uint32_t mine = 0;
+            for (int i = digit + 1 + tid; i < bins; i += kSelThreads) mine += hist[i];
+            mine = __reduce_add_sync(0xffffffffu, mine);
+            if (lane == 0) s.wgt[warp] = mine;
+            __syncthreads();
+            local_above += sum_below(s.wgt, kSelWarps, lane);
+            if (d == 2 && tid == 0) {
+                s.gt = local_above;
+                s.eq = hist[digit];
+            }
+            __syncthreads();  // s.wgt is written again
         }
         prefix |= digit << shift;
         mask |= (uint32_t)(bins - 1) << shift;
-        __syncthreads();  // s.digit and s.wgt are written again
     }
-    if (kC > 1)
-        cluster_sync_all();  // every CTA's gt and eq
-    else
-        __syncthreads();
     const uint32_t T = prefix;  // tokens above T are kept, and the first `want` of those at T
     uint32_t gt_before = 0, eq_before = 0;
     if (kC > 1) {
+        cluster_sync_all();  // every CTA's gt and eq
         if (lane < rank) {
             gt_before = ld_cluster_u32(mapa_shared(smem_u32(&s.gt), lane));
             eq_before = ld_cluster_u32(mapa_shared(smem_u32(&s.eq), lane));
@@ -212,14 +304,18 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         eq_before = __reduce_add_sync(0xffffffffu, eq_before);
         cluster_arrive_all();  // done with the other CTAs' memory; waited for before the exit
     }
-    // each warp counts, then lists, a contiguous run of this CTA's share
-    const int per = ((n + 31) / 32 + 31) / 32 * 32;
-    const int w0 = min(n, warp * per), w1 = min(n, w0 + per);
+    // each warp counts, then lists, a contiguous run of this CTA's share, 128 keys at a time
+    const int per = (n + kSelWarps * 128 - 1) / (kSelWarps * 128) * 128;
+    const int w0 = (int)min((int64_t)n, (int64_t)warp * per), w1 = min(n, w0 + per);
     uint32_t gt = 0, eq = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t k = key(i);
-        gt += k > T;
-        eq += k == T;
+    for (int i = w0 + 4 * lane; i < w1; i += 128) {
+        uint32_t k[4];
+        keys4(i, k);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            gt += i + u < w1 && k[u] > T;
+            eq += i + u < w1 && k[u] == T;
+        }
     }
     gt = __reduce_add_sync(0xffffffffu, gt);
     eq = __reduce_add_sync(0xffffffffu, eq);
@@ -228,23 +324,44 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         s.weq[warp] = eq;
     }
     __syncthreads();
-    gt_before += __reduce_add_sync(0xffffffffu, lane < warp ? s.wgt[lane] : 0u);
-    eq_before += __reduce_add_sync(0xffffffffu, lane < warp ? s.weq[lane] : 0u);
+    gt_before += sum_below(s.wgt, warp, lane);
+    eq_before += sum_below(s.weq, warp, lane);
     const uint32_t below = (1u << lane) - 1u;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < w1 ? key(i) : 0u;
-        const bool g = i < w1 && k > T, e = i < w1 && k == T;
-        const uint32_t bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
-        const uint32_t eb = eq_before + __popc(be & below);   // equal tokens before this one
-        if (g || (e && eb < want)) {
-            const uint32_t at = gt_before + __popc(bg & below) + min(eb, want);
-            kept[F + at] = F + m0 + i;
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+        const int i = i0 + 4 * lane;
+        uint32_t k[4] = {0u, 0u, 0u, 0u};
+        if (i < w1) keys4(i, k);
+        bool g[4], e[4];
+        uint32_t at = gt_before, eb = eq_before;   // tokens above / at T before this lane's
+        bool any_e = false;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            g[u] = i + u < w1 && k[u] > T;
+            e[u] = i + u < w1 && k[u] == T;
+            any_e |= e[u];
+            const uint32_t m = __ballot_sync(0xffffffffu, g[u]);
+            at += __popc(m & below);
+            gt_before += __popc(m);
         }
-        gt_before += __popc(bg);
-        eq_before += __popc(be);
+        if (__any_sync(0xffffffffu, any_e)) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t m = __ballot_sync(0xffffffffu, e[u]);
+                eb += __popc(m & below);
+                eq_before += __popc(m);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (g[u] || (e[u] && eb < want)) kept[F + at + min(eb, want)] = F + m0 + i + u;
+            at += g[u];
+            eb += e[u];
+        }
     }
-    if (kC > 1) cluster_wait_all();
+    if (kC > 1) {
+        __syncwarp();
+        cluster_wait_all();
+    }
 }
 
 constexpr int kCopyThreads = 256;
@@ -306,14 +423,16 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_c
 }
 
 template <int kC>
-cudaError_t launch_select(const EvictParams &p, int key_bytes, cudaStream_t stream, bool pdl) {
+cudaError_t launch_select(const EvictParams &p, int64_t keys, cudaStream_t stream, bool pdl) {
     const auto kern = evict_select_kernel<kC>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         sel_keys_at(kC) + kKeyCap * 4);
     if (e != cudaSuccess) return e;
+    const int smem = sel_keys_at(kC) + (int)(keys < kKeyCap ? keys : kKeyCap) * 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.B * p.H_kv * kC));
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = key_bytes;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     int n = 0;
@@ -335,17 +454,16 @@ cudaError_t launch_select(const EvictParams &p, int key_bytes, cudaStream_t stre
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream, bool pdl) {
-    // CTAs per row: as many as there are SMs for, while each still has a few thousand tokens of the longest
-    // length the block table allows
+    // CTAs per row: as many as there are SMs for, while each still has a few thousand tokens of the longest length
+    // that the block table allows
     const int64_t rows = (int64_t)p.B * p.H_kv, longest = (int64_t)p.max_pages * p.page_size;
     int c = 1;
     while (c < 8 && rows * c * 2 <= num_sms && longest / c > 4096) c *= 2;
-    const int64_t share = (longest + c - 1) / c + 32;
-    const int key_bytes = (int)(share < kKeyCap ? share : kKeyCap) * 4;
-    cudaError_t e = c == 8   ? launch_select<8>(p, key_bytes, stream, pdl)
-                    : c == 4 ? launch_select<4>(p, key_bytes, stream, pdl)
-                    : c == 2 ? launch_select<2>(p, key_bytes, stream, pdl)
-                             : launch_select<1>(p, key_bytes, stream, pdl);
+    const int64_t share = (longest + c - 1) / c + 128;
+    cudaError_t e = c == 8   ? launch_select<8>(p, share, stream, pdl)
+                    : c == 4 ? launch_select<4>(p, share, stream, pdl)
+                    : c == 2 ? launch_select<2>(p, share, stream, pdl)
+                             : launch_select<1>(p, share, stream, pdl);
     if (e != cudaSuccess) return e;
     // tile: about 64 KB of rows per CTA
     const int64_t token_bytes = (int64_t)p.H_kv * p.row_bytes * (p.v_pool ? 2 : 1);

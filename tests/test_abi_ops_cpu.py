@@ -100,6 +100,7 @@ def test_evict_refusals(lib):
     assert call(_desc(kv_dtype=da.KV_FP8, D_qk=72, D_v=72)) == -3             # rows of 16-byte vectors
     assert call(_desc(D_qk=100, D_v=100)) == -3
     assert call(_latent(), vp=P(0x400000)) == -3
+    assert call(_desc(B=1, max_pages_per_seq=(1 << 26) + 1)) == -2            # over 2^30 tokens a request
     assert call(_desc(B=1 << 22, H_kv=256, max_pages_per_seq=10)) == -2
 
 
