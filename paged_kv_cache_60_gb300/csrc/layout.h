@@ -178,7 +178,8 @@ struct RopeParams {
     int32_t in_place;              // q_out is q: values that are not rotated stay where they are
     int32_t items;                 // 16-value items per head
     int32_t heads;                 // head slots per token: q heads, then K and V heads (not for the 656-byte token)
-    int32_t tokens;                // tokens a block works on at a time
+    int32_t tokens;                // tokens of a tile
+    int32_t parts;                 // blocks that share a tile's rows
     int32_t q_blocks;              // 656-byte token: blocks before this one rotate q, the others write tokens
 };
 

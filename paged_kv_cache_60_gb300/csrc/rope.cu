@@ -18,11 +18,13 @@
 // the phase error is below |pos| * 2^-63 turns. The top 32 bits, as a signed
 // fraction of half a turn, go to sincospif.
 //
-// Bound by HBM: every value is read and written once. Work item = 16 values of
-// a head (two 16-byte vectors, the two halves of eight pairs); a thread keeps
-// the same place in a head and walks over the heads of a token, so cos and sin
-// of its eight pairs are read from shared memory, where each angle is computed
-// once per token.
+// Bound by HBM: every value is read and written once. A block works on a tile
+// of tokens: it computes each token's angles once, into shared memory, and then
+// walks over the tile's rows (a row is one head of q, K or V of one token). Work
+// item = 16 values of a row (two 16-byte vectors, the two halves of eight
+// pairs); a thread keeps its place in the rows and takes a few rows at a time,
+// their loads in flight together. The next tile's angles are computed before
+// this tile's rows, so one barrier a tile is all there is.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -36,7 +38,10 @@ namespace da {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;  // tokens a block works on at a time
+constexpr int kMaxTokens = 32;    // tokens of a tile
+constexpr int kMaxAngles = 1024;  // angles of a tile (at least one token's)
+// rows a thread has in flight (the e4m3 build's quotients leave registers for two)
+constexpr int unroll_of(int kv) { return kv == DA_KV_FP8_PER_TENSOR ? 2 : 4; }
 
 // inv_freq / (2 pi) mod 1, in units of 2^-64, from the fp32 bits: mantissa
 // (24 bits) times floor(2^64 / (2 pi)), shifted by the exponent. Finite input.
@@ -123,12 +128,13 @@ __device__ __forceinline__ uint4 pack8(const float *v) {
     return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
-// Rotates the eight pairs of an item; cs: their (cos, sin).
+// Rotates the eight pairs of item j; cs: a token's (cos, sin), two pairs to a
+// vector, vector k of item j at [k][j] (so that the items' lanes read side by side).
 template <bool kAdjacent>
-__device__ __forceinline__ void rotate16(float (&x)[16], const float2 *cs) {
+__device__ __forceinline__ void rotate16(float (&x)[16], const float4 *cs, int j, int turned) {
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
-        const float4 c2 = *reinterpret_cast<const float4 *>(cs + k);
+        const float4 c2 = cs[(k / 2) * turned + j];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const float c = u ? c2.z : c2.x, s = u ? c2.w : c2.y;
@@ -170,11 +176,12 @@ __device__ __forceinline__ void latent_token(const RopeParams &p, int n, int lan
 }
 
 template <int kKv, bool kAdjacent>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    extern __shared__ float4 smem[];
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeParams p) {
+    extern __shared__ float4 smem[];  // [2][tokens][4][turned] angles
     __shared__ int64_t s_slot[2][kMaxTokens];
     constexpr bool kLatent = kKv == DA_KV_FP8_MLA656;
-    const int tid = threadIdx.x, pairs = p.rot / 2;
+    constexpr int kUnroll = unroll_of(kKv);
+    const int tid = threadIdx.x, pairs = p.rot / 2, turned = p.rot / 16;  // items j < turned are rotated (q and K)
     pdl_wait();
     pdl_launch_dependents();
 
@@ -202,14 +209,26 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         F = finite ? turns_of(f) : 0;
         apos += (int64_t)axis_of(p, ia) * p.N;
     }
-    // items: thread (head slot, j) holds 16-value item j of a head
+    const int cs_at = (((ia & 7) >> 1) * turned + (ia >> 3)) * 2 + (ia & 1);  // of its (cos, sin) in a token's angles
+    const int tiles = (p.N + p.tokens - 1) / p.tokens;
+    // block -> tile (the grid strides over them) and part of the tile's rows
+    const int first = blockIdx.x / p.parts, part = blockIdx.x - first * p.parts;
+    const int stride = (kLatent ? p.q_blocks : (int)gridDim.x) / p.parts;
+    auto prepare = [&](int tile, int buf) {
+        const int n0 = tile * p.tokens, nt = min(p.tokens, p.N - n0);
+        if (ta < at) {
+            float2 *cs = reinterpret_cast<float2 *>(smem) + (size_t)buf * p.tokens * pairs + cs_at;
+            for (int t = ta; t < nt; t += at) cs[t * pairs] = cos_sin(__ldg(apos + n0 + t), F, finite);
+        }
+        const int t = tid - (kThreads - 32);
+        if (t >= 0 && t < nt)
+            s_slot[buf][t] = kLatent ? (__ldg(p.positions + n0 + t) < 0 ? kSkip : kNowhere) : slot_of(p, n0 + t, part == 0);
+    };
+
+    // this thread's place in the rows: item j, of every per_pass-th row
     const int per_pass = kThreads / p.items, hs = tid / p.items, j = tid - hs * p.items;
-    const int ts = p.tokens > 1 ? hs / p.heads : 0, h_first = hs - ts * p.heads;
-    const bool mine = hs < per_pass && ts < p.tokens;
-    const int h_step = p.tokens > 1 ? p.heads : per_pass;
-    const int turned = p.rot / 16;                     // items j < turned are rotated (q and K)
     const bool in_rot = j < turned;
-    // the item's two vectors in q and K heads; on the 656-byte format the rotated values start at 512, and the
+    // the item's two vectors in q and K rows; on the 656-byte format the rotated values start at 512, and the
     // copied items are those before them, then what is left behind them
     int r0, r1;
     if (in_rot) {
@@ -220,94 +239,113 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         r0 = !kLatent || c >= kLatentNope ? c + p.rot : c;
         r1 = r0 + 8;
     }
-    const bool has1 = in_rot || r1 < p.D;                     // D = 8 mod 16: the last item has one vector
+    const int v0 = 16 * j, v1 = 16 * j + 8;              // in V rows
+    const bool has1 = in_rot || r1 < p.D, v_has1 = v1 < p.D;  // D = 8 mod 16: the last item has one vector
     const int hq = p.H_q, hk = kLatent ? 0 : p.H_kv;
+    const int step_t = per_pass / p.heads, step_h = per_pass - step_t * p.heads;
 
-    const int tiles = (p.N + p.tokens - 1) / p.tokens;
-    const int blocks = kLatent ? p.q_blocks : gridDim.x;
-    int buf = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += blocks, buf ^= 1) {
-        const int n0 = tile * p.tokens, nt = min(p.tokens, p.N - n0);
-        const int n = n0 + ts;
-        const bool work = mine && ts < nt;
-        // the source of this thread's item of head h
-        auto src_of = [&](int h) -> const uint16_t * {
-            if (h < hq) return p.q + (int64_t)n * p.q_stride + (int64_t)h * p.D;
-            if (h < hq + hk) return p.k + (int64_t)n * p.k_stride + (int64_t)(h - hq) * p.D;
-            return p.v + (int64_t)n * p.v_stride + (int64_t)(h - hq - hk) * p.D;
-        };
-        auto load = [&](int h, uint4 &x0, uint4 &x1) {
-            if (h < hq && p.in_place && !in_rot) return;
-            const bool is_v = !kLatent && h >= hq + hk;
-            const uint16_t *s = src_of(h);
-            x0 = ld_row(s + (is_v ? 16 * j : r0));
-            if (has1 && (!is_v || 16 * j + 8 < p.D)) x1 = ld_row(s + (is_v ? 16 * j + 8 : r1));
-        };
-        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
-        if (work && h_first < p.heads) load(h_first, x0, x1);
-        float2 *cs = reinterpret_cast<float2 *>(smem) + (size_t)buf * p.tokens * pairs;
-        if (ta < at)
-            for (int t = ta; t < nt; t += at) cs[t * pairs + ia] = cos_sin(__ldg(apos + n0 + t), F, finite);
-        if (tid >= kThreads - 32 && tid - (kThreads - 32) < nt) {
-            const int t = tid - (kThreads - 32);
-            s_slot[buf][t] = kLatent ? (__ldg(p.positions + n0 + t) < 0 ? kSkip : kNowhere) : slot_of(p, n0 + t, true);
-        }
-        __syncthreads();
-        if (!work) continue;
-        const int64_t slot = s_slot[buf][ts];
-        if (slot == kSkip) continue;
-        for (int h = h_first; h < p.heads; h += h_step) {
-            uint4 y0 = make_uint4(0u, 0u, 0u, 0u), y1 = y0;
-            if (h + h_step < p.heads && p.tokens == 1) load(h + h_step, y0, y1);
-            const bool is_q = h < hq, is_k = !is_q && h < hq + hk, is_v = !is_q && !is_k;
-            const bool turn = in_rot && !is_v;
-            if (is_q) {
-                if (!(p.in_place && !in_rot)) {
-                    if (turn) {
-                        float x[16];
-                        unpack8(x0, x);
-                        unpack8(x1, x + 8);
-                        rotate16<kAdjacent>(x, cs + ts * pairs + 8 * j);
-                        x0 = pack8(x);
-                        x1 = pack8(x + 8);
-                    }
-                    uint16_t *o = p.q_out + ((int64_t)n * hq + h) * p.D;
-                    st_v4(o + r0, x0);
-                    if (has1) st_v4(o + r1, x1);
-                }
-            } else if (!kLatent && slot >= 0) {
-                const int hh = is_k ? h - hq : h - hq - hk;
-                const int o0 = is_v ? 16 * j : r0, o1 = is_v ? 16 * j + 8 : r1;
-                const bool two = is_v ? 16 * j + 8 < p.D : has1;
-                const int64_t row = (slot * p.H_kv + hh) * p.D;
-                uint8_t *pool = is_k ? p.k_pool : p.v_pool;
-                if (kKv == DA_KV_BF16) {
-                    if (turn) {
-                        float x[16];
-                        unpack8(x0, x);
-                        unpack8(x1, x + 8);
-                        rotate16<kAdjacent>(x, cs + ts * pairs + 8 * j);
-                        x0 = pack8(x);
-                        x1 = pack8(x + 8);
-                    }
-                    st_v4(pool + (row + o0) * 2, x0);
-                    if (two) st_v4(pool + (row + o1) * 2, x1);
-                } else {
-                    float x[16], q[16];
-                    unpack8(x0, x);
-                    unpack8(x1, x + 8);
-                    if (turn) rotate16<kAdjacent>(x, cs + ts * pairs + 8 * j);
-                    quot_rn(x, recip_of(__ldg((is_k ? p.k_scale : p.v_scale) + hh)), q);
-                    uint32_t c[8];
+    if (first >= tiles) return;
+    // rows [r, end) of the tile at n0 are left, the first of them head h of token t
+    int n0, r, end, t, h;
+    auto enter = [&](int tile) {
+        n0 = tile * p.tokens;
+        const int rows = min(p.tokens, p.N - n0) * p.heads;
+        end = (int)((int64_t)rows * (part + 1) / p.parts);
+        r = (int)((int64_t)rows * part / p.parts) + hs;
+        t = r / p.heads;
+        h = r - t * p.heads;
+        if (hs >= per_pass) r = end;                     // threads behind the last whole row of a pass
+    };
+    // a batch of rows: loaded before the tile's slots are known (rows of skipped tokens are read in vain)
+    uint4 x0[kUnroll], x1[kUnroll];
+    int tt[kUnroll], hh[kUnroll], nb;
+    auto load = [&]() {
+        nb = n0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) c[i] = e4m3x2(q[2 * i], q[2 * i + 1]);
-                    st_v2(pool + row + o0, make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16)));
-                    if (two) st_v2(pool + row + o1, make_uint2(c[4] | (c[5] << 16), c[6] | (c[7] << 16)));
-                }
+        for (int u = 0; u < kUnroll; ++u) {
+            tt[u] = t;
+            hh[u] = r < end && !(h < hq && p.in_place && !in_rot) ? h : -1;
+            x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (hh[u] >= 0) {
+                const int64_t n = n0 + t;
+                const bool is_v = !kLatent && h >= hq + hk;
+                const uint16_t *src = h < hq        ? p.q + n * p.q_stride + (int64_t)h * p.D
+                                      : h < hq + hk ? p.k + n * p.k_stride + (int64_t)(h - hq) * p.D
+                                                    : p.v + n * p.v_stride + (int64_t)(h - hq - hk) * p.D;
+                x0[u] = ld_row(src + (is_v ? v0 : r0));
+                if (is_v ? v_has1 : has1) x1[u] = ld_row(src + (is_v ? v1 : r1));
             }
-            x0 = y0;
-            x1 = y1;
+            r += per_pass;
+            t += step_t;
+            h += step_h;
+            if (h >= p.heads) {
+                h -= p.heads;
+                ++t;
+            }
         }
+    };
+    int buf = 0;
+    auto finish = [&]() {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int hd = hh[u];
+            if (hd < 0) continue;
+            const int64_t slot = s_slot[buf][tt[u]];
+            if (slot == kSkip || (hd >= hq && slot < 0)) continue;
+            const float4 *cs = smem + ((size_t)buf * p.tokens + tt[u]) * (pairs / 2);
+            const bool is_q = hd < hq, is_k = !is_q && hd < hq + hk, is_v = !is_q && !is_k;
+            const bool turn = in_rot && !is_v;
+            if (kKv != DA_KV_FP8_PER_TENSOR || is_q) {
+                if (turn) {
+                    float x[16];
+                    unpack8(x0[u], x);
+                    unpack8(x1[u], x + 8);
+                    rotate16<kAdjacent>(x, cs, j, turned);
+                    x0[u] = pack8(x);
+                    x1[u] = pack8(x + 8);
+                }
+                uint16_t *o;
+                if (is_q)
+                    o = p.q_out + ((int64_t)(nb + tt[u]) * hq + hd) * p.D;
+                else
+                    o = reinterpret_cast<uint16_t *>(is_k ? p.k_pool : p.v_pool) +
+                        (slot * p.H_kv + (is_k ? hd - hq : hd - hq - hk)) * p.D;
+                st_v4(o + (is_v ? v0 : r0), x0[u]);
+                if (is_v ? v_has1 : has1) st_v4(o + (is_v ? v1 : r1), x1[u]);
+            } else {
+                const int kh = is_k ? hd - hq : hd - hq - hk;
+                float x[16], q[16];
+                unpack8(x0[u], x);
+                unpack8(x1[u], x + 8);
+                if (turn) rotate16<kAdjacent>(x, cs, j, turned);
+                quot_rn(x, recip_of(__ldg((is_k ? p.k_scale : p.v_scale) + kh)), q);
+                uint32_t c[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = e4m3x2(q[2 * i], q[2 * i + 1]);
+                uint8_t *o = (is_k ? p.k_pool : p.v_pool) + (slot * p.H_kv + kh) * p.D;
+                st_v2(o + (is_v ? v0 : r0), make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16)));
+                if (is_v ? v_has1 : has1)
+                    st_v2(o + (is_v ? v1 : r1), make_uint2(c[4] | (c[5] << 16), c[6] | (c[7] << 16)));
+            }
+        }
+    };
+    enter(first);
+    load();
+    prepare(first, 0);
+    __syncthreads();
+    for (int tile = first; tile < tiles; tile += stride, buf ^= 1) {
+        const bool more = tile + stride < tiles;
+        if (more) prepare(tile + stride, buf ^ 1);
+        for (;;) {
+            finish();
+            if (r >= end) break;
+            load();
+        }
+        if (more) {
+            enter(tile + stride);
+            load();
+        }
+        __syncthreads();  // the next tile's angles and slots are there, this one's have been used
     }
 }
 
@@ -319,21 +357,35 @@ cudaError_t launch(const cudaLaunchConfig_t &cfg, const RopeParams &p) {
 
 }  // namespace
 
-// Fills in p.items, heads, tokens and q_blocks and launches.
+// Fills in p.items, heads, tokens, parts and q_blocks and launches.
 cudaError_t launch_rope(int kv_dtype, RopeParams p, int num_sms, cudaStream_t stream, bool pdl) {
     const bool latent = kv_dtype == DA_KV_FP8_MLA656;
     p.items = latent && p.in_place ? p.rot / 16 : (p.D + 15) / 16;
     p.heads = p.H_q + (latent ? 0 : 2 * p.H_kv);
-    const int per_pass = kThreads / p.items;
-    const int t = per_pass / p.heads;
-    p.tokens = t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t;
+    const int64_t per_pass = kThreads / p.items, resident = (int64_t)num_sms * 3;
+    // tokens of a tile: what leaves every resident block the same number of tiles, at least what one pass of a block
+    // covers, at most what fits
+    const int64_t fits = kMaxAngles / (p.rot / 2) < kMaxTokens ? kMaxAngles / (p.rot / 2) : kMaxTokens;
+    const int64_t rounds = (p.N + resident * fits - 1) / (resident * fits);
+    int64_t t = (p.N + resident * rounds - 1) / (resident * rounds);
+    if (t < per_pass / p.heads) t = per_pass / p.heads;
+    if (t > fits) t = fits;
+    // few rows: whole batches of them, so that no thread waits at the barrier with nothing in flight
+    const int64_t batch = per_pass * unroll_of(kv_dtype);
+    if (t * p.heads > batch && t * p.heads < 4 * batch) t = t * p.heads / batch * batch / p.heads;
+    p.tokens = (int32_t)(t < 1 ? 1 : t);
     const int64_t tiles = ((int64_t)p.N + p.tokens - 1) / p.tokens;
-    const int64_t most = (int64_t)num_sms * 8;  // resident blocks; each walks over the tiles beyond
-    int64_t blocks = tiles < most ? tiles : most;
+    // few tiles: several blocks share a tile's rows, each still with rows for all its threads
+    int64_t parts = resident / tiles;
+    const int64_t most = ((int64_t)p.tokens * p.heads + per_pass - 1) / per_pass;
+    if (parts > most) parts = most;
+    p.parts = (int32_t)(parts < 1 ? 1 : parts);
+    int64_t blocks = (tiles < resident / p.parts ? tiles : resident / p.parts) * p.parts;
+    if (blocks < p.parts) blocks = p.parts;
     p.q_blocks = (int32_t)blocks;
     if (latent) {
         const int64_t lt = ((int64_t)p.N + kThreads / 32 - 1) / (kThreads / 32);
-        blocks += lt < most ? lt : most;
+        blocks += lt < resident ? lt : resident;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
