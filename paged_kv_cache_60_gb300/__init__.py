@@ -141,6 +141,10 @@ def _ptr(t):
 def _stream(stream):
     import torch
     if stream is None:
+        # the handle alone: building a Stream object costs more than a small call's launch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            return ctypes.c_void_p(raw(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
