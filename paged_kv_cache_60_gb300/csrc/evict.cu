@@ -11,8 +11,15 @@
 // evict_select_kernel: one thread-block cluster per (request, KV head), each
 // CTA holding a contiguous share of the middle tokens' keys in shared memory.
 // A key orders the weights as unsigned integers; the key of the last token
-// kept is found digit by digit (11, 11 and 10 bits) from histograms that the
-// CTAs of the cluster add up through distributed shared memory. The counts of
+// kept is found digit by digit (8, 12 and 12 bits) from histograms that the
+// CTAs of the cluster add up through distributed shared memory. Weights crowd
+// into few exponents, so the first digit is short enough for every lane to
+// count into a copy of its own (256 bins x 32 lanes, one bank each): its shared
+// atomics never meet in a warp. The later digits are mantissa bits and spread
+// over 4096 bins; where most keys share the first digit's bin they are counted
+// with one add per warp when they are equal (weights that are all zero). With
+// 2048 bins in four copies the first digit alone took half of the selection.
+// The counts of
 // heavier and of equal tokens in the lower shares then give every CTA its
 // place in the list, and ballots keep the order within it. No atomic changes
 // an order: the histograms are integer sums.
@@ -23,7 +30,6 @@
 // and written once.
 #include <cuda_runtime.h>
 
-#include <cstddef>
 #include <cstdint>
 
 #include "common.cuh"
@@ -35,8 +41,7 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;     // of the first two digits (11 bits); the third has 1024
-constexpr int kCopies = 4;      // of the first digit's histogram
+constexpr int kBins0 = 256, kBins = 4096;   // bins of the first digit, and of the two others
 constexpr int kKeyCap = 36864;  // keys a CTA keeps in shared memory (144 KB); later ones are read again from the pool
 
 __device__ __forceinline__ int page_index(int t, int page_size, int log2_page) {
@@ -64,10 +69,6 @@ __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t caddr) {
                  : "memory");
     return v;
 }
-__device__ __forceinline__ void red_cluster_add(uint32_t caddr, uint32_t v) {
-    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
-}
-
 // One token's key; 0 for a token on a page outside the pool.
 __device__ __noinline__ uint32_t weight_key(const EvictParams &p, const int32_t *table, int h, int t) {
     const int pi = page_index(t, p.page_size, p.log2_page), page = __ldg(table + pi);
@@ -79,34 +80,37 @@ __device__ __noinline__ uint32_t weight_key(const EvictParams &p, const int32_t 
 }
 
 struct SelSmem {
-    // this CTA's counts: the first digit's in kCopies interleaved copies (a warp's lanes spread over them, since
-    // weights crowd into few exponents), then the other digits'
-    uint32_t hist0[kBins * kCopies];
-    uint32_t hist[3][kBins];
+    // this CTA's counts: the first digit's, a copy per lane; then the other two digits', in the same place
+    union {
+        uint32_t lanes[kBins0][32];
+        uint32_t hist[2][kBins];
+    };
+    uint32_t hist0[kBins0];        // the first digit's, summed over the lanes
     uint32_t warp_sum[kSelWarps], wgt[kSelWarps], weq[kSelWarps];
-    uint32_t digit, above;         // the digit found, tokens above it
+    uint32_t digit, above, at;     // the digit found, tokens above it and at it, in the row
+    uint32_t slice;                // this CTA's slice of the row's histogram: all of its tokens
     uint32_t gt, eq;               // this CTA's tokens above / at the last kept key
 };
+static_assert(sizeof(uint32_t) * kBins0 * 32 == sizeof(uint32_t) * 2 * kBins, "one region");
 constexpr int kSelBase = (sizeof(SelSmem) + 15) / 16 * 16;
-constexpr int kRowHist = 3 * kBins * 4;   // in a cluster: the whole row's histograms, on rank 0
-constexpr int sel_keys_at(int cluster) { return kSelBase + (cluster > 1 ? kRowHist : 0); }
+// in a cluster, behind it: this CTA's slice of the row's histogram; then the keys
+constexpr int sel_keys_at(int cluster) { return kSelBase + (cluster > 1 ? kBins / cluster * 4 : 0); }
 
 // sum of one value per warp over the warps below `upto`
 __device__ __forceinline__ uint32_t sum_below(const uint32_t *per_warp, int upto, int lane) {
     return __reduce_add_sync(0xffffffffu, lane < upto ? per_warp[lane] : 0u);
 }
 
-// Counts one key per lane that is `in`: one add for the whole warp where many of its keys share a bin (equal weights).
-__device__ __forceinline__ void count(uint32_t *hist, uint32_t bin, bool in, int lane) {
+// Counts one key per lane that is `in`: one add for the whole warp where its keys share a bin.
+__device__ __forceinline__ void count_crowded(uint32_t *hist, uint32_t bin, bool in, int lane) {
     const uint32_t act = __ballot_sync(0xffffffffu, in);
-    if (__popc(act) >= 8) {
-        const uint32_t b0 = __shfl_sync(0xffffffffu, bin, __ffs(act) - 1);
-        if (__all_sync(0xffffffffu, !in || bin == b0)) {
-            if (lane == 0) atomicAdd(hist + b0, (uint32_t)__popc(act));
-            return;
-        }
+    if (!act) return;
+    const uint32_t b0 = __shfl_sync(0xffffffffu, bin, __ffs(act) - 1);
+    if (__all_sync(0xffffffffu, !in || bin == b0)) {
+        if (lane == 0) atomicAdd(hist + b0, (uint32_t)__popc(act));
+    } else if (in) {
+        atomicAdd(hist + bin, 1u);
     }
-    if (in) atomicAdd(hist + bin, 1u);
 }
 
 // kC: CTAs per cluster
@@ -114,17 +118,13 @@ template <int kC>
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __grid_constant__ EvictParams p) {
     extern __shared__ __align__(16) uint8_t sel_smem[];
     SelSmem &s = *reinterpret_cast<SelSmem *>(sel_smem);
-    uint32_t *row_hist = reinterpret_cast<uint32_t *>(sel_smem + kSelBase);
+    uint32_t *row_slice = reinterpret_cast<uint32_t *>(sel_smem + kSelBase);
     uint32_t *keys = reinterpret_cast<uint32_t *>(sel_smem + sel_keys_at(kC));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = kC > 1 ? (int)cluster_ctarank() : 0;
     const int row = blockIdx.x / kC, b = row / p.H_kv, h = row - b * p.H_kv;
-    static_assert(offsetof(SelSmem, hist) == sizeof(s.hist0), "cleared as one");
-    for (int i = tid; i < (kCopies + 3) * kBins / 4; i += kSelThreads)
-        reinterpret_cast<uint4 *>(s.hist0)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (kC > 1)
-        for (int i = tid; i < kRowHist / 16; i += kSelThreads)
-            reinterpret_cast<uint4 *>(row_hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < kBins0 * 32 / 4; i += kSelThreads)
+        reinterpret_cast<uint4 *>(&s.lanes[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
     pdl_wait();
     pdl_launch_dependents();
 
@@ -158,38 +158,52 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
     // kBatch pages, then their weights: two latencies for kBatch * kSelThreads keys
     constexpr int kBatch = 8;
     const int nc = min(n, kKeyCap);
+    const int head = h * p.page_size, page_stride = p.H_kv * p.page_size;
     for (int i0 = 0; i0 < nc; i0 += kBatch * kSelThreads) {
-        int page[kBatch];
+        int page[kBatch], slot[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int i = min(i0 + u * kSelThreads + tid, nc - 1);
-            page[u] = __ldg(table + page_index(t0 + i, p.page_size, p.log2_page));
+            const int t = t0 + min(i0 + u * kSelThreads + tid, nc - 1);
+            const int pi = page_index(t, p.page_size, p.log2_page);
+            slot[u] = t - pi * p.page_size;
+            page[u] = __ldg(table + pi);
         }
         float w[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int t = t0 + min(i0 + u * kSelThreads + tid, nc - 1);
-            const int slot = t - page_index(t, p.page_size, p.log2_page) * p.page_size;
-            const bool ok = page[u] >= 0 && page[u] < p.num_pages;
-            w[u] = ok ? __ldg(p.weights + ((int64_t)page[u] * p.H_kv + h) * p.page_size + slot) : 0.f;
-            if (!ok) page[u] = -1;
+            const bool ok = (uint32_t)page[u] < (uint32_t)p.num_pages;
+            w[u] = __ldg(p.weights + (int64_t)(ok ? page[u] : 0) * page_stride + (head + slot[u]));
+            if (!ok) slot[u] = -1;
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int i = i0 + u * kSelThreads + tid;
-            if (i0 + u * kSelThreads >= nc) break;
-            const uint32_t k = page[u] < 0 ? 0u : key_of(w[u]);
             if (i < nc) {
+                uint32_t k = key_of(w[u]);
+                if (slot[u] < 0) {
+                    k = 0u;
+                    if (p.error) atomicOr(p.error, DA_DEV_BAD_PAGE);
+                }
                 keys[i] = k;
-                if (page[u] < 0 && p.error) atomicOr(p.error, DA_DEV_BAD_PAGE);
+                atomicAdd(&s.lanes[k >> 24][lane], 1u);
             }
-            count(s.hist0 + (lane & (kCopies - 1)), (k >> 21) * kCopies, i < nc, lane);
         }
     }
-    for (int i0 = nc; i0 < n; i0 += kSelThreads) {  // keys beyond shared memory
-        const int i = i0 + tid;
-        count(s.hist0 + (lane & (kCopies - 1)), i < n ? (weight_key(p, table, h, t0 + i) >> 21) * kCopies : 0u, i < n, lane);
+    for (int i = nc + tid; i < n; i += kSelThreads)  // keys beyond shared memory
+        atomicAdd(&s.lanes[weight_key(p, table, h, t0 + i) >> 24][lane], 1u);
+    __syncthreads();
+    {   // two threads a bin, each half of the lanes, starting at different ones
+        const int bin = tid >> 1, half = (tid & 1) * 16;
+        uint32_t c = 0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) c += s.lanes[bin][half + ((k + bin) & 15)];
+        c += __shfl_xor_sync(0xffffffffu, c, 1);
+        if (!(tid & 1)) s.hist0[bin] = c;
+        static_assert(kSelThreads == 2 * kBins0, "two threads a bin");
     }
+    __syncthreads();
+    for (int i = tid; i < 2 * kBins / 4; i += kSelThreads)
+        reinterpret_cast<uint4 *>(&s.hist[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     // keys i .. i + 3 (i a multiple of 4); what lies past n is not a key
     auto keys4 = [&](int i, uint32_t(&k)[4]) {
@@ -202,59 +216,86 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
         }
     };
 
-    // digits of 11, 11 and 10 bits, highest first
-    uint32_t prefix = 0, mask = 0, local_above = 0;
+    // digits of 8, 12 and 12 bits, highest first
+    uint32_t prefix = 0, mask = 0, local_above = 0, at = (uint32_t)M;
 #pragma unroll
     for (int d = 0; d < 3; ++d) {
-        const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
-        const int bins = d == 2 ? 1024 : kBins;
-        uint32_t *hist = s.hist[d];
+        const int shift = d == 0 ? 24 : d == 1 ? 12 : 0;
+        const int bins = d == 0 ? kBins0 : kBins;
+        uint32_t *hist = d == 0 ? s.hist0 : s.hist[d - 1];
         if (d > 0) {
+            const bool crowded = at > (uint32_t)M / 2;  // most keys are in the bins found so far
             for (int i0 = 4 * (tid - lane); i0 < n; i0 += 4 * kSelThreads) {
                 const int i = i0 + 4 * lane;
                 uint32_t k[4] = {0u, 0u, 0u, 0u};
                 if (i < n) keys4(i, k);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) count(hist, (k[u] >> shift) & (bins - 1), i + u < n && (k[u] & mask) == prefix, lane);
+                for (int u = 0; u < 4; ++u) {
+                    const bool in = i + u < n && (k[u] & mask) == prefix;
+                    const uint32_t bin = (k[u] >> shift) & (bins - 1);
+                    if (crowded)
+                        count_crowded(hist, bin, in, lane);
+                    else if (in)
+                        atomicAdd(hist + bin, 1u);
+                }
             }
             __syncthreads();
         }
-        // four bins a thread, from the top
-        const int base = bins - 4 * (tid + 1);
-        uint32_t c[4] = {0u, 0u, 0u, 0u};
-        if (base >= 0) {
-            if (d == 0) {
-                static_assert(kCopies == 4, "one 16-byte vector of copies per bin");
+        // the row's counts: kPer bins a thread, from the top of the bins, or in a cluster of the slice of them that
+        // holds the digit
+        constexpr int kPer = kC == 1 ? 8 : 4;
+        const int slice = bins / kC;
+        const int base = slice - kPer * (tid + 1);
+        uint32_t c[kPer], first_bin = 0, over = 0;       // over: tokens above the slice
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(s.hist0 + (base + i) * kCopies);
-                    c[i] = v.x + v.y + v.z + v.w;
+        for (int i = 0; i < kPer; ++i) c[i] = 0u;
+        auto put = [&](int i, uint4 q) { c[i] = q.x, c[i + 1] = q.y, c[i + 2] = q.z, c[i + 3] = q.w; };
+        if constexpr (kC == 1) {
+            if (base >= 0) {
+                put(0, *reinterpret_cast<const uint4 *>(hist + base));
+                put(kPer - 4, *reinterpret_cast<const uint4 *>(hist + base + kPer - 4));
+            }
+        } else {
+            __syncwarp();
+            cluster_sync_all();  // every CTA's counts
+            // this CTA adds up its slice of all CTAs' bins
+            uint32_t sum = 0;
+            if (4 * tid < slice) {
+                const uint32_t a = smem_u32(hist + rank * slice + 4 * tid);
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int r = 0; r < kC; ++r) {
+                    const uint4 x = ld_cluster_v4(mapa_shared(a, r));
+                    q.x += x.x, q.y += x.y, q.z += x.z, q.w += x.w;
                 }
-                if (kC > 1) *reinterpret_cast<uint4 *>(hist + base) = make_uint4(c[0], c[1], c[2], c[3]);
-            } else {
-                const uint4 v = *reinterpret_cast<const uint4 *>(hist + base);
-                c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
+                *reinterpret_cast<uint4 *>(row_slice + 4 * tid) = q;
+                sum = q.x + q.y + q.z + q.w;
             }
-        }
-        if (kC > 1) {
-            // the whole row's counts: every CTA adds its bins that are not empty to rank 0's, then reads the sums
-            __syncwarp();
-            if (d == 0) cluster_sync_all();  // rank 0's memory is there, and clear
-            const uint32_t a = mapa_shared(smem_u32(row_hist + d * kBins + max(base, 0)), 0);
-            if (base >= 0) {
+            sum = __reduce_add_sync(0xffffffffu, sum);
+            if (lane == 0) s.wgt[warp] = sum;
+            __syncthreads();
+            if (warp == 0) {
+                sum = sum_below(s.wgt, kSelWarps, lane);
+                if (lane == 0) s.slice = sum;
+                __syncwarp();
+            }
+            cluster_sync_all();  // every CTA's slice
+            uint32_t all = 0, mine = 0;                  // lane r: tokens of rank r's slice, and of those above it
+            if (lane < kC) mine = ld_cluster_u32(mapa_shared(smem_u32(&s.slice), lane));
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c[i]) red_cluster_add(a + 4 * i, c[i]);
+            for (int r = 0; r < kC; ++r) {
+                const uint32_t x = __shfl_sync(0xffffffffu, mine, r);
+                all += r > lane ? x : 0u;
             }
-            __syncwarp();
-            cluster_sync_all();
-            if (base >= 0) {
-                const uint4 v = ld_cluster_v4(a);
-                c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
-            }
+            const int owner = __ffs(__ballot_sync(0xffffffffu, lane < kC && all < want && want <= all + mine)) - 1;
+            over = __shfl_sync(0xffffffffu, all, owner);
+            first_bin = owner * slice;
+            if (base >= 0) put(0, ld_cluster_v4(mapa_shared(smem_u32(row_slice + base), owner)));
         }
-        const uint32_t mine4 = c[0] + c[1] + c[2] + c[3];
-        uint32_t v = mine4;
+        uint32_t mine8 = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) mine8 += c[i];
+        uint32_t v = mine8;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
@@ -262,13 +303,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
         }
         if (lane == 31) s.warp_sum[warp] = v;
         __syncthreads();
-        uint32_t above = sum_below(s.warp_sum, warp, lane) + v - mine4;   // tokens above this thread's bins
+        uint32_t above = over + sum_below(s.warp_sum, warp, lane) + v - mine8;   // tokens above this thread's bins
         if (base >= 0) {
 #pragma unroll
-            for (int i = 3; i >= 0; --i) {
+            for (int i = kPer - 1; i >= 0; --i) {
                 if (above < want && want <= above + c[i]) {
-                    s.digit = base + i;
+                    s.digit = first_bin + base + i;
                     s.above = above;
+                    s.at = c[i];
                 }
                 above += c[i];
             }
@@ -276,6 +318,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
         __syncthreads();
         const uint32_t digit = s.digit;
         want -= s.above;
+        at = s.at;
         if (kC > 1) {  // this CTA's tokens above the digit
             uint32_t mine = 0;
             for (int i = digit + 1 + tid; i < bins; i += kSelThreads) mine += hist[i];
@@ -287,8 +330,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
                 s.gt = local_above;
                 s.eq = hist[digit];
             }
-            __syncthreads();  // s.wgt is written again
         }
+        __syncthreads();  // s.digit and s.wgt are written again
         prefix |= digit << shift;
         mask |= (uint32_t)(bins - 1) << shift;
     }
