@@ -289,7 +289,7 @@ typedef struct {
  * pass through. (No counterpart on the source pages, which append finished
  * rows.)
  *   desc: as for decode_attn_append_kv, and G (H_q = H_kv * G).
- *   n_tokens: N >= 0 (0: nothing is launched). Token n belongs to request
+ *   n_tokens: N in [0, 2^30] (0: nothing is launched). Token n belongs to request
  *     requests[n]; requests = NULL: to request n / s_q, and N must be B * s_q.
  *   q: bf16, token n's [H_q][D_qk] at q + n * q_stride. k_new, v_new: likewise
  *     [H_kv][D]; on the 656-byte format k_new holds the 576 values of the latent
@@ -302,8 +302,8 @@ typedef struct {
  *     in its request's cache (slot t % page_size of page block_table[b][t /
  *     page_size]); negative: the token is skipped, its q_out row left as it was.
  *   q_out: bf16 [N][H_q][D_qk], the q of decode_attn_fwd when the tokens come
- *     request by request. It may be q itself (packed rows); else the two must
- *     not overlap (DA_ERR_UNSUPPORTED).
+ *     request by request. It may be q itself (packed rows); else it must not
+ *     overlap q, k_new or v_new (DA_ERR_UNSUPPORTED).
  *   k_pool, v_pool, k_scale, v_scale, device_error: as for decode_attn_append_kv.
  *     Besides its bits, DA_DEV_BAD_REQUEST; such a token's q is still rotated.
  * Products and sums are fp32; each value is rounded once, K to the pool's format
@@ -338,8 +338,9 @@ int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_
  *     start from 0, whatever their slot held.
  *   decay: finite, >= 0.
  *   weights: device fp32 [num_pages][H_kv][page_size], written in place; only
- *     slots of tokens t < L_b change. A page that two requests share would be
- *     updated by both: give every request pages of its own.
+ *     slots of tokens t < L_b change. A page that two requests share, or that
+ *     one lists twice, would be updated twice at once: give every request pages of
+ *     its own.
  * A query row whose lse is -inf adds nothing. Each weight is summed in fp32 in
  * a fixed order. Launches one kernel on `stream`. No allocation, no sync.
  */

@@ -357,7 +357,7 @@ def verify_drafts(target_probs, draft_probs, draft_tokens, uniform, num_accepted
     K = rows - 1
     kind = {torch.float32: PROB_F32, torch.bfloat16: PROB_BF16, torch.float16: PROB_F16}.get(dtype, -1)
     tp, ts = _prob_rows(dev, "target_probs", target_probs, dtype, (B, rows, V))
-    dp, ds = (None, 0) if draft_probs is None else _prob_rows(dev, "draft_probs", draft_probs, dtype, (B, K, V))
+    dp, ds = (None, 0) if draft_probs is None or K == 0 else _prob_rows(dev, "draft_probs", draft_probs, dtype, (B, K, V))
     _check((lib or load_library()).decode_attn_verify_drafts(
         B, K, V, kind, tp, ts, dp, ds, _opt(dev, "draft_tokens", draft_tokens, i32, (B, K)),
         _need(dev, "uniform", uniform, torch.float32, (B, rows)), _opt(dev, "cache_seqlens", cache_seqlens, i32, (B,)),

@@ -576,7 +576,7 @@ int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_
     int rc = check_pool_desc(desc, &row_len);
     if (rc) return rc;
     const bool mla = is_mla(desc);
-    if (desc->G < 1 || desc->G > 1024 || n_tokens < 0 || desc->s_q < 0 || desc->s_q > 64) return DA_ERR_DIMS;
+    if (desc->G < 1 || desc->G > 1024 || n_tokens < 0 || n_tokens > (1 << 30) || desc->s_q < 0 || desc->s_q > 64) return DA_ERR_DIMS;
     const int64_t H_q = (int64_t)desc->H_kv * desc->G, q_len = H_q * desc->D_qk;
     if (rope->rot_dim < 16 || rope->rot_dim % 16 != 0 || rope->rot_dim > 512 || rope->rot_dim > (mla ? 64 : desc->D_qk) ||
         rope->n_axes < 1 || rope->n_axes > 4)
@@ -606,14 +606,16 @@ int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_
         if (!k_scale || !v_scale) return DA_ERR_SCALE;
         if (!aligned4(k_scale) || !aligned4(v_scale)) return DA_ERR_ALIGN;
     }
-    // q_out is q, row for row, or does not touch it
+    // q_out is q, row for row, or touches no input (byte ranges from the first row's start to the last row's end)
     const bool in_place = q == q_out && q_stride == q_len;
-    if (!in_place) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(q), b = reinterpret_cast<uintptr_t>(q_out);
-        const uint64_t a_len = 2ull * ((uint64_t)(n_tokens - 1) * q_stride + q_len), b_len = 2ull * n_tokens * q_len;
-        // byte ranges from the first row's start to the last row's end
-        if (a < b + b_len && b < a + a_len) return DA_ERR_UNSUPPORTED;
-    }
+    const auto touches = [&](const void *rows, int64_t stride, int64_t len) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(rows), b = reinterpret_cast<uintptr_t>(q_out);
+        const uint64_t a_len = 2 * ((uint64_t)(n_tokens - 1) * stride + len), b_len = 2 * (uint64_t)n_tokens * q_len;
+        return a < b + b_len && b < a + a_len;
+    };
+    if ((!in_place && touches(q, q_stride, q_len)) || touches(k_new, k_stride, row_len) ||
+        (v_new && touches(v_new, v_stride, row_len)))
+        return DA_ERR_UNSUPPORTED;
     const int sms = current_sms();
     if (!sms) return DA_ERR_CUDA;
     RopeParams p = {};

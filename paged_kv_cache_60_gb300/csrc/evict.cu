@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
     // kBatch pages, then their weights: two latencies for kBatch * kSelThreads keys
     constexpr int kBatch = 8;
     const int nc = min(n, kKeyCap);
-    const int head = h * p.page_size, page_stride = p.H_kv * p.page_size;
+    const int64_t page_stride = (int64_t)p.H_kv * p.page_size;
+    const float *head = p.weights + (int64_t)h * p.page_size;
     for (int i0 = 0; i0 < nc; i0 += kBatch * kSelThreads) {
         int page[kBatch], slot[kBatch];
 #pragma unroll
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const bool ok = (uint32_t)page[u] < (uint32_t)p.num_pages;
-            w[u] = __ldg(p.weights + (int64_t)(ok ? page[u] : 0) * page_stride + (head + slot[u]));
+            w[u] = __ldg(head + (ok ? page[u] : 0) * page_stride + slot[u]);
             if (!ok) slot[u] = -1;
         }
 #pragma unroll
@@ -517,7 +518,9 @@ cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream,
     if (tiles * p.B > INT32_MAX) return cudaErrorInvalidConfiguration;
     cfg.gridDim = dim3((unsigned)(tiles * p.B));
     cfg.blockDim = dim3(kCopyThreads);
-    cfg.dynamicSmemBytes = (size_t)tile * p.H_kv * 16;
+    cfg.dynamicSmemBytes = (size_t)tile * p.H_kv * 16;  // 64 KB at most (one token of 4096 heads)
+    e = cudaFuncSetAttribute(evict_copy_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10);
+    if (e != cudaSuccess) return e;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -36,7 +36,7 @@ def _rope(rot=128, sections=(64,), **kw):
 
 
 def test_rope_append_refusals(lib):
-    def call(d, r=None, n=4, q=G, qs=0, k=G, ks=0, v=G, vs=0, freq=G, at=G, req=G, pos=G, bt=G, out=P(0x900000), kp=G, vp=G,
+    def call(d, r=None, n=4, q=G, qs=0, k=P(0x300000), ks=0, v=P(0x400000), vs=0, freq=G, at=G, req=G, pos=G, bt=G, out=P(0x900000), kp=G, vp=G,
              sk=None, sv=None, err=None):
         return lib.decode_attn_rope_append(ctypes.byref(d), ctypes.byref(r or _rope()), n, q, qs, k, ks, v, vs, freq, at, req,
                                            pos, bt, out, kp, vp, sk, sv, err, None)
@@ -46,7 +46,7 @@ def test_rope_append_refusals(lib):
         off = 8 if name in ("q", "k", "v", "out", "kp", "vp") else 2
         assert call(d, **{name: P(0x900000 + off)}) == -4, name
     assert call(d, req=P(0x100002)) == -4 and call(d, err=P(0x100002)) == -4
-    assert call(d, n=-1) == -2
+    assert call(d, n=-1) == -2 and call(d, n=(1 << 30) + 1) == -2
     assert call(d, n=0) == 0 and call(d, n=0, q=None, out=None) == 0          # nothing to do
     assert call(d, req=None, n=5) == -2                                       # not B * s_q tokens
     for bad in (_rope(8, (4,)), _rope(24, (12,)), _rope(144, (72,)), _rope(64, (30,)), _rope(64, (40, -8)),
@@ -60,6 +60,7 @@ def test_rope_append_refusals(lib):
     assert call(_desc(kv_dtype=da.KV_FP8)) == -8 and call(_desc(kv_dtype=da.KV_FP8), sk=G, sv=P(0x100002)) == -4
     # q_out is q row for row, or apart from it
     assert call(d, out=P(0x100000 + 2 * 128)) == -3 and call(d, out=G, qs=2 * 8 * 128 * 2) == -3
+    assert call(d, out=P(0x300000 - 0x1000)) == -3 and call(d, out=P(0x400000 + 2 * 4 * 256 - 16)) == -3
     m = _latent()
     assert call(m, _rope(64, (32,))) == -3                                    # no v_new
     assert call(m, _rope(128, (64,)), v=None, vp=None) == -2                  # more than the 64 RoPE values

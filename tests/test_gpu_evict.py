@@ -125,6 +125,13 @@ def test_the_other_tokens_of_a_shared_page_stay():
     c.check()
 
 
+def test_odd_pages_and_many_heads():
+    """Pages of any size, and as many heads as the library takes (one token a copy tile)."""
+    Case(BF16, 2, 64, 3, [50, 7, 31], 11, 1, 2, seed=20).check()
+    Case(FP8, 3, 16, 7, [300], 123, seed=21).check()
+    Case(BF16, 4096, 8, 2, [5, 3], 3, 1, 1, seed=22).check()
+
+
 def test_captured_replayed_other_stream_and_repeated():
     c = Case(BF16, 4, 64, 16, [300, 20, 150], 64, 2, 8, seed=12)
     t = c.tensors()

@@ -171,6 +171,7 @@ SHAPES = [
     (BF16, 2, 9, 1, 1, 72, 64, [8], 16),
     (BF16, 2, 33, 1, 3, 256, 192, [40, 0, 24, 64], 256),
     (BF16, 4, 700, 1, 8, 64, 16, [10, 6], 32),
+    (BF16, 2, 40, 2, 2, 64, 5, [32], 64),
     (FP8, 3, 50, 4, 8, 128, 32, [24, 20, 20], 128),
     (FP8, 2, 31, 1, 2, 72, 16, [3, 2, 3], 16),
     (FP8, 2, 300, 2, 8, 64, 64, [16], 32),

@@ -169,6 +169,12 @@ def test_lengths_in_place_and_left_out():
     t2 = c.tensors()
     da.verify_drafts(t2["p"], t2["q"], t2["x"], t2["u"], t2["a"], t2["out"])
     assert torch.equal(t2["out"], t["out"]) and (t2["new"] == -7).all()
+    none = torch.empty(5, 0, 600, device="cuda")           # no drafts: their tensors may be empty ones
+    one = (t["p"][:, :1].contiguous(), none, torch.empty(5, 0, dtype=torch.int32, device="cuda"), t["u"][:, :1].contiguous())
+    a, b = [torch.full((5, 1), -7, dtype=torch.int32, device="cuda") for _ in range(2)]
+    da.verify_drafts(*one, t2["a"], a)
+    da.verify_drafts(one[0], None, None, one[3], t2["a"], b)
+    assert torch.equal(a, b) and (a >= 0).all() and (t2["a"] == 0).all()
     with pytest.raises(da.DecodeAttnError):
         da.verify_drafts(t["p"].double(), t["q"], t["x"], t["u"], t["a"], t["out"])
     with pytest.raises(da.DecodeAttnError):
