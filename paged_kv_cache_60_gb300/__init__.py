@@ -138,13 +138,14 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
+    """The stream's handle; None: the current stream (of device ``dev``, if the caller has looked it up)."""
     import torch
     if stream is None:
         # the handle alone: building a Stream object costs more than a small call's launch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and torch.cuda.is_initialized():
-            return ctypes.c_void_p(raw(torch.cuda.current_device()))
+        if raw is not None and (dev is not None or torch.cuda.is_initialized()):
+            return raw(torch.cuda.current_device() if dev is None else dev) or None
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -229,11 +230,11 @@ def _device():
 
 def _need(dev, name, t, dtype, shape=None):
     """A contiguous tensor of this dtype (and shape) on device ``dev``; its address."""
-    if not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape)):
-        want = "" if shape is None else f" of shape {tuple(shape)}"
-        raise DecodeAttnError(f"{name}: want a contiguous {dtype} tensor{want} on the current CUDA device, "
-                              f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
+    want = "" if shape is None else f" of shape {tuple(shape)}"
+    raise DecodeAttnError(f"{name}: want a contiguous {dtype} tensor{want} on the current CUDA device, "
+                          f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
 
 def _opt(dev, name, t, dtype, shape=None):
@@ -286,7 +287,7 @@ def rope_append(desc: Desc, rope: Rope, q, k_new, v_new, inv_freq, rope_position
         _need(dev, "block_table", block_table, i32, (desc.B, desc.max_pages_per_seq)),
         _need(dev, "q_out", q_out, bf16), _pool(dev, "k_pool", k_pool, desc),
         None if v_pool is None else _pool(dev, "v_pool", v_pool, desc), _opt(dev, "k_scale", k_scale, f32, heads),
-        _opt(dev, "v_scale", v_scale, f32, heads), _opt(dev, "device_error", device_error, i32), _stream(stream)))
+        _opt(dev, "v_scale", v_scale, f32, heads), _opt(dev, "device_error", device_error, i32), _stream(stream, dev)))
 
 
 def accum_weights(desc: Desc, q, k_pool, k_scale, block_table, cache_seqlens, meta, lse, weights, num_accepted=None,
@@ -309,7 +310,7 @@ def accum_weights(desc: Desc, q, k_pool, k_scale, block_table, cache_seqlens, me
         _need(dev, "cache_seqlens", cache_seqlens, i32, (B,)), _need(dev, "meta", meta, meta.dtype),
         meta.numel() * meta.element_size(), _need(dev, "lse", lse, f32),
         _opt(dev, "num_accepted", num_accepted, i32, (B,)), _opt(dev, "weighted_lens", weighted_lens, i32, (B,)),
-        decay, _need(dev, "weights", weights, f32, (desc.num_pages, desc.H_kv, desc.page_size)), _stream(stream)))
+        decay, _need(dev, "weights", weights, f32, (desc.num_pages, desc.H_kv, desc.page_size)), _stream(stream, dev)))
 
 
 def evict(desc: Desc, budget, cache_seqlens, block_table, dst_block_table, k_pool, v_pool, weights, kept, new_seqlens,
@@ -328,7 +329,7 @@ def evict(desc: Desc, budget, cache_seqlens, block_table, dst_block_table, k_poo
         _pool(dev, "k_pool", k_pool, desc), None if v_pool is None else _pool(dev, "v_pool", v_pool, desc),
         _need(dev, "weights", weights, torch.float32, (desc.num_pages, desc.H_kv, desc.page_size)),
         _need(dev, "kept", kept, i32, (B, desc.H_kv, budget)), _need(dev, "new_seqlens", new_seqlens, i32, (B,)),
-        _opt(dev, "device_error", device_error, i32), _stream(stream)))
+        _opt(dev, "device_error", device_error, i32), _stream(stream, dev)))
 
 
 def _prob_rows(dev, name, t, dtype, shape):
@@ -363,7 +364,7 @@ def verify_drafts(target_probs, draft_probs, draft_tokens, uniform, num_accepted
         _need(dev, "uniform", uniform, torch.float32, (B, rows)), _opt(dev, "cache_seqlens", cache_seqlens, i32, (B,)),
         _need(dev, "num_accepted", num_accepted, i32, (B,)), _need(dev, "out_tokens", out_tokens, i32, (B, rows)),
         _opt(dev, "new_seqlens", new_seqlens, i32, (B,)), _opt(dev, "device_error", device_error, i32),
-        _stream(stream)))
+        _stream(stream, dev)))
 
 
 def get_error(meta, stream=None) -> int:
