@@ -30,40 +30,40 @@
 namespace da {
 namespace {
 
-// NQ: query tokens held in registers
-template <int D, bool FP8, int NQ>
+// NQ: query tokens held in registers. HP: KV heads of a CTA (neighbours, whose rows lie side by side).
+template <int D, bool FP8, int NQ, int HP>
 struct AccumCfg {
     static constexpr int ROW = D * (FP8 ? 1 : 2);      // bytes of one token's head
-    static constexpr int NX = ROW / 128;
+    static constexpr int SROW = ROW * HP;              // bytes of one token in a stage
+    static constexpr int NX = SROW / 128;
     static constexpr int KS = D / 16;                  // MMA steps
-    static constexpr int STAGE = kChunk * ROW;
+    static constexpr int STAGE = kChunk * SROW;
     // Consumer warps, and stages (a multiple, so that a stage always belongs to one warp): 192 KB in flight on an SM. A
-    // producer warp issues a chunk in about 0.35 us, which 16 KB chunks (bf16, D = 128) hide behind HBM; 8 KB chunks
-    // take two CTAs, and so two producers, per SM (e4m3: 174 us against 307 with one CTA of twelve consumer warps, for
-    // 64 x 32768 tokens of 4 heads).
-    static constexpr int NCW = 6;
-    static constexpr int NS = 2 * NCW;
-    static constexpr int MIN_BLOCKS = ROW == 128 ? 2 : 1;
+    // producer warp issues a chunk in about 0.35 us, which 16 KB chunks hide behind HBM; the builds with 8 KB chunks
+    // take two CTAs, and so two producers, per SM. Rows of 128 bytes are best taken two heads at a time: the CTAs of
+    // the heads drift apart, and DRAM then sees 128-byte reads 128 H_kv bytes apart (64 x 32768 e4m3 tokens of 4 heads,
+    // three pools in turn: 181 us against 212 with one head to a CTA).
+    static constexpr int NCW = HP == 2 ? 12 : 6;
+    static constexpr int NS = HP == 2 ? NCW : 2 * NCW;
+    static constexpr int MIN_BLOCKS = SROW == 128 ? 2 : 1;
     static constexpr int THREADS = (NCW + 1) * 32;
     static constexpr int TT = NQ == 1 ? 4 : NQ == 2 ? 2 : 1;   // tiles whose scores are in registers at a time
     static constexpr int OFF_BAR = NS * STAGE;
-    static constexpr int OFF_PAGE = OFF_BAR + 2 * NS * 8;
-    static constexpr int OFF_FLAG = OFF_PAGE + NS * 8 * 4;
+    static constexpr int OFF_FLAG = OFF_BAR + 2 * NS * 8;
     static constexpr int SMEM = OFF_FLAG + 16 + 1024;  // + alignment slack
 };
 
-template <int D, bool FP8, int NQ>
-__global__ void __launch_bounds__(AccumCfg<D, FP8, NQ>::THREADS, AccumCfg<D, FP8, NQ>::MIN_BLOCKS)
+template <int D, bool FP8, int NQ, int HP>
+__global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D, FP8, NQ, HP>::MIN_BLOCKS)
     accum_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ AccumParams p) {
-    using C = AccumCfg<D, FP8, NQ>;
+    using C = AccumCfg<D, FP8, NQ, HP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *empty = full + C::NS;
-    int32_t *pages = reinterpret_cast<int32_t *>(smem + C::OFF_PAGE);   // [stage][box]: the box's page, -1: none
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y, Z = gridDim.z;
+    const int h = blockIdx.y * HP, Z = gridDim.z;   // (first of) this CTA's KV head(s)
     // this CTA's parts, one after the other through the same ring
     const int part0 = blockIdx.x * p.parts_per_cta, part1 = min(part0 + p.parts_per_cta, p.num_parts);
 
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ>::THREADS, AccumCfg<D, FP8
         const int nb = p.boxes_per_chunk, bt = p.box_tokens, P = p.page_size;
         if (lane >= nb) return;
         const uint64_t pol = policy_evict_first();
-        const uint32_t box_bytes = (uint32_t)bt * C::ROW;
+        const uint32_t box_bytes = (uint32_t)bt * C::SROW;
         bool aborted = false;
         while (!aborted && next_segment()) {
             const int32_t *table = p.block_table + (size_t)sg.b * p.max_pages;
@@ -152,8 +152,7 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ>::THREADS, AccumCfg<D, FP8
                         p.meta.header[kHErrorDetail] = pg;
                         pg = -2;  // skipped: its rows keep stale bytes, its weights stay
                     }
-                    pages[stage * 8 + lane] = pg < 0 ? -1 : pg;
-                    mbar_arrive_expect_tx(&full[stage], pg < 0 ? 0u : box_bytes);  // (releases the page id too)
+                    mbar_arrive_expect_tx(&full[stage], pg < 0 ? 0u : box_bytes);
                     if (pg >= 0) {
                         const int tok = c * kChunk + lane * bt;
                         const int in_page = (P > kChunk) ? (tok % P) : 0;
@@ -173,8 +172,9 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ>::THREADS, AccumCfg<D, FP8
 
     // ---------------------------------------------------------------- consumers
     const int r8 = lane >> 2, c4 = lane & 3, lrow = lane & 7, lmat = lane >> 3;
-    const float sl2 = p.scale_log2 * (FP8 ? __ldg(p.k_scale + h) : 1.f);
-    const int lbt = p.log2_box_tokens;
+    float sl2[HP];
+#pragma unroll
+    for (int e = 0; e < HP; ++e) sl2[e] = p.scale_log2 * (FP8 ? __ldg(p.k_scale + h + e) : 1.f);
     // tokens whose weights this lane updates: 16 c4 + r8 of a chunk, and the eighth one after it
     const int own = 16 * c4 + r8;
     while (next_segment()) {
@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ>::THREADS, AccumCfg<D, FP8
             continue;
         }
         // q: B fragments, n = query head r8; lse of the two heads whose scores this lane gets
-        uint32_t qf[C::KS][NQ][2];
-        float lse2[NQ][2];
+        uint32_t qf[HP][C::KS][NQ][2];
+        float lse2[HP][NQ][2];
         int last[NQ];  // last token that query token j sees, -1 where it does not count
         const int acc = p.accepted ? p.accepted[b] : p.s_q - 1;
         const int wl = p.weighted ? p.weighted[b] : L;
@@ -197,36 +197,68 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ>::THREADS, AccumCfg<D, FP8
         for (int j = 0; j < NQ; ++j) {
             const bool on = j < p.s_q && j <= acc;
             last[j] = on ? L - p.s_q + j : -1;
-            lse2[j][0] = lse2[j][1] = 0.f;
-            if (!on) {
 #pragma unroll
-                for (int ks = 0; ks < C::KS; ++ks) qf[ks][j][0] = qf[ks][j][1] = 0u;
-                continue;
-            }
-            const size_t head0 = ((size_t)b * p.s_q + j) * p.H_q + (size_t)h * 8;
-            const float2 ls = *reinterpret_cast<const float2 *>(p.lse + head0 + 2 * c4);
-            constexpr float kLog2e = 1.4426950408889634f;
-            lse2[j][0] = ls.x * kLog2e;
-            lse2[j][1] = ls.y * kLog2e;
-            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + (head0 + r8) * D;
-            if constexpr (!FP8) {
-                const uint32_t *q32 = reinterpret_cast<const uint32_t *>(q);
+            for (int e = 0; e < HP; ++e) {
+                lse2[e][j][0] = lse2[e][j][1] = 0.f;
 #pragma unroll
-                for (int ks = 0; ks < C::KS; ++ks) {
-                    qf[ks][j][0] = q32[ks * 8 + c4];
-                    qf[ks][j][1] = q32[ks * 8 + 4 + c4];
-                }
-            } else {
+                for (int ks = 0; ks < C::KS; ++ks) qf[e][ks][j][0] = qf[e][ks][j][1] = 0u;
+                if (!on) continue;
+                const size_t head0 = ((size_t)b * p.s_q + j) * p.H_q + (size_t)(h + e) * 8;
+                const float2 ls = *reinterpret_cast<const float2 *>(p.lse + head0 + 2 * c4);
+                constexpr float kLog2e = 1.4426950408889634f;
+                lse2[e][j][0] = ls.x * kLog2e;
+                lse2[e][j][1] = ls.y * kLog2e;
+                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + (head0 + r8) * D;
+                if constexpr (!FP8) {
+                    const uint32_t *q32 = reinterpret_cast<const uint32_t *>(q);
 #pragma unroll
-                for (int ks = 0; ks < C::KS; ++ks) {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(q + ks * 16 + c4 * 4);
-                    qf[ks][j][0] = pack_f16(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
-                    qf[ks][j][1] = pack_f16(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+                    for (int ks = 0; ks < C::KS; ++ks) {
+                        qf[e][ks][j][0] = q32[ks * 8 + c4];
+                        qf[e][ks][j][1] = q32[ks * 8 + 4 + c4];
+                    }
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ++ks) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(q + ks * 16 + c4 * 4);
+                        qf[e][ks][j][0] = pack_f16(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+                        qf[e][ks][j][1] = pack_f16(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+                    }
                 }
             }
         }
         const int i1 = i + n;
         int c = lcf + skip * Z;
+        // the weights that this lane updates, loaded a chunk ahead of their use, their pages two: they come from DRAM
+        // (217 -> 212 us on the largest e4m3 workload, one head to a CTA)
+        const int32_t *table = p.block_table + (size_t)b * p.max_pages;
+        const auto page_of = [&](int chunk, int k) -> int {
+            const int t = chunk * kChunk + own + 8 * k;
+            return chunk < sg.lc1 && t < L ? __ldg(table + (p.log2_page >= 0 ? t >> p.log2_page : t / p.page_size)) : -1;
+        };
+        const auto weight_at = [&](int chunk, int k, int pg) -> float * {
+            const int t = chunk * kChunk + own + 8 * k;
+            return (uint32_t)pg < (uint32_t)p.num_pages
+                       ? p.weights + ((size_t)pg * p.H_kv + h) * p.page_size +
+                             (p.log2_page >= 0 ? t & (p.page_size - 1) : t % p.page_size)
+                       : nullptr;
+        };
+        const int step = C::NCW * Z;
+        float *wp[2];           // the first head's; the next head's is a page of floats behind it
+        float old[HP][2];
+        int pg[2];
+        const auto old_of = [&](int chunk, int k, const float *w, float(&to)[HP][2]) {
+#pragma unroll
+            for (int e = 0; e < HP; ++e)
+                to[e][k] = w && chunk * kChunk + own + 8 * k < wl ? w[(size_t)e * p.page_size] : 0.f;
+        };
+#pragma unroll
+        for (int k = 0; k < 2; ++k) pg[k] = page_of(c, k);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            wp[k] = weight_at(c, k, pg[k]);
+            old_of(c, k, wp[k], old);
+            pg[k] = page_of(c + step, k);
+        }
         for (i += skip; i < i1; i += C::NCW, c += C::NCW * Z) {
             const int stage = i % C::NS;
             if (!mbar_wait_warp(&full[stage], (i / C::NS) & 1, abort_flag, p.wait_limit_ns)) {
@@ -237,115 +269,123 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ>::THREADS, AccumCfg<D, FP8
                 return;
             }
             const int t0 = c * kChunk;
-            // the old weights, loaded under the products
-            float *wp[2];
-            float old[2];
+            float *wp_next[2];
+            float old_next[HP][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const int u = own + 8 * k, t = t0 + u;
-                const int pg = pages[stage * 8 + (u >> lbt)];
-                const int slot = p.page_size > kChunk ? t % p.page_size : u & (p.page_size - 1);
-                wp[k] = t < L && pg >= 0 ? p.weights + ((size_t)pg * p.H_kv + h) * p.page_size + slot : nullptr;
-                old[k] = 0.f;
-                if (wp[k] && t < wl) old[k] = *wp[k];   // scaled at the end: nothing waits for it here
+                wp_next[k] = weight_at(c + step, k, pg[k]);
+                old_of(c + step, k, wp_next[k], old_next);
+                pg[k] = page_of(c + 2 * step, k);
             }
             const uint32_t s_base = smem_u32(smem + (size_t)stage * C::STAGE);
-            float add[2] = {0.f, 0.f};
+            float add[HP][2];
 #pragma unroll
-            for (int tt = 0; tt < 4; tt += C::TT) {
-                float s[C::TT][NQ][4];
+            for (int e = 0; e < HP; ++e) {
+                add[e][0] = add[e][1] = 0.f;
 #pragma unroll
-                for (int t = 0; t < C::TT; ++t)
+                for (int tt = 0; tt < 4; tt += C::TT) {
+                    float s[C::TT][NQ][4];
 #pragma unroll
-                    for (int j = 0; j < NQ; ++j) s[t][j][0] = s[t][j][1] = s[t][j][2] = s[t][j][3] = 0.f;
-                if constexpr (!FP8) {
+                    for (int t = 0; t < C::TT; ++t)
 #pragma unroll
-                    for (int ks = 0; ks < C::KS; ++ks)
+                        for (int j = 0; j < NQ; ++j) s[t][j][0] = s[t][j][1] = s[t][j][2] = s[t][j][3] = 0.f;
+                    if constexpr (!FP8) {
 #pragma unroll
-                        for (int t = 0; t < C::TT; ++t) {
-                            const int tok = 16 * (tt + t) + lrow + (lmat & 1) * 8;
-                            const int d = ks * 16 + (lmat >> 1) * 8, x = d >> 6;
-                            const uint32_t addr = s_base + tok * C::ROW + x * 128 +
-                                                  ((((d & 63) >> 3) ^ ((tok * C::NX + x) & 7)) << 4);
-                            uint32_t a[4];
-                            ldsm_x4(addr, a[0], a[1], a[2], a[3]);
+                        for (int ks = 0; ks < C::KS; ++ks)
 #pragma unroll
-                            for (int j = 0; j < NQ; ++j) mma_bf16(s[t][j], a, qf[ks][j][0], qf[ks][j][1]);
-                        }
-                } else {
+                            for (int t = 0; t < C::TT; ++t) {
+                                const int tok = 16 * (tt + t) + lrow + (lmat & 1) * 8;
+                                const int d = ks * 16 + (lmat >> 1) * 8, x = (d >> 6) + e;  // (with two heads a row has one 128-byte box)
+                                const uint32_t addr = s_base + tok * C::SROW + x * 128 +
+                                                      ((((d & 63) >> 3) ^ ((tok * C::NX + x) & 7)) << 4);
+                                uint32_t a[4];
+                                ldsm_x4(addr, a[0], a[1], a[2], a[3]);
 #pragma unroll
-                    for (int kk = 0; kk < D / 32; ++kk)
+                                for (int j = 0; j < NQ; ++j) mma_bf16(s[t][j], a, qf[e][ks][j][0], qf[e][ks][j][1]);
+                            }
+                    } else {
 #pragma unroll
-                        for (int t = 0; t < C::TT; ++t) {
-                            const int tok = 16 * (tt + t) + lrow + (lmat & 1) * 8;
-                            const uint32_t addr = s_base + tok * 128 + (((kk * 2 + (lmat >> 1)) ^ (tok & 7)) << 4);
-                            uint32_t R[4];
-                            ldsm_x4(addr, R[0], R[1], R[2], R[3]);
+                        for (int kk = 0; kk < D / 32; ++kk)
 #pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                const uint32_t ra = R[hf * 2], rb = R[hf * 2 + 1];
-                                const uint32_t a[4] = {
-                                    e4m3x2_to_f16x2((uint16_t)(ra & 0xffff)), e4m3x2_to_f16x2((uint16_t)(rb & 0xffff)),
-                                    e4m3x2_to_f16x2((uint16_t)(ra >> 16)), e4m3x2_to_f16x2((uint16_t)(rb >> 16))};
+                            for (int t = 0; t < C::TT; ++t) {
+                                const int tok = 16 * (tt + t) + lrow + (lmat & 1) * 8;
+                                const uint32_t addr = s_base + tok * C::SROW + e * 128 +
+                                                  (((kk * 2 + (lmat >> 1)) ^ ((tok * C::NX + e) & 7)) << 4);
+                                uint32_t R[4];
+                                ldsm_x4(addr, R[0], R[1], R[2], R[3]);
 #pragma unroll
-                                for (int j = 0; j < NQ; ++j)
-                                    mma_f16(s[t][j], a, qf[kk * 2 + hf][j][0], qf[kk * 2 + hf][j][1]);
+                                for (int hf = 0; hf < 2; ++hf) {
+                                    const uint32_t ra = R[hf * 2], rb = R[hf * 2 + 1];
+                                    const uint32_t a[4] = {
+                                        e4m3x2_to_f16x2((uint16_t)(ra & 0xffff)), e4m3x2_to_f16x2((uint16_t)(rb & 0xffff)),
+                                        e4m3x2_to_f16x2((uint16_t)(ra >> 16)), e4m3x2_to_f16x2((uint16_t)(rb >> 16))};
+#pragma unroll
+                                    for (int j = 0; j < NQ; ++j)
+                                        mma_f16(s[t][j], a, qf[e][kk * 2 + hf][j][0], qf[e][kk * 2 + hf][j][1]);
+                                }
+                            }
+                    }
+                    // a row that does not count or see the token adds nothing, whatever its score
+#pragma unroll
+                    for (int t = 0; t < C::TT; ++t) {
+                        float e0 = 0.f, e1 = 0.f;
+                        const int ta = t0 + 16 * (tt + t) + r8;
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j) {
+                            const bool on0 = lse2[e][j][0] != -INFINITY, on1 = lse2[e][j][1] != -INFINITY;
+                            if (ta <= last[j]) {
+                                e0 += on0 ? ex2(fmaf(s[t][j][0], sl2[e], -lse2[e][j][0])) : 0.f;
+                                e0 += on1 ? ex2(fmaf(s[t][j][1], sl2[e], -lse2[e][j][1])) : 0.f;
+                            }
+                            if (ta + 8 <= last[j]) {
+                                e1 += on0 ? ex2(fmaf(s[t][j][2], sl2[e], -lse2[e][j][0])) : 0.f;
+                                e1 += on1 ? ex2(fmaf(s[t][j][3], sl2[e], -lse2[e][j][1])) : 0.f;
                             }
                         }
-                }
-                // a row that does not count or see the token adds nothing, whatever its score
-#pragma unroll
-                for (int t = 0; t < C::TT; ++t) {
-                    float e0 = 0.f, e1 = 0.f;
-                    const int ta = t0 + 16 * (tt + t) + r8;
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j) {
-                        const bool on0 = lse2[j][0] != -INFINITY, on1 = lse2[j][1] != -INFINITY;
-                        if (ta <= last[j]) {
-                            e0 += on0 ? ex2(fmaf(s[t][j][0], sl2, -lse2[j][0])) : 0.f;
-                            e0 += on1 ? ex2(fmaf(s[t][j][1], sl2, -lse2[j][1])) : 0.f;
+                        e0 += __shfl_xor_sync(0xffffffffu, e0, 1);
+                        e1 += __shfl_xor_sync(0xffffffffu, e1, 1);
+                        e0 += __shfl_xor_sync(0xffffffffu, e0, 2);
+                        e1 += __shfl_xor_sync(0xffffffffu, e1, 2);
+                        if (c4 == tt + t) {
+                            add[e][0] = e0;
+                            add[e][1] = e1;
                         }
-                        if (ta + 8 <= last[j]) {
-                            e1 += on0 ? ex2(fmaf(s[t][j][2], sl2, -lse2[j][0])) : 0.f;
-                            e1 += on1 ? ex2(fmaf(s[t][j][3], sl2, -lse2[j][1])) : 0.f;
-                        }
-                    }
-                    e0 += __shfl_xor_sync(0xffffffffu, e0, 1);
-                    e1 += __shfl_xor_sync(0xffffffffu, e1, 1);
-                    e0 += __shfl_xor_sync(0xffffffffu, e0, 2);
-                    e1 += __shfl_xor_sync(0xffffffffu, e1, 2);
-                    if (c4 == tt + t) {
-                        add[0] = e0;
-                        add[1] = e1;
                     }
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[stage]);  // rows and page ids have been read
+            if (lane == 0) mbar_arrive(&empty[stage]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (wp[k]) *wp[k] = (t0 + own + 8 * k < wl ? old[k] * p.decay : 0.f) + add[k];
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int e = 0; e < HP; ++e) {
+                    if (wp[k])
+                        wp[k][(size_t)e * p.page_size] = (t0 + own + 8 * k < wl ? old[e][k] * p.decay : 0.f) + add[e][k];
+                    old[e][k] = old_next[e][k];
+                }
+                wp[k] = wp_next[k];
+            }
         }
         i = i1;
     }
 }
 
-template <int D, bool FP8, int NQ>
+template <int D, bool FP8, int NQ, int HP>
 cudaError_t launch(const CUtensorMap &tk, AccumParams p, int num_sms, cudaStream_t stream, bool pdl) {
-    using C = AccumCfg<D, FP8, NQ>;
-    const auto kern = accum_kernel<D, FP8, NQ>;
+    using C = AccumCfg<D, FP8, NQ, HP>;
+    const auto kern = accum_kernel<D, FP8, NQ, HP>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     // As many CTAs as fit the GPU at once: several to a (part, head) pair where there are fewer pairs, several parts to
     // a CTA where there are more (a fixed split of many requests: a CTA for every short part spends most of its time
     // starting, 70 us against 47 for 32 requests of 2048 to 4096 tokens of 8 bf16 heads in 8 splits).
-    const int64_t room = (int64_t)num_sms * C::MIN_BLOCKS, pairs = (int64_t)p.num_parts * p.H_kv;
+    const int64_t room = (int64_t)num_sms * C::MIN_BLOCKS, pairs = (int64_t)p.num_parts * (p.H_kv / HP);
     int64_t z = room / pairs;
     z = z < 1 ? 1 : z > 8 ? 8 : z;
     p.parts_per_cta = (int32_t)((pairs + room - 1) / room);
     const int gx = (p.num_parts + p.parts_per_cta - 1) / p.parts_per_cta;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)gx, (unsigned)p.H_kv, (unsigned)z);
+    cfg.gridDim = dim3((unsigned)gx, (unsigned)(p.H_kv / HP), (unsigned)z);
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
@@ -359,12 +399,18 @@ cudaError_t launch(const CUtensorMap &tk, AccumParams p, int num_sms, cudaStream
 
 template <int D, bool FP8>
 cudaError_t launch_for(const CUtensorMap &tk, const AccumParams &p, int num_sms, cudaStream_t stream, bool pdl) {
-    if (p.s_q == 1) return launch<D, FP8, 1>(tk, p, num_sms, stream, pdl);
-    if (p.s_q == 2) return launch<D, FP8, 2>(tk, p, num_sms, stream, pdl);
-    return launch<D, FP8, 4>(tk, p, num_sms, stream, pdl);
+    if constexpr (D * (FP8 ? 1 : 2) == 128)
+        if (p.heads_per_cta == 2) return launch<D, FP8, 1, 2>(tk, p, num_sms, stream, pdl);
+    if (p.s_q == 1) return launch<D, FP8, 1, 1>(tk, p, num_sms, stream, pdl);
+    if (p.s_q == 2) return launch<D, FP8, 2, 1>(tk, p, num_sms, stream, pdl);
+    return launch<D, FP8, 4, 1>(tk, p, num_sms, stream, pdl);
 }
 
 }  // namespace
+
+// KV heads that a CTA takes (the tensor map's box has as many): two where their rows are 128 bytes, for one query
+// token (more tokens' queries of two heads do not fit the registers).
+int accum_heads(int row_bytes, int H_kv, int s_q) { return row_bytes == 128 && H_kv % 2 == 0 && s_q == 1 ? 2 : 1; }
 
 cudaError_t launch_accum(int D, bool fp8, const CUtensorMap &tk, const AccumParams &p, int num_sms,
                          cudaStream_t stream, bool pdl) {

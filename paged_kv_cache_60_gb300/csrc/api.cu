@@ -19,6 +19,7 @@ cudaError_t launch_mla(const MlaParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_combine(int DV, const CombineParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_append(int kv_dtype, const AppendParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_rope(int kv_dtype, RopeParams p, int num_sms, cudaStream_t stream, bool pdl);
+int accum_heads(int row_bytes, int H_kv, int s_q);
 cudaError_t launch_accum(int D, bool fp8, const CUtensorMap &tk, const AccumParams &p, int num_sms,
                          cudaStream_t stream, bool pdl);
 cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream, bool pdl);
@@ -251,9 +252,10 @@ EncodeTiledFn get_encode_tiled() {
 // of the two pools. With pool = nullptr, a 4-D map of one pool (dims 0-3) and
 // a box {16, NX, 1, box_tok}. With half_major the token dimension (1) and the
 // half and head dimensions (2, 3) trade places: the box lands as
-// [pool][half][token][128 B].
+// [pool][half][token][128 B]. box_heads (token-major maps): neighbouring heads that a
+// box brings, in shared memory as [pool][token][head][half][128 B].
 int make_kv_map(CUtensorMap *m, const void *base, uint64_t pool_dist, bool two_pools, const da_desc *d,
-                int elem_bytes, int box_tok, bool half_major) {
+                int elem_bytes, int box_tok, bool half_major, int box_heads = 1) {
     EncodeTiledFn enc = get_encode_tiled();
     if (!enc) return DA_ERR_CUDA;
     const cuuint64_t row = (cuuint64_t)d->D_qk * elem_bytes;  // bytes of one token's head
@@ -261,7 +263,7 @@ int make_kv_map(CUtensorMap *m, const void *base, uint64_t pool_dist, bool two_p
     const cuuint64_t ntok = (cuuint64_t)d->page_size * (cuuint64_t)d->num_pages;
     cuuint64_t dims[5] = {128 / kTmaElemBytes, nx, (cuuint64_t)d->H_kv, ntok, 2};
     cuuint64_t strides[4] = {128, row, row * d->H_kv, pool_dist};
-    cuuint32_t box[5] = {128 / kTmaElemBytes, (cuuint32_t)nx, 1, (cuuint32_t)box_tok, 2};
+    cuuint32_t box[5] = {128 / kTmaElemBytes, (cuuint32_t)nx, (cuuint32_t)box_heads, (cuuint32_t)box_tok, 2};
     if (half_major) {  // the token dimension inside the half dimension
         dims[1] = ntok;
         dims[2] = nx;
@@ -704,10 +706,11 @@ int decode_attn_accum_weights(const da_desc *desc, const void *q, const void *k_
     p.num_parts = L.num_parts;
     p.box_tokens = desc->page_size < kChunk ? desc->page_size : kChunk;
     p.boxes_per_chunk = kChunk / p.box_tokens;
-    p.log2_box_tokens = log2_of(p.box_tokens);
+    p.log2_page = log2_of(desc->page_size);
     p.wait_limit_ns = g_wait_limit_ns ? g_wait_limit_ns : kWaitLimitNs;
     CUtensorMap tk;
-    const int mrc = make_kv_map(&tk, k_pool, 0, false, desc, fp8 ? 1 : 2, p.box_tokens, false);
+    p.heads_per_cta = accum_heads(desc->D_qk * (fp8 ? 1 : 2), desc->H_kv, p.s_q);
+    const int mrc = make_kv_map(&tk, k_pool, 0, false, desc, fp8 ? 1 : 2, p.box_tokens, false, p.heads_per_cta);
     if (mrc) return mrc;
     if (launch_accum(desc->D_qk, fp8, tk, p, sms, stream, true) != cudaSuccess) return DA_ERR_CUDA;
     return DA_OK;

@@ -197,8 +197,9 @@ struct AccumParams {
     float *weights;                // [num_pages][H_kv][page_size]
     float decay, scale_log2;
     int32_t B, H_kv, G, H_q, s_q, page_size, max_pages, num_pages, splits, num_parts;
-    int32_t box_tokens, boxes_per_chunk, log2_box_tokens;  // as in GqaParams
-    int32_t parts_per_cta;
+    int32_t box_tokens, boxes_per_chunk;  // as in GqaParams
+    int32_t log2_page;             // log2(page_size) when it is a power of two, else -1
+    int32_t parts_per_cta, heads_per_cta;
     uint64_t wait_limit_ns;
 };
 

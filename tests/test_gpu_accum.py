@@ -101,6 +101,9 @@ CASES = [
     (KV_FP8, 3, 4, 128, 8, [33, 600, 17], 2, 2),
     (KV_FP8, 2, 1, 128, 64, [129, 1], 4, 0),
     (KV_FP8, 70, 1, 128, 16, [(37 * i) % 150 for i in range(70)], 3, 0),
+    (KV_BF16, 3, 4, 64, 192, [385, 100, 1], 1, 0),       # two heads to a CTA
+    (KV_BF16, 40, 6, 64, 8, [(53 * i) % 300 for i in range(40)], 1, 8),
+    (KV_FP8, 40, 4, 128, 64, [(71 * i) % 500 for i in range(40)], 1, 5),
 ]
 
 
