@@ -30,6 +30,7 @@
 // and written once.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "common.cuh"
@@ -466,12 +467,44 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_c
     }
 }
 
+// Whether the current device can hold a cluster of 16 selecting CTAs (asked once per device, with the most shared
+// memory that one takes).
+bool wide_clusters() {
+    static std::atomic<int> known[64];   // 1: no, 2: yes
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    int k = known[dev].load(std::memory_order_relaxed);
+    if (!k) {
+        const auto kern = evict_select_kernel<16>;
+        const int smem = sel_keys_at(16) + kKeyCap * 4;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(kSelThreads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {16, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        const bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+                        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n >= 1;
+        if (!ok) cudaGetLastError();
+        k = ok ? 2 : 1;
+        known[dev].store(k, std::memory_order_relaxed);
+    }
+    return k == 2;
+}
+
 template <int kC>
 cudaError_t launch_select(const EvictParams &p, int64_t keys, cudaStream_t stream, bool pdl) {
     const auto kern = evict_select_kernel<kC>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          sel_keys_at(kC) + kKeyCap * 4);
     if (e != cudaSuccess) return e;
+    if (kC > 8 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+        return e;
     const int smem = sel_keys_at(kC) + (int)(keys < kKeyCap ? keys : kKeyCap) * 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.B * p.H_kv * kC));
@@ -502,9 +535,11 @@ cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream,
     // that the block table allows
     const int64_t rows = (int64_t)p.B * p.H_kv, longest = (int64_t)p.max_pages * p.page_size;
     int c = 1;
-    while (c < 8 && rows * c * 2 <= num_sms && longest / c > 4096) c *= 2;
+    while (c < 16 && rows * c * 2 <= num_sms && longest / c > 4096) c *= 2;
+    if (c == 16 && !wide_clusters()) c = 8;
     const int64_t share = (longest + c - 1) / c + 128;
-    cudaError_t e = c == 8   ? launch_select<8>(p, share, stream, pdl)
+    cudaError_t e = c == 16  ? launch_select<16>(p, share, stream, pdl)
+                    : c == 8 ? launch_select<8>(p, share, stream, pdl)
                     : c == 4 ? launch_select<4>(p, share, stream, pdl)
                     : c == 2 ? launch_select<2>(p, share, stream, pdl)
                              : launch_select<1>(p, share, stream, pdl);

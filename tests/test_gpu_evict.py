@@ -95,7 +95,7 @@ def test_evict(case, kind):
 @pytest.mark.parametrize("kind", ["spread", "zero", "wild"])
 @pytest.mark.parametrize("lens,P", [([9000], 64), ([20000, 500], 32), ([70001], 64), ([40961 + 7, 8193], 256)])
 def test_long_rows_are_shared_by_a_cluster(lens, P, kind):
-    """Lengths at which two, four and eight CTAs select together, one request far shorter than the table allows."""
+    """Lengths at which two, four, eight and sixteen CTAs select together, one request far shorter than the table allows."""
     Case(MLA, 1, 576, P, lens, 2003, 3, 64, kind=kind, seed=len(lens) + P).check()
 
 
