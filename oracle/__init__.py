@@ -13,8 +13,10 @@ benchmark's CPU-baseline leg may import this package; the library under
 * ``sched_ref.py``  -- the integer split-KV scheduling metadata.
 * ``append_ref.py`` -- appending one new token per request into its page slot,
   with the e4m3 encoder (per-head scales, or the 656-byte latent token).
+* ``ops_ref.py``    -- the operators around the step: rotary positions, gathered
+  attention weight, eviction, verification of drafts.
 
-Parity pins are in tests/test_oracle.py, tests/test_sched_oracle.py and
+Parity pins are in tests/test_oracle.py, tests/test_oracle_ops.py, tests/test_sched_oracle.py and
 tests/test_oracle_append.py.
 """
 import ctypes

@@ -12,6 +12,11 @@ import raises.
     meta = torch.empty(sched_meta_bytes(desc), dtype=torch.uint8, device="cuda")
     sched_meta(desc, cache_seqlens, meta)
     fwd(desc, q, k_pool, v_pool, k_scale, v_scale, block_table, cache_seqlens, meta, out, lse)
+
+Around the step: append_kv and rope_append write new tokens, verify_drafts
+accepts a chain of drafts, accum_weights gathers the attention weight of cached
+tokens and evict keeps the heaviest. All but append_kv check every
+tensor's dtype, shape, strides and device and raise DecodeAttnError.
 """
 import ctypes
 import os
@@ -358,7 +363,9 @@ def verify_drafts(target_probs, draft_probs, draft_tokens, uniform, num_accepted
     K = rows - 1
     kind = {torch.float32: PROB_F32, torch.bfloat16: PROB_BF16, torch.float16: PROB_F16}.get(dtype, -1)
     tp, ts = _prob_rows(dev, "target_probs", target_probs, dtype, (B, rows, V))
-    dp, ds = (None, 0) if draft_probs is None or K == 0 else _prob_rows(dev, "draft_probs", draft_probs, dtype, (B, K, V))
+    dp, ds = None, 0
+    if draft_probs is not None and K > 0:
+        dp, ds = _prob_rows(dev, "draft_probs", draft_probs, dtype, (B, K, V))
     _check((lib or load_library()).decode_attn_verify_drafts(
         B, K, V, kind, tp, ts, dp, ds, _opt(dev, "draft_tokens", draft_tokens, i32, (B, K)),
         _need(dev, "uniform", uniform, torch.float32, (B, rows)), _opt(dev, "cache_seqlens", cache_seqlens, i32, (B,)),

@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "decode_attn.h"
@@ -40,14 +41,14 @@ struct AccumCfg {
     static constexpr int STAGE = kChunk * SROW;
     // Consumer warps, and stages (a multiple, so that a stage always belongs to one warp): 192 KB in flight on an SM. A
     // producer warp issues a chunk in about 0.35 us, which 16 KB chunks hide behind HBM; the builds with 8 KB chunks
-    // take two CTAs, and so two producers, per SM. Rows of 128 bytes are best taken two heads at a time: the CTAs of
+    // take two CTAs, and so two producers, per SM, with five consumer warps each for four query tokens: twelve warps on
+    // an SM leave a thread 168 registers. Rows of 128 bytes are best taken two heads at a time: the CTAs of
     // the heads drift apart, and DRAM then sees 128-byte reads 128 H_kv bytes apart (64 x 32768 e4m3 tokens of 4 heads,
     // three pools in turn: 181 us against 212 with one head to a CTA).
-    static constexpr int NCW = HP == 2 ? 12 : 6;
+    static constexpr int NCW = HP == 2 ? 12 : NQ < 4 ? 6 : SROW == 128 ? 5 : 7;
     static constexpr int NS = HP == 2 ? NCW : 2 * NCW;
     static constexpr int MIN_BLOCKS = SROW == 128 ? 2 : 1;
     static constexpr int THREADS = (NCW + 1) * 32;
-    static constexpr int TT = NQ == 1 ? 4 : NQ == 2 ? 2 : 1;   // tiles whose scores are in registers at a time
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int OFF_FLAG = OFF_BAR + 2 * NS * 8;
     static constexpr int SMEM = OFF_FLAG + 16 + 1024;  // + alignment slack
@@ -165,7 +166,8 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D,
         }
         if (aborted) {
             // let copies already in flight land before the CTA exits (ignoring the abort flag)
-            for (int k = max(0, i - C::NS); k < i; ++k) mbar_wait_timed(&full[k % C::NS], (k / C::NS) & 1, 100000000ull);
+            for (int k = max(0, i - C::NS); k < i; ++k)
+                mbar_wait_timed(&full[k % C::NS], (k / C::NS) & 1, 100000000ull);
         }
         return;
     }
@@ -190,16 +192,16 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D,
         // q: B fragments, n = query head r8; lse of the two heads whose scores this lane gets
         uint32_t qf[HP][C::KS][NQ][2];
         float lse2[HP][NQ][2];
-        int last[NQ];  // last token that query token j sees, -1 where it does not count
-        const int acc = p.accepted ? p.accepted[b] : p.s_q - 1;
+        int last[HP][NQ][2];  // last token that query token j sees, -1 for a head that adds nothing
+        const int nj = p.accepted ? min(p.accepted[b], p.s_q - 1) + 1 : p.s_q;  // query tokens that count
         const int wl = p.weighted ? p.weighted[b] : L;
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            const bool on = j < p.s_q && j <= acc;
-            last[j] = on ? L - p.s_q + j : -1;
+            const bool on = j < nj;
 #pragma unroll
             for (int e = 0; e < HP; ++e) {
                 lse2[e][j][0] = lse2[e][j][1] = 0.f;
+                last[e][j][0] = last[e][j][1] = -1;
 #pragma unroll
                 for (int ks = 0; ks < C::KS; ++ks) qf[e][ks][j][0] = qf[e][ks][j][1] = 0u;
                 if (!on) continue;
@@ -208,6 +210,8 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D,
                 constexpr float kLog2e = 1.4426950408889634f;
                 lse2[e][j][0] = ls.x * kLog2e;
                 lse2[e][j][1] = ls.y * kLog2e;
+                last[e][j][0] = ls.x == -INFINITY ? -1 : L - p.s_q + j;
+                last[e][j][1] = ls.y == -INFINITY ? -1 : L - p.s_q + j;
                 const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + (head0 + r8) * D;
                 if constexpr (!FP8) {
                     const uint32_t *q32 = reinterpret_cast<const uint32_t *>(q);
@@ -233,7 +237,8 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D,
         const int32_t *table = p.block_table + (size_t)b * p.max_pages;
         const auto page_of = [&](int chunk, int k) -> int {
             const int t = chunk * kChunk + own + 8 * k;
-            return chunk < sg.lc1 && t < L ? __ldg(table + (p.log2_page >= 0 ? t >> p.log2_page : t / p.page_size)) : -1;
+            if (chunk >= sg.lc1 || t >= L) return -1;
+            return __ldg(table + (p.log2_page >= 0 ? t >> p.log2_page : t / p.page_size));
         };
         const auto weight_at = [&](int chunk, int k, int pg) -> float * {
             const int t = chunk * kChunk + own + 8 * k;
@@ -280,87 +285,100 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D,
             const uint32_t s_base = smem_u32(smem + (size_t)stage * C::STAGE);
             float add[HP][2];
 #pragma unroll
-            for (int e = 0; e < HP; ++e) {
-                add[e][0] = add[e][1] = 0.f;
+            for (int e = 0; e < HP; ++e) add[e][0] = add[e][1] = 0.f;
+            // the chunk's products with the first NJ query tokens: one build for each count
+            const auto products = [&](auto count) {
+                constexpr int NJ = decltype(count)::value, TT = NJ == 1 ? 4 : 2;  // TT: tiles in registers at a time
 #pragma unroll
-                for (int tt = 0; tt < 4; tt += C::TT) {
-                    float s[C::TT][NQ][4];
+                for (int e = 0; e < HP; ++e) {
 #pragma unroll
-                    for (int t = 0; t < C::TT; ++t)
+                    for (int tt = 0; tt < 4; tt += TT) {
+                        float s[TT][NJ][4];
 #pragma unroll
-                        for (int j = 0; j < NQ; ++j) s[t][j][0] = s[t][j][1] = s[t][j][2] = s[t][j][3] = 0.f;
-                    if constexpr (!FP8) {
+                        for (int t = 0; t < TT; ++t)
 #pragma unroll
-                        for (int ks = 0; ks < C::KS; ++ks)
+                            for (int j = 0; j < NJ; ++j) s[t][j][0] = s[t][j][1] = s[t][j][2] = s[t][j][3] = 0.f;
+                        if constexpr (!FP8) {
 #pragma unroll
-                            for (int t = 0; t < C::TT; ++t) {
-                                const int tok = 16 * (tt + t) + lrow + (lmat & 1) * 8;
-                                const int d = ks * 16 + (lmat >> 1) * 8, x = (d >> 6) + e;  // (with two heads a row has one 128-byte box)
-                                const uint32_t addr = s_base + tok * C::SROW + x * 128 +
-                                                      ((((d & 63) >> 3) ^ ((tok * C::NX + x) & 7)) << 4);
-                                uint32_t a[4];
-                                ldsm_x4(addr, a[0], a[1], a[2], a[3]);
+                            for (int ks = 0; ks < C::KS; ++ks)
 #pragma unroll
-                                for (int j = 0; j < NQ; ++j) mma_bf16(s[t][j], a, qf[e][ks][j][0], qf[e][ks][j][1]);
-                            }
-                    } else {
+                                for (int t = 0; t < TT; ++t) {
+                                    const int tok = 16 * (tt + t) + lrow + (lmat & 1) * 8;
+                                    // (with two heads a row is one 128-byte box)
+                                    const int d = ks * 16 + (lmat >> 1) * 8, x = (d >> 6) + e;
+                                    const uint32_t addr = s_base + tok * C::SROW + x * 128 +
+                                                          ((((d & 63) >> 3) ^ ((tok * C::NX + x) & 7)) << 4);
+                                    uint32_t a[4];
+                                    ldsm_x4(addr, a[0], a[1], a[2], a[3]);
 #pragma unroll
-                        for (int kk = 0; kk < D / 32; ++kk)
-#pragma unroll
-                            for (int t = 0; t < C::TT; ++t) {
-                                const int tok = 16 * (tt + t) + lrow + (lmat & 1) * 8;
-                                const uint32_t addr = s_base + tok * C::SROW + e * 128 +
-                                                  (((kk * 2 + (lmat >> 1)) ^ ((tok * C::NX + e) & 7)) << 4);
-                                uint32_t R[4];
-                                ldsm_x4(addr, R[0], R[1], R[2], R[3]);
-#pragma unroll
-                                for (int hf = 0; hf < 2; ++hf) {
-                                    const uint32_t ra = R[hf * 2], rb = R[hf * 2 + 1];
-                                    const uint32_t a[4] = {
-                                        e4m3x2_to_f16x2((uint16_t)(ra & 0xffff)), e4m3x2_to_f16x2((uint16_t)(rb & 0xffff)),
-                                        e4m3x2_to_f16x2((uint16_t)(ra >> 16)), e4m3x2_to_f16x2((uint16_t)(rb >> 16))};
-#pragma unroll
-                                    for (int j = 0; j < NQ; ++j)
-                                        mma_f16(s[t][j], a, qf[e][kk * 2 + hf][j][0], qf[e][kk * 2 + hf][j][1]);
+                                    for (int j = 0; j < NJ; ++j)
+                                        mma_bf16(s[t][j], a, qf[e][ks][j][0], qf[e][ks][j][1]);
                                 }
-                            }
-                    }
-                    // a row that does not count or see the token adds nothing, whatever its score
+                        } else {
 #pragma unroll
-                    for (int t = 0; t < C::TT; ++t) {
-                        float e0 = 0.f, e1 = 0.f;
-                        const int ta = t0 + 16 * (tt + t) + r8;
+                            for (int kk = 0; kk < D / 32; ++kk)
 #pragma unroll
-                        for (int j = 0; j < NQ; ++j) {
-                            const bool on0 = lse2[e][j][0] != -INFINITY, on1 = lse2[e][j][1] != -INFINITY;
-                            if (ta <= last[j]) {
-                                e0 += on0 ? ex2(fmaf(s[t][j][0], sl2[e], -lse2[e][j][0])) : 0.f;
-                                e0 += on1 ? ex2(fmaf(s[t][j][1], sl2[e], -lse2[e][j][1])) : 0.f;
-                            }
-                            if (ta + 8 <= last[j]) {
-                                e1 += on0 ? ex2(fmaf(s[t][j][2], sl2[e], -lse2[e][j][0])) : 0.f;
-                                e1 += on1 ? ex2(fmaf(s[t][j][3], sl2[e], -lse2[e][j][1])) : 0.f;
-                            }
+                                for (int t = 0; t < TT; ++t) {
+                                    const int tok = 16 * (tt + t) + lrow + (lmat & 1) * 8;
+                                    const uint32_t addr = s_base + tok * C::SROW + e * 128 +
+                                                          (((kk * 2 + (lmat >> 1)) ^ ((tok * C::NX + e) & 7)) << 4);
+                                    uint32_t R[4];
+                                    ldsm_x4(addr, R[0], R[1], R[2], R[3]);
+#pragma unroll
+                                    for (int hf = 0; hf < 2; ++hf) {
+                                        const uint32_t ra = R[hf * 2], rb = R[hf * 2 + 1];
+                                        const uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)(ra & 0xffff)),
+                                                               e4m3x2_to_f16x2((uint16_t)(rb & 0xffff)),
+                                                               e4m3x2_to_f16x2((uint16_t)(ra >> 16)),
+                                                               e4m3x2_to_f16x2((uint16_t)(rb >> 16))};
+#pragma unroll
+                                        for (int j = 0; j < NJ; ++j)
+                                            mma_f16(s[t][j], a, qf[e][kk * 2 + hf][j][0], qf[e][kk * 2 + hf][j][1]);
+                                    }
+                                }
                         }
-                        e0 += __shfl_xor_sync(0xffffffffu, e0, 1);
-                        e1 += __shfl_xor_sync(0xffffffffu, e1, 1);
-                        e0 += __shfl_xor_sync(0xffffffffu, e0, 2);
-                        e1 += __shfl_xor_sync(0xffffffffu, e1, 2);
-                        if (c4 == tt + t) {
-                            add[e][0] = e0;
-                            add[e][1] = e1;
+                        // a row that does not see the token adds nothing, whatever its score
+#pragma unroll
+                        for (int t = 0; t < TT; ++t) {
+                            float e0 = 0.f, e1 = 0.f;
+                            const int ta = t0 + 16 * (tt + t) + r8;
+#pragma unroll
+                            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                                for (int g = 0; g < 2; ++g) {
+                                    const float x = ex2(fmaf(s[t][j][g], sl2[e], -lse2[e][j][g]));
+                                    const float y = ex2(fmaf(s[t][j][2 + g], sl2[e], -lse2[e][j][g]));
+                                    e0 += ta <= last[e][j][g] ? x : 0.f;
+                                    e1 += ta + 8 <= last[e][j][g] ? y : 0.f;
+                                }
+                            e0 += __shfl_xor_sync(0xffffffffu, e0, 1);
+                            e1 += __shfl_xor_sync(0xffffffffu, e1, 1);
+                            e0 += __shfl_xor_sync(0xffffffffu, e0, 2);
+                            e1 += __shfl_xor_sync(0xffffffffu, e1, 2);
+                            if (c4 == tt + t) {
+                                add[e][0] = e0;
+                                add[e][1] = e1;
+                            }
                         }
                     }
                 }
+            };
+            if constexpr (NQ == 4) {
+                if (nj >= 4) products(std::integral_constant<int, 4>{});
+                if (nj == 3) products(std::integral_constant<int, 3>{});
             }
+            if constexpr (NQ >= 2) {
+                if (nj == 2) products(std::integral_constant<int, 2>{});
+            }
+            if (nj == 1) products(std::integral_constant<int, 1>{});
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[stage]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
 #pragma unroll
                 for (int e = 0; e < HP; ++e) {
-                    if (wp[k])
-                        wp[k][(size_t)e * p.page_size] = (t0 + own + 8 * k < wl ? old[e][k] * p.decay : 0.f) + add[e][k];
+                    const float kept = t0 + own + 8 * k < wl ? old[e][k] * p.decay : 0.f;
+                    if (wp[k]) wp[k][(size_t)e * p.page_size] = kept + add[e][k];
                     old[e][k] = old_next[e][k];
                 }
                 wp[k] = wp_next[k];

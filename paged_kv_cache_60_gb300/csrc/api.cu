@@ -581,10 +581,11 @@ int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_
     int rc = check_pool_desc(desc, &row_len);
     if (rc) return rc;
     const bool mla = is_mla(desc);
-    if (desc->G < 1 || desc->G > 1024 || n_tokens < 0 || n_tokens > (1 << 30) || desc->s_q < 0 || desc->s_q > 64) return DA_ERR_DIMS;
+    if (desc->G < 1 || desc->G > 1024 || n_tokens < 0 || n_tokens > (1 << 30) || desc->s_q < 0 || desc->s_q > 64)
+        return DA_ERR_DIMS;
     const int64_t H_q = (int64_t)desc->H_kv * desc->G, q_len = H_q * desc->D_qk;
-    if (rope->rot_dim < 16 || rope->rot_dim % 16 != 0 || rope->rot_dim > 512 || rope->rot_dim > (mla ? 64 : desc->D_qk) ||
-        rope->n_axes < 1 || rope->n_axes > 4)
+    if (rope->rot_dim < 16 || rope->rot_dim % 16 != 0 || rope->rot_dim > 512 ||
+        rope->rot_dim > (mla ? 64 : desc->D_qk) || rope->n_axes < 1 || rope->n_axes > 4)
         return DA_ERR_DIMS;
     int64_t pairs = 0;
     for (int a = 0; a < 4; ++a) {

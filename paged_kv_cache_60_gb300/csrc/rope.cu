@@ -222,7 +222,9 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
         }
         const int t = tid - (kThreads - 32);
         if (t >= 0 && t < nt)
-            s_slot[buf][t] = kLatent ? (__ldg(p.positions + n0 + t) < 0 ? kSkip : kNowhere) : slot_of(p, n0 + t, part == 0);
+            s_slot[buf][t] = !kLatent                           ? slot_of(p, n0 + t, part == 0)
+                             : __ldg(p.positions + n0 + t) < 0 ? kSkip
+                                                               : kNowhere;
     };
 
     // this thread's place in the rows: item j, of every per_pass-th row

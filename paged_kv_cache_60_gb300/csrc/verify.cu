@@ -239,8 +239,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                 end1 = end;
             }
         }
-        const uint64_t go = (uint64_t)__ballot_sync(0xffffffffu, go0) | (uint64_t)__ballot_sync(0xffffffffu, go1) << 32;
-        const uint64_t end = (uint64_t)__ballot_sync(0xffffffffu, end0) | (uint64_t)__ballot_sync(0xffffffffu, end1) << 32;
+        const auto both = [](bool lo, bool hi) {
+            return (uint64_t)__ballot_sync(0xffffffffu, lo) | (uint64_t)__ballot_sync(0xffffffffu, hi) << 32;
+        };
+        const uint64_t go = both(go0, go1), end = both(end0, end1);
         const int a = __ffsll((long long)~go) - 1;  // bit 63 is never set: K <= 63
         const bool any_bad = __any_sync(0xffffffffu, bad);
         if (lane == 0) {
