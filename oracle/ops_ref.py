@@ -67,7 +67,8 @@ def accum_ref(q, k_of, lens, lse, sigma, s_q, accepted=None):
                     s = sigma * (k[:n, h] @ row)
                     t = np.exp(s - ls)
                     w[:n, h] += t
-                    e[:n, h] += t * (sigma * (np.abs(k[:n, h]) @ np.abs(row)) + abs(ls))
+                    if ls != math.inf:          # (a row of zeros has no error to bound)
+                        e[:n, h] += t * (sigma * (np.abs(k[:n, h]) @ np.abs(row)) + abs(ls))
         add.append(w)
         err.append(e)
     return add, err

@@ -250,7 +250,7 @@ def _rows(dev, name, t, dtype, n, width):
     """n rows of `width` contiguous values; their address and the distance between rows."""
     d = t.dim()
     if not (t.dtype is dtype and t.get_device() == dev and d in (2, 3) and t.shape[0] == n and t.numel() == n * width
-            and t.stride(d - 1) == 1 and (d == 2 or t.stride(1) == t.shape[2])):
+            and t.stride(d - 1) == 1 and (d == 2 or t.stride(1) == t.shape[2]) and (n < 2 or t.stride(0) >= width)):
         raise DecodeAttnError(f"{name}: want a {dtype} tensor of {n} rows of {width} contiguous values on the current "
                               f"CUDA device, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
     return t.data_ptr(), (t.stride(0) if n > 1 else width)
@@ -340,11 +340,12 @@ def evict(desc: Desc, budget, cache_seqlens, block_table, dst_block_table, k_poo
 def _prob_rows(dev, name, t, dtype, shape):
     """Probabilities [B, rows, V], the rows evenly spaced; their address and the distance between rows."""
     B, rows, V = shape
+    step = V if t.dim() != 3 or B * rows < 2 else t.stride(1) if rows > 1 else t.stride(0)
     if not (t.dtype is dtype and t.get_device() == dev and t.shape == shape and (V == 1 or t.stride(2) == 1)
-            and (B == 1 or rows == 1 or t.stride(0) == rows * t.stride(1))):
+            and step >= V and (B == 1 or rows == 1 or t.stride(0) == rows * step)):
         raise DecodeAttnError(f"{name}: want a {dtype} tensor of shape {shape} with evenly spaced rows on the current "
                               f"CUDA device, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
-    return t.data_ptr(), (t.stride(1) if rows > 1 else t.stride(0) if B > 1 else V)
+    return t.data_ptr(), step
 
 
 def verify_drafts(target_probs, draft_probs, draft_tokens, uniform, num_accepted, out_tokens, cache_seqlens=None,

@@ -102,6 +102,8 @@ CASES = [
     (KV_FP8, 2, 1, 128, 64, [129, 1], 4, 0),
     (KV_FP8, 70, 1, 128, 16, [(37 * i) % 150 for i in range(70)], 3, 0),
     (KV_BF16, 3, 4, 64, 192, [385, 100, 1], 1, 0),       # two heads to a CTA
+    (KV_BF16, 3, 3, 64, 16, [85, 0, 230], 1, 0),         # an odd number of them
+    (KV_FP8, 2, 3, 128, 16, [200, 77], 1, 2),
     (KV_BF16, 40, 6, 64, 8, [(53 * i) % 300 for i in range(40)], 1, 8),
     (KV_FP8, 40, 4, 128, 64, [(71 * i) % 500 for i in range(40)], 1, 5),
 ]
@@ -177,6 +179,20 @@ def test_nan_key_poisons_its_request_and_head_only():
         for t in range(40):
             v = got[int(s.w.block_table[b, t // 16]), :, t % 16]
             assert torch.isnan(v[1]).item() == (b == 0) and not torch.isnan(v[0]).item()
+
+
+@pytest.mark.parametrize("kv,H,s_q", [(KV_BF16, 2, 1), (KV_FP8, 2, 1), (KV_BF16, 1, 3)])
+def test_rows_without_a_sum(kv, H, s_q):
+    """An lse of -inf (nothing was seen) or +inf adds nothing, NaN poisons its KV head's weights and no other's."""
+    s = Step(_spec(kv, 2, H, 128 if kv == KV_FP8 else 64, 16, [70, 45], s_q, 0, seed=71))
+    s.lse[0, ..., 3], s.lse[0, ..., 6], s.lse[1, ..., :8] = -math.inf, math.inf, -math.inf
+    s.check(s.run())
+    if H > 1:
+        s.lse[0, ..., 9] = math.nan
+        got = s.run().cpu()
+        for t in range(70):
+            v = got[int(s.w.block_table[0, t // 16]), :, t % 16]
+            assert torch.isnan(v[1]) and not torch.isnan(v[0])
 
 
 def test_captured_replayed_and_on_another_stream():

@@ -2,6 +2,9 @@
 lengths, every byte of the pools and every weight are exact, ties, NaN,
 infinities and bad pages included."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -130,6 +133,26 @@ def test_odd_pages_and_many_heads():
     Case(BF16, 2, 64, 3, [50, 7, 31], 11, 1, 2, seed=20).check()
     Case(FP8, 3, 16, 7, [300], 123, seed=21).check()
     Case(BF16, 4096, 8, 2, [5, 3], 3, 1, 1, seed=22).check()
+
+
+def test_first_call_of_a_process_in_a_capture():
+    """The first call in a process asks the device what clusters it holds; that happens inside a capture too."""
+    code = """
+import torch
+import test_gpu_evict as m
+c = m.Case(m.MLA, 1, 576, 64, [70001], 2003, 3, 64, seed=5)
+t = c.tensors()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    c.call(t)
+g.replay()
+c.check(t)
+print("same")
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")]))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 def test_captured_replayed_other_stream_and_repeated():

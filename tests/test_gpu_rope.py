@@ -172,6 +172,9 @@ SHAPES = [
     (BF16, 2, 33, 1, 3, 256, 192, [40, 0, 24, 64], 256),
     (BF16, 4, 700, 1, 8, 64, 16, [10, 6], 32),
     (BF16, 2, 40, 2, 2, 64, 5, [32], 64),
+    (BF16, 1, 9, 1, 2, 512, 16, [200, 56], 512),         # as many angles as a block has threads
+    (BF16, 2, 7, 1, 1, 4096, 8, [256], 512),             # one row to a block
+    (BF16, 1, 3, 1, 700, 16, 8, [4, 4], 16),
     (FP8, 3, 50, 4, 8, 128, 32, [24, 20, 20], 128),
     (FP8, 2, 31, 1, 2, 72, 16, [3, 2, 3], 16),
     (FP8, 2, 300, 2, 8, 64, 64, [16], 32),

@@ -183,6 +183,22 @@ def test_lengths_in_place_and_left_out():
         da.verify_drafts(t["p"].transpose(0, 1).contiguous().transpose(0, 1), t["q"], t["x"], t["u"], t["a"], t["out"])
 
 
+def test_refuses_rows_that_are_not_there():
+    """Expanded probabilities (stride 0) are not packed ones; a single row may be any."""
+    c = Case(3, 2, 50, seed=11)
+    t = c.tensors()
+    for name, bad in (("p", t["p"][:1].expand(3, 3, 50)), ("p", t["p"][:, :1].expand(3, 3, 50)), ("q", t["q"][:1, :1].expand(3, 2, 50)),
+                      ("p", t["p"][:, :, :1].expand(3, 3, 50)), ("q", t["q"][0]), ("x", t["x"][:1].expand(3, 2)),
+                      ("u", t["u"].double()), ("a", t["a"].long())):
+        with pytest.raises(da.DecodeAttnError):
+            c.call({**t, name: bad})
+    one = Case(1, 0, 50, seed=12)
+    o = one.tensors()
+    o["p"] = torch.cat([o["p"], o["p"]], 2)[:, :, :50]
+    one.call(o)
+    one.check(o)
+
+
 def test_captured_replayed_and_on_another_stream():
     c = Case(4, 3, 30000, seed=10)
     t = c.tensors()
