@@ -22,6 +22,7 @@ cudaError_t launch_rope(int kv_dtype, RopeParams p, int num_sms, cudaStream_t st
 int accum_heads(int row_bytes, int H_kv, int s_q);
 cudaError_t launch_accum(int D, bool fp8, const CUtensorMap &tk, const AccumParams &p, int num_sms,
                          cudaStream_t stream, bool pdl);
+cudaError_t launch_accum_mla(AccumParams p, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_verify(int prob_dtype, const VerifyParams &p, int num_sms, cudaStream_t stream, bool pdl);
 int mla_ctas_per_part(int s_q);
@@ -668,7 +669,7 @@ int decode_attn_accum_weights(const da_desc *desc, const void *q, const void *k_
     MetaLayout L;
     const int rc = make_layout(desc, &L);
     if (rc) return rc;
-    if (is_mla(desc) || desc->window != 0 || desc->topk != 0) return DA_ERR_UNSUPPORTED;
+    if (desc->window != 0 || desc->topk != 0) return DA_ERR_UNSUPPORTED;
     if (!(decay >= 0.f) || std::isinf(decay)) return DA_ERR_DIMS;
     const bool fp8 = desc->kv_dtype == DA_KV_FP8_PER_TENSOR;
     if (!q || !k_pool || !block_table || !cache_seqlens || !sched_meta || !lse || !weights) return DA_ERR_NULL;
@@ -709,6 +710,7 @@ int decode_attn_accum_weights(const da_desc *desc, const void *q, const void *k_
     p.boxes_per_chunk = kChunk / p.box_tokens;
     p.log2_page = log2_of(desc->page_size);
     p.wait_limit_ns = g_wait_limit_ns ? g_wait_limit_ns : kWaitLimitNs;
+    if (is_mla(desc)) return launch_accum_mla(p, sms, stream, true) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
     CUtensorMap tk;
     p.heads_per_cta = accum_heads(desc->D_qk * (fp8 ? 1 : 2), desc->H_kv, p.s_q);
     const int mrc = make_kv_map(&tk, k_pool, 0, false, desc, fp8 ? 1 : 2, p.box_tokens, false, p.heads_per_cta);

@@ -84,7 +84,7 @@ def test_accum_weights_refusals(lib):
     assert call(_desc(kv_dtype=da.KV_FP8)) == -8
     assert call(_desc(D_qk=96, D_v=96), n=1 << 30) == -3 and call(_desc(s_q=5), n=1 << 30) == -3
     assert call(_desc(num_pages=1 << 28), n=1 << 30) == -2
-    assert call(_latent(num_sms=2), n=1 << 30) == -3
+    assert call(_latent(num_sms=2, topk=64), n=1 << 30) == -3                 # sparse decode
 
 
 def test_evict_refusals(lib):

@@ -6,7 +6,7 @@ sum |q||k|: D / 16 fp32 accumulations of a warp MMA (each within an ulp of the
 largest partial, 2^-22 of A_i at most with truncation), the products and the
 roundings of the exponent (score and lse scaled by log2 e, one fused
 multiply-add: four roundings of at most 2^-24 of their values), and exp2
-within 2 ulp. The sum of n = 8 s_q terms and the old weight rounds n + 2 times:
+within 2 ulp. The sum of n = G s_q terms and the old weight rounds n + 2 times:
 (n + 2) 2^-24 of the result. sum e_i A_i and sum e_i |lse| come from the oracle."""
 import math
 
@@ -16,7 +16,7 @@ import torch
 
 import paged_kv_cache_60_gb300 as da
 from oracle.ops_ref import accum_ref
-from workloads import KV_BF16, KV_FP8, WorkloadSpec, make_workload
+from workloads import KV_BF16, KV_FP8, KV_MLA656, WorkloadSpec, make_workload
 
 from gpu_util import DeviceWorkload, ensure_built, make_desc, run
 
@@ -31,6 +31,9 @@ def _built():
 
 
 def _spec(kv, B, H_kv, D, P, lens, s_q=1, splits=0, seed=0):
+    if kv == KV_MLA656:
+        return WorkloadSpec(name="t", B=B, H_kv=1, G=128, D_qk=576, D_v=512, page_size=P, kv_dtype=kv, lengths=lens,
+                            splits=splits, seed=seed, s_q=s_q, extra_pages=2)
     return WorkloadSpec(name="t", B=B, H_kv=H_kv, G=8, D_qk=D, D_v=D, page_size=P, kv_dtype=kv, lengths=lens, splits=splits,
                         seed=seed, s_q=s_q, extra_pages=2)
 
@@ -63,14 +66,20 @@ class Step:
     def check(self, got):
         w, s = self.w, self.s
         P, H, D, s_q = s.page_size, s.H_kv, s.D_qk, s.s_q
-        kp = w.k_pool.float() if w.k_scale is None else w.k_pool.view(torch.float8_e4m3fn).float() * w.k_scale.view(H, 1)
+        G = s.G
+        if s.kv_dtype == KV_MLA656:       # NoPE as the attention kernel has it: bf16(fp32(e4m3) * scale)
+            scale = w.k_pool[..., 512:528].contiguous().view(torch.float32).repeat_interleave(128, -1)
+            nope = (w.k_pool[..., :512].view(torch.float8_e4m3fn).float() * scale).to(torch.bfloat16).float()
+            kp = torch.cat([nope, w.k_pool[..., 528:].contiguous().view(torch.bfloat16).float()], -1)
+        else:
+            kp = w.k_pool.float() if w.k_scale is None else w.k_pool.view(torch.float8_e4m3fn).float() * w.k_scale.view(H, 1)
 
         def k_of(b):
             L = w.lengths[b]
             pages = w.block_table[b, :-(-L // P)].long()
             return kp[pages].reshape(-1, H, D)[:L].double().numpy()
-        lse = self.lse.cpu().double().numpy().reshape(s.B, s_q, H, 8)
-        q = w.q.double().numpy().reshape(s.B, s_q, H, 8, D)
+        lse = self.lse.cpu().double().numpy().reshape(s.B, s_q, H, G)
+        q = w.q.double().numpy().reshape(s.B, s_q, H, G, D)
         add, mag = accum_ref(q, k_of, w.lengths, lse, w.softmax_scale, s_q, self.accepted)
         want, tol = self.weights.double().clone(), torch.zeros(got.shape, dtype=torch.float64)
         wl = w.lengths if self.weighted is None else self.weighted
@@ -80,7 +89,7 @@ class Step:
                 old = want[at] * float(np.float32(self.decay)) if t < wl[b] else torch.zeros(H, dtype=torch.float64)
                 want[at] = old + torch.from_numpy(add[b][t])
                 tol[at] = torch.from_numpy(mag[b][t] * (D / 16 + 3) * 2.0 ** -22 + add[b][t] * 2.0 ** -21) + \
-                    want[at].abs() * (8 * s_q + 2) * 2.0 ** -24
+                    want[at].abs() * (G * s_q + 2) * 2.0 ** -24
         off = (got.cpu().double() - want).abs()
         keep = torch.isnan(want)             # stale NaN in slots that are not a token's stays there
         assert torch.equal(torch.isnan(got.cpu()), keep)
@@ -101,6 +110,10 @@ CASES = [
     (KV_FP8, 3, 4, 128, 8, [33, 600, 17], 2, 2),
     (KV_FP8, 2, 1, 128, 64, [129, 1], 4, 0),
     (KV_FP8, 70, 1, 128, 16, [(37 * i) % 150 for i in range(70)], 3, 0),
+    (KV_MLA656, 1, 1, 576, 64, [1], 1, 0),
+    (KV_MLA656, 4, 1, 576, 16, [0, 1, 31, 300], 1, 0),
+    (KV_MLA656, 3, 1, 576, 8, [33, 97, 5], 2, 3),
+    (KV_MLA656, 2, 1, 576, 192, [200, 64], 4, 1),
     (KV_BF16, 3, 4, 64, 192, [385, 100, 1], 1, 0),       # two heads to a CTA
     (KV_BF16, 3, 3, 64, 16, [85, 0, 230], 1, 0),         # an odd number of them
     (KV_FP8, 2, 3, 128, 16, [200, 77], 1, 2),
@@ -117,26 +130,32 @@ def test_accum(case):
     assert da.get_error(s.meta) == 0
 
 
-@pytest.mark.parametrize("kv", [KV_BF16, KV_FP8])
+@pytest.mark.parametrize("kv", [KV_BF16, KV_FP8, KV_MLA656])
 def test_accepted_rows_fresh_tokens_and_decay(kv):
-    lens = [100, 3, 0, 64, 513, 2]
+    lens = [100, 3, 0, 64, 513, 2] if kv != KV_MLA656 else [100, 3, 0, 64, 65, 2]
+    G = 128 if kv == KV_MLA656 else 8
     for decay in (1.0, 0.5, 0.0):
         s = Step(_spec(kv, 6, 2, 128, 16, lens, 4, 0, seed=21), accepted=[0, 3, 1, -1, 2, 60], weighted=[96, 0, 5, 64, 1000, -2],
                  decay=decay)
         s.check(s.run())
-    # rows sum to the query rows that count: G heads each, over the tokens that they see
+    # rows sum to the query rows that count: G heads each, over the tokens that they see (their lse is within 2^-18)
     s = Step(_spec(kv, 2, 1, 128, 16, [90, 40], 2, 0, seed=22), accepted=[0, 1], weighted=[0, 0])
     s.weights.zero_()
     w = s.run().cpu().double()
-    for b, n in ((0, 8), (1, 16)):
+    for b, n in ((0, G), (1, 2 * G)):
         total = sum(float(w[s.w.block_table[b, t // 16], 0, t % 16]) for t in range(s.w.lengths[b]))
-        assert abs(total - n) < 1e-3
+        assert abs(total - n) < 1e-3 * G / 8
 
 
 def test_repeats_are_bitwise_equal_and_any_split_gives_the_same():
+    for kv in (KV_BF16, KV_FP8, KV_MLA656):
+        _repeats(kv)
+
+
+def _repeats(kv):
     base = None
     for splits in (0, 1, 5):
-        s = Step(_spec(KV_BF16, 4, 2, 128, 32, [77, 300, 1, 640], 2, splits, seed=31))
+        s = Step(_spec(kv, 4, 2, 128, 32, [77, 300, 1, 640], 2, splits, seed=31))
         if base is not None:
             s.lse = base.lse
         a, b = s.run(), s.run()
@@ -146,8 +165,9 @@ def test_repeats_are_bitwise_equal_and_any_split_gives_the_same():
         assert torch.equal(a.view(torch.int32), first.view(torch.int32))
 
 
-def test_bad_page_long_length_and_foreign_meta():
-    s = Step(_spec(KV_BF16, 3, 2, 128, 16, [100, 50, 20], 1, 0, seed=41))
+@pytest.mark.parametrize("kv", [KV_BF16, KV_MLA656])
+def test_bad_page_long_length_and_foreign_meta(kv):
+    s = Step(_spec(kv, 3, 2, 128, 16, [100, 50, 20], 1, 0, seed=41))
     good = s.run().cpu()
     bad = s.dw.block_table.clone()
     bad[0, 2], bad[1, 1] = -1, s.w.num_pages
@@ -181,7 +201,7 @@ def test_nan_key_poisons_its_request_and_head_only():
             assert torch.isnan(v[1]).item() == (b == 0) and not torch.isnan(v[0]).item()
 
 
-@pytest.mark.parametrize("kv,H,s_q", [(KV_BF16, 2, 1), (KV_FP8, 2, 1), (KV_BF16, 1, 3)])
+@pytest.mark.parametrize("kv,H,s_q", [(KV_BF16, 2, 1), (KV_FP8, 2, 1), (KV_BF16, 1, 3), (KV_MLA656, 1, 2)])
 def test_rows_without_a_sum(kv, H, s_q):
     """An lse of -inf (nothing was seen) or +inf adds nothing, NaN poisons its KV head's weights and no other's."""
     s = Step(_spec(kv, 2, H, 128 if kv == KV_FP8 else 64, 16, [70, 45], s_q, 0, seed=71))
@@ -196,7 +216,12 @@ def test_rows_without_a_sum(kv, H, s_q):
 
 
 def test_captured_replayed_and_on_another_stream():
-    s = Step(_spec(KV_FP8, 3, 2, 128, 32, [200, 31, 90], 1, 0, seed=61), decay=0.5, weighted=[199, 30, 89])
+    for kv in (KV_FP8, KV_MLA656):
+        _captured(kv)
+
+
+def _captured(kv):
+    s = Step(_spec(kv, 3, 2, 128, 32, [200, 31, 90], 1, 0, seed=61), decay=0.5, weighted=[199, 30, 89])
     want = s.run()
     assert torch.equal(s.run(stream=torch.cuda.Stream()), want)
     wl = torch.tensor(s.weighted, dtype=torch.int32, device="cuda")
