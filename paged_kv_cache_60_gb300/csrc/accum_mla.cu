@@ -5,16 +5,26 @@
 // does: bf16(fp32(e4m3) * scale)) and 64 bf16.
 //
 // 147 thousand floating-point operations a token and query token against 656
-// bytes: the products bound it, not HBM. One CTA per SM holds the 128 x 576
-// query rows of one query token in shared memory, in the order in which the
-// warp MMA's B fragments want them (147 KB, one 8-byte read per lane and
-// fragment, no conflicts). A warp takes 32 tokens at a time: the rows go from
-// global memory straight into A fragments, every lane reading and dequantising
-// 16 contiguous values of a row (a dot product does not care which dims the k
-// index of an MMA stands for, as long as q and K agree), each B fragment feeds
-// the two 16-token tiles, and the 32 x 128 scores stay in registers until their
-// exponentials are summed. Several query tokens take one pass over the tokens
-// each, later ones adding to what the same lane stored before.
+// bytes: HBM and the bf16 tensor peak would take about the same time, so the
+// products run on the 5th-generation tensor cores, as
+//     S = K Q^T      M = 128 tokens, N = 128 heads, K = 576 dims: 36 MMAs,
+// with the tokens as rows: a token's scores then lie in one lane of tensor
+// memory, and the sum over its heads is one thread's. K is read once and needed
+// once, so it never becomes a shared-memory operand: raw rows come in by bulk
+// copies (whole runs of a page), are dequantised by the thread that has the
+// token's lane and stored to tensor memory as the A operand, in pieces of 64
+// dims. The 128 query rows of one query token stay in shared memory as B (147 KB)
+// for a whole pass; several query tokens take one pass over the tokens each.
+//
+// Roles (512 threads): warp 0 issues MMAs and owns the tensor memory; warp 1
+// copies rows, 32 tokens (a quarter of a unit of 128) at a time into the
+// quarter's buffer; warps 4-7 sum the exponentials of a finished S and update the
+// weights; warps 8-15 dequantise, two to a quarter, each one half of the dims:
+// a warp takes its part of the rows into registers, hands the buffer back, and
+// converts while the next rows arrive. The two halves have rings of four
+// operand slots of their own, and S has two buffers, so that every barrier is
+// waited on phase by phase by those who use it.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -27,191 +37,343 @@
 namespace da {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kHeads = 128;
-constexpr int kDim = 576, kNope = 512;
-constexpr int kRow = 656, kScales = 512, kRope = 528;
-constexpr int kSteps = kDim / 16;     // MMA steps
-constexpr int kNT = kHeads / 8;       // n tiles
-constexpr int kTok = 32;              // tokens of a warp's unit
-constexpr int kSmem = kSteps * kNT * 32 * 8 + kHeads * 4;
+constexpr int kThreads = 512;
+constexpr int kHeads = 128, kDim = 576;
+constexpr int kRow = 656, kScaleAt = 512, kRopeAt = 528;
+constexpr int kUnit = 128, kQuarter = 32;            // tokens
+constexpr int kQSlice = kHeads * 128;                // 64 dims of the query rows, 128-byte swizzle: 16 KB
+constexpr int kItems = 5;                            // operand pieces of a half per unit: four of 64 dims, one of 32
+constexpr int kSlots = 4;                            // operand slots of a half
+constexpr int kOffRaw = 9 * kQSlice;
+constexpr int kOffLse = kOffRaw + 4 * kQuarter * kRow;
+constexpr int kOffBars = kOffLse + kHeads * 4;
+constexpr int kBars = 4 + 4 + 2 * 2 * kSlots + 2 + 2 + 1;
+constexpr int kOffTmem = kOffBars + kBars * 8;
+constexpr int kSmem = kOffTmem + 16;                 // no slack: the base has to be 1024-byte aligned, see below
+static_assert(kSmem <= 232448, "shared memory budget");
+static_assert(kOffRaw % 1024 == 0 && kOffBars % 8 == 0, "alignment");
+// tensor memory (512 columns x 128 lanes; lane = token of the unit): S twice, then the operand slots (32 columns each)
+constexpr uint32_t kTmemCols = 512, kACol = 256;
 
-// Two e4m3 values (a 16-bit piece of w) times the scale, as two bf16.
-__device__ __forceinline__ uint32_t dequant2(uint32_t w, bool high, float scale) {
-    const uint32_t f = e4m3x2_to_f16x2((uint16_t)(high ? w >> 16 : w & 0xFFFFu));
-    const __half2 v = *reinterpret_cast<const __half2 *>(&f);
-    return pack_bf16(__low2float(v) * scale, __high2float(v) * scale);
+struct Bars {
+    uint64_t *rfull, *rempty;    // [quarter] raw rows
+    uint64_t *afull, *aempty;    // [half * kSlots + slot] operand pieces
+    uint64_t *sfull, *sempty;    // [2] scores
+    uint64_t *drain;
+};
+__device__ __forceinline__ Bars bars_at(uint8_t *smem) {
+    uint64_t *b = reinterpret_cast<uint64_t *>(smem + kOffBars);
+    return Bars{b, b + 4, b + 8, b + 8 + 2 * kSlots, b + 8 + 4 * kSlots, b + 10 + 4 * kSlots, b + 12 + 4 * kSlots};
 }
 
-// s += A B for one step of both tiles and all heads
-__device__ __forceinline__ void step(float (&s)[2][kNT][4], const uint32_t (&a)[2][4], const uint2 *qs, int lane) {
+// Untiled bulk copy of `bytes` (a multiple of 16) into shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// 16 e4m3 values times the scale, as 16 bf16 in eight words.
+__device__ __forceinline__ void dequant16(uint4 v, float scale, uint32_t *o) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-        const uint2 b = qs[nt * 32 + lane];
-        mma_bf16(s[0][nt], a[0], b.x, b.y);
-        mma_bf16(s[1][nt], a[1], b.x, b.y);
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = e4m3x2_to_f16x2((uint16_t)(w[k] & 0xFFFFu)), hi = e4m3x2_to_f16x2((uint16_t)(w[k] >> 16));
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        o[2 * k] = pack_bf16(__fmul_rn(a.x, scale), __fmul_rn(a.y, scale));
+        o[2 * k + 1] = pack_bf16(__fmul_rn(b.x, scale), __fmul_rn(b.y, scale));
     }
 }
+
+// One pass: query token j of a segment over its tokens. Units are dealt out to the CTAs of a part.
+struct Pass {
+    int b, L, j, nj;
+    int base, end;      // tokens [base, end)
+    int units;          // units of 128 of them that are this CTA's: u = z + Z k
+};
 
 __global__ void __launch_bounds__(kThreads, 1) accum_mla_kernel(const __grid_constant__ AccumParams p) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    uint2 *qs = reinterpret_cast<uint2 *>(smem);                                   // [step][n tile][lane]
-    float *lse2 = reinterpret_cast<float *>(smem + kSteps * kNT * 32 * 8);         // [head], +inf: adds nothing
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r8 = lane >> 2, c4 = lane & 3, Z = gridDim.z;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const Bars bar = bars_at(smem);
+    float *lse2 = reinterpret_cast<float *>(smem + kOffLse);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffTmem);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffTmem + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3;
+    const int Z = gridDim.z, z = blockIdx.z;
     const int part0 = blockIdx.x * p.parts_per_cta, part1 = min(part0 + p.parts_per_cta, p.num_parts);
+
+    const int P = p.page_size, bt = min(P, kQuarter), nb = kQuarter / bt;   // tokens of a copy, copies of a quarter
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bar.rfull[i], nb);
+            mbar_init(&bar.rempty[i], 2);
+        }
+        for (int i = 0; i < 2 * kSlots; ++i) {
+            mbar_init(&bar.afull[i], 4);
+            mbar_init(&bar.aempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.sfull[i], 1);
+            mbar_init(&bar.sempty[i], 4);
+        }
+        mbar_init(bar.drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 0) tmem_alloc(tmem_slot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
     pdl_wait();
     pdl_launch_dependents();
-    if (!meta_header_ok(load_meta_header(p.meta.header), p.B, p.H_kv, p.G, p.splits, p.num_parts, p.s_q, 0, 0)) {
-        if (tid == 0) atomicOr(&p.meta.header[kHError], DA_DEV_META_MISMATCH);
-        return;
-    }
-    const int max_len = p.max_pages * p.page_size;
-    for (int part = part0; part < part1; ++part) {
-        SegWalker wk = make_walker(p.meta, p.meta.parts[2 * part], p.meta.parts[2 * part + 1], p.B, p.seqlens, max_len,
-                                   p.s_q, 0, 0);
-        Seg sg;
-        while (wk.next(sg)) {
-            // tokens [lc0, lc1) * 64 of the request, 32 to a unit; the warps of the pair's CTAs share them
-            const int b = sg.b, L = sg.L, u0 = sg.lc0 * 2;
-            const int units = min((sg.lc1 - sg.lc0) * 2, (L - sg.lc0 * kChunk + kTok - 1) / kTok);
-            if (units <= 0) continue;
-            const int nj = p.accepted ? min(p.accepted[b], p.s_q - 1) + 1 : p.s_q;   // query tokens that count
-            const int wl = p.weighted ? p.weighted[b] : L;
-            const int32_t *table = p.block_table + (size_t)b * p.max_pages;
-            // (no query token counts: one pass all the same, for the decay)
-            for (int j = 0; j < max(nj, 1); ++j) {
-                const size_t row0 = ((size_t)b * p.s_q + j) * kHeads;
-                __syncthreads();  // the previous pass is done with q
-                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + row0 * kDim;
-                for (int i = tid; i < kHeads * 40; i += kThreads) {
-                    // head i / 40: 32 groups of 16 NoPE dims, then 8 groups of 8 RoPE dims
-                    const int head = i / 40, g = i - head * 40, nt = head >> 3, ln = (head & 7) * 4;
-                    if (g < 32) {
-                        const uint4 *src = reinterpret_cast<const uint4 *>(q + (size_t)head * kDim + g * 16);
-                        const uint4 x = src[0], y = src[1];
-                        uint2 *dst = qs + ((g >> 2) * 4 * kNT + nt) * 32 + ln + (g & 3);
-                        dst[0] = make_uint2(x.x, x.y);
-                        dst[kNT * 32] = make_uint2(x.z, x.w);
-                        dst[2 * kNT * 32] = make_uint2(y.x, y.y);
-                        dst[3 * kNT * 32] = make_uint2(y.z, y.w);
-                    } else {
-                        const int r = g - 32;
-                        const uint4 x = *reinterpret_cast<const uint4 *>(q + (size_t)head * kDim + kNope + r * 8);
-                        uint2 *dst = qs + ((32 + (r >> 2) * 2) * kNT + nt) * 32 + ln + (r & 3);
-                        dst[0] = make_uint2(x.x, x.y);
-                        dst[kNT * 32] = make_uint2(x.z, x.w);
+
+    const bool meta_ok =
+        meta_header_ok(load_meta_header(p.meta.header), p.B, p.H_kv, p.G, p.splits, p.num_parts, p.s_q, 0, 0);
+    // the query tiles' swizzle needs a 1024-byte aligned base (dynamic shared memory without static starts there)
+    const bool aligned = (smem_u32(smem) & 1023u) == 0;
+    if (tid == 0 && !meta_ok) atomicOr(&p.meta.header[kHError], DA_DEV_META_MISMATCH);
+    if (tid == 0 && !aligned) atomicOr(&p.meta.header[kHError], DA_DEV_TIMEOUT);
+    const int max_len = p.max_pages * P;
+    // every thread walks the same passes
+    int part = part0 - 1;
+    bool open = false;   // wk holds a part
+    SegWalker wk;
+    Seg sg;
+    Pass ps;
+    ps.j = ps.nj = 0;
+    const auto next_pass = [&]() -> bool {
+        if (ps.j + 1 < ps.nj) {
+            ++ps.j;
+            return true;
+        }
+        for (;;) {
+            while (!open || !wk.next(sg)) {
+                if (++part >= part1) return false;
+                wk = make_walker(p.meta, p.meta.parts[2 * part], p.meta.parts[2 * part + 1], p.B, p.seqlens, max_len,
+                                 p.s_q, 0, 0);
+                open = true;
+            }
+            ps.base = sg.lc0 * kChunk;
+            ps.end = min(sg.lc1 * kChunk, sg.L);
+            const int all = (ps.end - ps.base + kUnit - 1) / kUnit;
+            ps.units = all > z ? (all - z + Z - 1) / Z : 0;
+            if (ps.units > 0) break;
+        }
+        ps.b = sg.b;
+        ps.L = sg.L;
+        ps.j = 0;
+        // query tokens that count; where none does, one pass all the same, for the decay
+        ps.nj = p.accepted ? min(p.accepted[ps.b], p.s_q - 1) + 1 : p.s_q;
+        return true;
+    };
+    const auto unit_base = [&](int k) { return ps.base + (z + k * Z) * kUnit; };
+
+    bool ok = true;
+    int done = 0, pass = 0;         // units and passes so far
+    const auto give_up = [&]() {
+        if (lane == 0) {
+            atomicOr(&p.meta.header[kHError], DA_DEV_TIMEOUT);
+            *abort_flag = 1;
+        }
+        ok = false;
+    };
+    const auto wait = [&](uint64_t *b, uint32_t parity) -> bool {
+        if (ok && !mbar_wait_warp_ool(b, parity, abort_flag, p.wait_limit_ns)) give_up();
+        return ok;
+    };
+    int issued = 0;                 // producer: quarters whose copies this lane has issued
+    const uint64_t pol = policy_evict_first();
+    const uint64_t dq = umma_desc(smem_u32(smem), 16, 1024);
+    constexpr uint32_t kIdesc = umma_idesc_bf16(128, 128, 0, 0);
+    const uint32_t trow = tmem + ((uint32_t)(32 * quad) << 16);
+
+    while (meta_ok && aligned && next_pass()) {
+        // all roles are done with the last pass (the MMA warp has seen its products complete)
+        if (__syncthreads_or(*abort_flag != 0)) break;
+        {
+            const size_t row0 = ((size_t)ps.b * p.s_q + ps.j) * kHeads;
+            const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + row0 * kDim);
+            for (int i = tid; i < kHeads * (kDim / 8); i += kThreads) {
+                const int head = i / (kDim / 8), c = i - head * (kDim / 8);
+                *reinterpret_cast<uint4 *>(smem + (c >> 3) * kQSlice + head * 128 + (((c & 7) ^ (head & 7)) << 4)) = q[i];
+            }
+            if (tid < kHeads) {
+                const float l = p.lse[row0 + tid];
+                lse2[tid] = l == -INFINITY || ps.j >= ps.nj ? INFINITY : l * 1.4426950408889634f;
+            }
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        const int32_t *table = p.block_table + (size_t)ps.b * p.max_pages;
+        const auto page_at = [&](int t) -> int {
+            return t < ps.end ? __ldg(table + (p.log2_page >= 0 ? t >> p.log2_page : t / P)) : -2;
+        };
+        const auto slot_at = [&](int t) { return p.log2_page >= 0 ? t & (P - 1) : t % P; };
+        if (warp == 0) {
+            // -------------------------------------------------------- MMA issuer
+            for (int k = 0; k < ps.units && ok; ++k) {
+                const int n = done + k, d = n & 1;
+                if (!wait(&bar.sempty[d], ((n >> 1) & 1) ^ 1)) break;
+                tc_fence_after();
+                for (int o = 0; o < kItems && ok; ++o) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int m = n * kItems + o, slot = half * kSlots + (m & (kSlots - 1));
+                        if (!wait(&bar.afull[slot], (uint32_t)(m / kSlots) & 1u)) break;
+                        tc_fence_after();
+                        const uint32_t a = tmem + kACol + 32 * slot;
+                        const int slice = o < 4 ? half * 4 + o : 8, first = o < 4 ? 0 : 2 * half;
+                        const uint64_t b = dq + (uint64_t)((slice * kQSlice) >> 4) + 2 * first;
+                        for (int i = 0; i < (o < 4 ? 4 : 2); ++i)
+                            umma_bf16_tmem_a_w(tmem + 128 * d, a + 8 * i, b + 2 * i, kIdesc, !(o == 0 && half == 0 && i == 0));
+                        umma_commit_w(&bar.aempty[slot]);
                     }
                 }
-                for (int i = tid; i < kHeads; i += kThreads) {
-                    const float l = p.lse[row0 + i];
-                    lse2[i] = l == -INFINITY || j >= nj ? INFINITY : l * 1.4426950408889634f;
-                }
-                __syncthreads();
-                const int last = L - p.s_q + j;   // last token that query token j sees
-                for (int u = blockIdx.z * kWarps + warp; u < units; u += kWarps * Z) {
-                    const int t0 = (u0 + u) * kTok;
-                    // the four rows of this lane: tokens t0 + 8 k + r8 (a group of eight lies in one page)
-                    const uint8_t *row[4];
-                    float *wp = nullptr;
-                    float old = 0.f;
+                if (ok) umma_commit_w(&bar.sfull[d]);
+            }
+            // every product has read its operands before the query rows are replaced or the tensor memory goes away
+            umma_commit_w(bar.drain);
+            if (!mbar_wait_timed(bar.drain, (uint32_t)pass & 1u, 100000000ull)) give_up();
+        } else if (warp == 1) {
+            // -------------------------------------------------------- rows into the quarters' buffers
+            if (lane < nb) {
+                int id[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int tg = t0 + 8 * k, t = tg + r8;
-                        const int pi = p.log2_page >= 0 ? tg >> p.log2_page : tg / p.page_size;
-                        int pg = tg < L ? table[pi] : -2;
+                for (int c = 0; c < 4; ++c) id[c] = page_at(unit_base(0) + c * kQuarter + lane * bt);
+                for (int k = 0; k < ps.units && ok; ++k) {
+                    const int n = done + k;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        int pg = id[c];
+                        const int t = unit_base(k) + c * kQuarter + lane * bt;
+                        if (k + 1 < ps.units) id[c] = page_at(unit_base(k + 1) + c * kQuarter + lane * bt);
+                        if (!mbar_wait_bounded(&bar.rempty[c], ((uint32_t)n & 1u) ^ 1u, abort_flag, p.wait_limit_ns)) {
+                            atomicOr(&p.meta.header[kHError], DA_DEV_TIMEOUT);
+                            *abort_flag = 1;
+                            ok = false;
+                            break;
+                        }
                         if (pg != -2 && (uint32_t)pg >= (uint32_t)p.num_pages) {
-                            if (lane == 0) {
-                                atomicOr(&p.meta.header[kHError], DA_DEV_BAD_PAGE);
-                                p.meta.header[kHErrorDetail] = pg;
-                            }
-                            pg = -2;
+                            atomicOr(&p.meta.header[kHError], DA_DEV_BAD_PAGE);
+                            p.meta.header[kHErrorDetail] = pg;
+                            pg = -2;  // skipped: its rows keep stale bytes, its weights stay
                         }
-                        const size_t slot = (size_t)max(pg, 0) * p.page_size + (tg - pi * p.page_size) + r8;
-                        row[k] = pg >= 0 && t < L ? p.k_pool + slot * kRow : nullptr;
-                        if (k == c4 && row[k]) {
-                            wp = p.weights + slot;     // one KV head: [page][slot]
-                            old = j > 0 ? *wp : t < wl ? *wp * p.decay : 0.f;
-                        }
+                        mbar_arrive_expect_tx(&bar.rfull[c], pg < 0 ? 0u : (uint32_t)(bt * kRow));
+                        if (pg >= 0)
+                            bulk_load(smem + kOffRaw + (c * kQuarter + lane * bt) * kRow,
+                                      p.k_pool + ((size_t)pg * P + slot_at(t)) * kRow, (uint32_t)(bt * kRow),
+                                      &bar.rfull[c], pol);
+                        ++issued;
                     }
-                    float s[2][kNT][4];
+                }
+            }
+            __syncwarp();
+        } else if (warp >= 4 && warp < 8) {
+            // -------------------------------------------------------- sums and weights: one token a thread
+            const int own = quad * 32 + lane;
+            const int last = ps.L - p.s_q + ps.j;    // last token that query token j sees
+            const int wl = p.weighted ? p.weighted[ps.b] : ps.L;
+            const auto weight_at = [&](int t, int pg) -> float * {
+                return (uint32_t)pg < (uint32_t)p.num_pages ? p.weights + (size_t)pg * P + slot_at(t) : nullptr;
+            };
+            const auto old_at = [&](int t, const float *w) -> float {
+                return !w ? 0.f : ps.j > 0 ? *w : t < wl ? *w * p.decay : 0.f;   // later passes add to the first
+            };
+            bool off = false;                        // some head adds nothing
+            for (int h = lane; h < kHeads; h += 32) off |= lse2[h] == INFINITY;
+            off = __any_sync(0xffffffffu, off);
+            int pg = page_at(unit_base(0) + own);
+            for (int k = 0; k < ps.units && ok; ++k) {
+                const int n = done + k, d = n & 1, t = unit_base(k) + own;
+                float *w = weight_at(t, pg);
+                const float old = old_at(t, w);
+                if (k + 1 < ps.units) pg = page_at(unit_base(k + 1) + own);
+                if (!wait(&bar.sfull[d], (uint32_t)(n >> 1) & 1u)) break;
+                tc_fence_after();
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t s[64];
+                    tmem_ld64_sync(trow + 128 * d + 64 * half, s);
+                    if (half == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.sempty[d]);
+                    }
 #pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt) s[m][nt][0] = s[m][nt][1] = s[m][nt][2] = s[m][nt][3] = 0.f;
-                    // vector v of a row: bytes [64 v, 64 v + 64) of it, this lane 16 of them; the RoPE part 128 bytes
-                    const auto get = [&](int k, int at) -> uint4 {
-                        return row[k] ? ldg_stream16(row[k] + at) : make_uint4(0u, 0u, 0u, 0u);
-                    };
-                    uint4 next[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) next[k] = get(k, c4 * 16);
-#pragma unroll 1
-                    for (int x = 0; x < 8; ++x) {
-                        uint4 v[4];
-                        float sc[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            v[k] = next[k];
-                            sc[k] = row[k] ? __ldg(reinterpret_cast<const float *>(row[k] + kScales) + (x >> 1)) : 0.f;
-                            next[k] = get(k, x < 7 ? (x + 1) * 64 + c4 * 16 : kRope + c4 * 16);
-                        }
+                    for (int h = 0; h < 64; h += 4) {
+                        const float4 l = *reinterpret_cast<const float4 *>(lse2 + 64 * half + h);
+                        const float ls[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            uint32_t a[2][4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t w = i == 0 ? v[k].x : i == 1 ? v[k].y : i == 2 ? v[k].z : v[k].w;
-                                a[k >> 1][k & 1] = dequant2(w, false, sc[k]);
-                                a[k >> 1][2 + (k & 1)] = dequant2(w, true, sc[k]);
-                            }
-                            step(s, a, qs + (x * 4 + i) * kNT * 32, lane);
+                            const float e = ex2(fmaf(__uint_as_float(s[h + i]), p.scale_log2, -ls[i]));
+                            sum[i] += off && ls[i] == INFINITY ? 0.f : e;
                         }
                     }
+                }
+                const float add = t <= last ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
+                if (w) *w = old + add;
+            }
+        } else if (warp >= 8) {
+            // -------------------------------------------------------- dequantise: one token a thread, half of its dims
+            const int half = (warp - 8) >> 2;
+            const uint8_t *row = smem + kOffRaw + (quad * kQuarter + lane) * kRow;
+            for (int k = 0; k < ps.units && ok; ++k) {
+                const int n = done + k;
+                if (!wait(&bar.rfull[quad], (uint32_t)n & 1u)) break;
+                uint4 v[16], r[4];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        uint4 v[4];
+                for (int i = 0; i < 16; ++i) v[i] = *reinterpret_cast<const uint4 *>(row + half * 256 + 16 * i);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            v[k] = next[k];
-                            if (y == 0) next[k] = get(k, kRope + 64 + c4 * 16);
-                        }
+                for (int i = 0; i < 4; ++i) r[i] = *reinterpret_cast<const uint4 *>(row + kRopeAt + half * 64 + 16 * i);
+                const float2 sc = *reinterpret_cast<const float2 *>(row + kScaleAt + 8 * half);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.rempty[quad]);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t a[2][4];
+                for (int o = 0; o < kItems; ++o) {
+                    const int m = n * kItems + o, slot = half * kSlots + (m & (kSlots - 1));
+                    uint32_t x[2][16];
+                    if (o < 4) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                a[k >> 1][k & 1] = i ? v[k].z : v[k].x;
-                                a[k >> 1][2 + (k & 1)] = i ? v[k].w : v[k].y;
-                            }
-                            step(s, a, qs + (32 + y * 2 + i) * kNT * 32, lane);
+                        for (int i = 0; i < 4; ++i) dequant16(v[4 * o + i], o < 2 ? sc.x : sc.y, &x[i >> 1][8 * (i & 1)]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            x[0][4 * i] = r[i].x, x[0][4 * i + 1] = r[i].y;
+                            x[0][4 * i + 2] = r[i].z, x[0][4 * i + 3] = r[i].w;
                         }
                     }
-                    // a row that does not see the token adds nothing, whatever its score
-                    float e[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int nt = 0; nt < kNT; ++nt) {
-                        const float2 l = *reinterpret_cast<const float2 *>(lse2 + nt * 8 + 2 * c4);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float x = ex2(fmaf(s[k >> 1][nt][2 * (k & 1)], p.scale_log2, -l.x));
-                            const float y = ex2(fmaf(s[k >> 1][nt][2 * (k & 1) + 1], p.scale_log2, -l.y));
-                            e[k] += (l.x == INFINITY ? 0.f : x) + (l.y == INFINITY ? 0.f : y);
-                        }
-                    }
-                    float mine = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (t0 + 8 * k + r8 > last) e[k] = 0.f;
-                        e[k] += __shfl_xor_sync(0xffffffffu, e[k], 1);
-                        e[k] += __shfl_xor_sync(0xffffffffu, e[k], 2);
-                        if (k == c4) mine = e[k];
-                    }
-                    if (wp) *wp = old + mine;
+                    if (!wait(&bar.aempty[slot], ((uint32_t)(m / kSlots) & 1u) ^ 1u)) break;
+                    tc_fence_after();
+                    tmem_st16(trow + kACol + 32 * slot, x[0]);
+                    if (o < 4) tmem_st16(trow + kACol + 32 * slot + 16, x[1]);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.afull[slot]);
                 }
             }
         }
+        done += ps.units;
+        ++pass;
     }
+    __syncthreads();
+    if (*abort_flag && warp == 1 && lane < nb) {
+        // copies that were issued land before the CTA exits: at most one a quarter is in flight
+        for (int c = 0; c < 4; ++c) {
+            const int mine = (issued + 3 - c) / 4;   // copies of quarter c
+            if (mine) mbar_wait_timed(&bar.rfull[c], (uint32_t)(mine - 1) & 1u, 100000000ull);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
 }  // namespace
