@@ -114,6 +114,10 @@ CASES = [
     (KV_MLA656, 4, 1, 576, 16, [0, 1, 31, 300], 1, 0),
     (KV_MLA656, 3, 1, 576, 8, [33, 97, 5], 2, 3),
     (KV_MLA656, 2, 1, 576, 192, [200, 64], 4, 1),
+    (KV_MLA656, 1, 1, 576, 64, [2500], 1, 1),            # several units of a cache to a CTA, one of them ragged
+    (KV_MLA656, 2, 1, 576, 32, [1301, 770], 3, 1),       # and a pass for each query token
+    (KV_MLA656, 40, 1, 576, 16, [(53 * i) % 300 for i in range(40)], 1, 8),   # several parts to a CTA
+    (KV_MLA656, 100, 1, 576, 8, [(29 * i) % 140 for i in range(100)], 2, 0),  # several requests to a part
     (KV_BF16, 3, 4, 64, 192, [385, 100, 1], 1, 0),       # two heads to a CTA
     (KV_BF16, 3, 3, 64, 16, [85, 0, 230], 1, 0),         # an odd number of them
     (KV_FP8, 2, 3, 128, 16, [200, 77], 1, 2),

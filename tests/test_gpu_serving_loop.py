@@ -120,3 +120,73 @@ def test_steps_with_verification_accumulation_and_eviction(H_kv, D, P, s_q):
             lens = cut.tolist()
             weighted = lens
     assert chosen                                         # some request was over its budget
+
+
+def test_latent_steps_with_accumulation_and_eviction():
+    """The same on the 656-byte format: the weights that its eviction goes by come from its own attention."""
+    B, P, cols, s_q, budget, dev = 2, 16, 12, 2, 100, "cuda"
+    g = torch.Generator().manual_seed(5)
+    num_pages = 2 * B * cols
+    perm = torch.randperm(num_pages, generator=g).int()
+    table, spare = perm[:B * cols].view(B, cols).clone().cuda(), perm[B * cols:].view(B, cols).clone().cuda()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    pool = torch.full((num_pages, P, 1, 656), 0xFF, dtype=torch.uint8, device=dev)
+    weights = torch.full((num_pages, 1, P), math.nan, device=dev)
+    rope, freq = da.Rope.make(64), (1000.0 ** (-torch.arange(32) / 32)).float().cuda()
+    desc = da.Desc.make(B=B, H_kv=1, G=128, D_qk=576, D_v=512, page_size=P, max_pages_per_seq=cols, num_pages=num_pages,
+                        kv_dtype=da.KV_MLA656, s_q=s_q)
+    meta, err = torch.empty(da.sched_meta_bytes(desc), dtype=torch.uint8, device=dev), i32([0])
+
+    def append(req, pos):
+        n = len(req)
+        x = torch.randn(n, 129 * 576, generator=g).to(torch.bfloat16).cuda()
+        q_out = torch.empty(n, 128, 576, dtype=torch.bfloat16, device=dev)
+        da.rope_append(desc, rope, x[:, :128 * 576], x[:, 128 * 576:], None, freq, i32([pos]), i32(pos), table, q_out, pool,
+                       None, requests=i32(req), device_error=err)
+        return q_out
+
+    def rows(tab, L):
+        raw = pool[tab[:-(-L // P)].long()].flatten(0, 2)[:L].cpu()
+        scale = raw[:, 512:528].contiguous().view(torch.float32).repeat_interleave(128, -1)
+        nope = (raw[:, :512].contiguous().view(torch.float8_e4m3fn).float() * scale).to(torch.bfloat16).double()
+        return torch.cat([nope, raw[:, 528:].contiguous().view(torch.bfloat16).double()], -1), raw
+
+    lens, weighted = [150, 61], [0, 0]
+    append([b for b in range(B) for _ in range(lens[b])], [t for b in range(B) for t in range(lens[b])])
+    for step in range(3):
+        q = append([b for b in range(B) for _ in range(s_q)], [lens[b] + j for b in range(B) for j in range(s_q)])
+        q = q.view(B, s_q, 128, 576)
+        lens = [n + s_q for n in lens]
+        seq, before = i32(lens), weights.cpu().double()
+        out, lse = torch.empty(B, s_q, 128, 512, dtype=torch.bfloat16, device=dev), torch.empty(B, s_q, 128, device=dev)
+        da.sched_meta(desc, seq, meta)
+        da.fwd(desc, q, pool, None, None, None, table, seq, meta, out, lse)
+        da.accum_weights(desc, q, pool, None, table, seq, meta, lse, weights, weighted_lens=i32(weighted), decay=0.5)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and da.get_error(meta) == 0
+        for b in range(B):
+            k, _ = rows(table[b], lens[b])
+            add = torch.zeros(lens[b], dtype=torch.float64)
+            for j in range(s_q):
+                n = lens[b] - s_q + 1 + j
+                s = q[b, j].double().cpu() @ k[:n].T / 24.0
+                assert (lse[b, j].cpu().double() - s.logsumexp(-1)).abs().max() <= LSE_TOL
+                assert (out[b, j].cpu().double() - s.softmax(-1) @ k[:n, :512]).abs().max() <= OUT_TOL
+                add[:n] += (s - lse[b, j].cpu().double()[:, None]).exp().sum(0)
+            for t in range(lens[b]):
+                at = (int(table[b, t // P]), 0, t % P)
+                old = float(before[at]) / 2 if t < weighted[b] else 0.0
+                assert math.isclose(float(weights[at]), old + float(add[t]), rel_tol=1e-4)
+        weighted = lens
+        if step == 1:
+            kept, cut = torch.empty(B, 1, budget, dtype=torch.int32, device=dev), i32([0] * B)
+            was = [weights.cpu()[table[b].cpu().long(), 0].flatten()[:lens[b]] for b in range(B)]
+            old = [rows(table[b], lens[b])[1] for b in range(B)]
+            da.evict(desc, budget, seq, table, spare, pool, None, weights, kept, cut, keep_first=2, keep_last=6, device_error=err)
+            torch.cuda.synchronize()
+            assert int(err.item()) == 0 and cut.tolist() == [min(n, budget) for n in lens]
+            for b in range(B):
+                want = evict_select(was[b].numpy(), budget, 2, 6)
+                assert kept[b, 0, :len(want)].tolist() == want
+                assert torch.equal(rows(spare[b], int(cut[b]))[1], old[b][want])
+            table, spare, lens, weighted = spare, table, cut.tolist(), cut.tolist()
