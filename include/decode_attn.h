@@ -326,7 +326,8 @@ int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_
  *             + sum_j sum_g exp(sigma * q_{b,j,hG+g} . k_t - lse[b,j,hG+g])
  * over the query tokens j <= num_accepted[b] that see t (t <= L_b - s_q + j).
  * (No counterpart on the source pages.) All three formats; no sliding window
- * and no sparse decode (DA_ERR_UNSUPPORTED).
+ * and no sparse decode (DA_ERR_UNSUPPORTED). On the 656-byte format
+ * max_pages_per_seq * page_size may be 2^31 - 257 at most.
  *   desc, q, k_pool, k_scale, block_table, cache_seqlens, sched_meta, lse: those
  *     of the step's decode_attn_fwd call, with the same requirements; sinks
  *     need no argument (they are in lse). Page errors go to sched_meta's word.

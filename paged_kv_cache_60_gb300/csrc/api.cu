@@ -670,6 +670,8 @@ int decode_attn_accum_weights(const da_desc *desc, const void *q, const void *k_
     const int rc = make_layout(desc, &L);
     if (rc) return rc;
     if (desc->window != 0 || desc->topk != 0) return DA_ERR_UNSUPPORTED;
+    // token indices run past the last one by less than the kernel's unit
+    if (is_mla(desc) && (int64_t)desc->max_pages_per_seq * desc->page_size > (int64_t)INT32_MAX - 256) return DA_ERR_DIMS;
     if (!(decay >= 0.f) || std::isinf(decay)) return DA_ERR_DIMS;
     const bool fp8 = desc->kv_dtype == DA_KV_FP8_PER_TENSOR;
     if (!q || !k_pool || !block_table || !cache_seqlens || !sched_meta || !lse || !weights) return DA_ERR_NULL;

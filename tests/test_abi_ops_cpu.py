@@ -85,6 +85,8 @@ def test_accum_weights_refusals(lib):
     assert call(_desc(D_qk=96, D_v=96), n=1 << 30) == -3 and call(_desc(s_q=5), n=1 << 30) == -3
     assert call(_desc(num_pages=1 << 28), n=1 << 30) == -2
     assert call(_latent(num_sms=2, topk=64), n=1 << 30) == -3                 # sparse decode
+    long = [_latent(num_sms=2, B=1, page_size=64, max_pages_per_seq=(1 << 25) - k) for k in (2, 5)]
+    assert call(long[0], q=None) == -2 and call(long[1], q=None) == -1        # token indices end below 2^31 - 256
 
 
 def test_evict_refusals(lib):
