@@ -47,6 +47,7 @@ class Case:
         n = (self.num_pages, H, P)
         self.weights = {"spread": lambda: np.exp(r.standard_normal(n) * 3 - 5), "zero": lambda: np.zeros(n),
                         "few": lambda: r.integers(0, 4, n) / 4, "fine": lambda: 1 + r.integers(0, 50, n) * 2.0 ** -23,
+                        "tied": lambda: 1 + r.integers(0, 400, n) / 2048, "close": lambda: 1 + r.integers(0, 400, n) / 2048 + r.integers(0, 7, n) * 2.0 ** -23,
                         "wild": lambda: r.choice([0.0, -0.0, 1.0, -1.0, math.inf, -math.inf, math.nan, 1e-40, -1e-40, 3e38], n),
                         }[kind]().astype(np.float32)
 
@@ -100,6 +101,27 @@ def test_evict(case, kind):
 def test_long_rows_are_shared_by_a_cluster(lens, P, kind):
     """Lengths at which two, four, eight and sixteen CTAs select together, one request far shorter than the table allows."""
     Case(MLA, 1, 576, P, lens, 2003, 3, 64, kind=kind, seed=len(lens) + P).check()
+
+
+@pytest.mark.parametrize("kind", ["tied", "close"])
+@pytest.mark.parametrize("lens", [[20000], [80000], [100001, 60000], [8000]])
+def test_the_last_kept_among_a_few_near_equals(lens, kind):
+    """About 20 to 250 tokens of a row share the upper bits of the last weight kept, in one CTA and over clusters."""
+    Case(MLA, 1, 576, 64, lens, 3011, 2, 17, kind=kind, seed=len(lens)).check()
+
+
+@pytest.mark.parametrize("near", [1, 2, 255, 256, 257, 300])
+@pytest.mark.parametrize("n", [1200, 21000])
+def test_counts_of_near_equals_about_what_is_compared_directly(n, near):
+    c = Case(BF16, 1, 64, 64, [n], 600, 0, 0, seed=near + n)
+    w = np.zeros(n, np.float32)
+    r = np.random.default_rng(near)
+    order = r.permutation(n)
+    w[order[:near]] = 1 + r.integers(0, 60, near) * np.float32(2.0 ** -23)       # one 20-bit prefix
+    w[order[near:near + 600 - (near + 1) // 2]] = 2 + r.random(600 - (near + 1) // 2)   # and the budget ends among them
+    for t in range(n):
+        c.weights[c.table[0, t // 64], 0, t % 64] = w[t]
+    c.check()
 
 
 def test_a_share_beyond_shared_memory():
