@@ -288,10 +288,15 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D,
             for (int e = 0; e < HP; ++e) add[e][0] = add[e][1] = 0.f;
             // the chunk's products with the first NJ query tokens: one build for each count
             const auto products = [&](auto count) {
-                constexpr int NJ = decltype(count)::value, TT = NJ == 1 ? 4 : 2;  // TT: tiles in registers at a time
+                // TT: tiles in registers at a time. The e4m3 build for three and four query tokens, whose code with the
+                // conversions is the longest, takes one tile in a loop: unrolled it waits for instructions (32 x 8192
+                // tokens of 8 heads: 89 us against 71 for four query tokens, 74 against 55 for three; two tiles in a
+                // loop 75 and 63)
+                constexpr bool kLoop = FP8 && NQ > 2;
+                constexpr int NJ = decltype(count)::value, TT = NJ == 1 && !kLoop ? 4 : kLoop && NJ > 2 ? 1 : 2;
 #pragma unroll
                 for (int e = 0; e < HP; ++e) {
-#pragma unroll
+#pragma unroll(kLoop ? 1 : 4 / TT)
                     for (int tt = 0; tt < 4; tt += TT) {
                         float s[TT][NJ][4];
 #pragma unroll
