@@ -237,3 +237,24 @@ def _captured(kv):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(weights.view(torch.int32), want.view(torch.int32))
+
+
+def test_calls_at_once_on_three_streams():
+    """Accumulations of three formats at the same time, with the attention calls of the same steps between them."""
+    steps = [Step(_spec(kv, 3, 2, 128, 32, [900, 31, 2000], 2, 0, seed=81 + kv)) for kv in (KV_BF16, KV_FP8, KV_MLA656)]
+    want = [s.run() for s in steps]
+    streams = [torch.cuda.Stream() for _ in steps]
+    got = [s.weights.cuda() for s in steps]
+    out, lse = [torch.empty_like(s.out) for s in steps], [torch.empty_like(s.lse) for s in steps]
+    torch.cuda.synchronize()
+    for rep in range(4):
+        for s, st, w, o, l in zip(steps, streams, got, out, lse):
+            d = s.dw
+            with torch.cuda.stream(st):
+                da.fwd(s.desc, d.q, d.k_pool, d.v_pool, d.k_scale, d.v_scale, d.block_table, d.cache_seqlens, s.meta, o, l)
+                w.copy_(s.weights.cuda())
+                da.accum_weights(s.desc, d.q, d.k_pool, d.k_scale, d.block_table, d.cache_seqlens, s.meta, l, w)
+    torch.cuda.synchronize()
+    for s, g, w, l in zip(steps, got, want, lse):
+        assert torch.equal(l, s.lse) and torch.equal(g.view(torch.int32), w.view(torch.int32))
+        assert da.get_error(s.meta) == 0
