@@ -22,7 +22,7 @@
 // After two digits a few tokens are usually left in the row: where they are at
 // most 256, their keys are brought together and compared with each other, one
 // exchange in a cluster instead of the third digit's three (two latent caches of
-// 115 thousand tokens, sixteen CTAs each: 30.1 us for the call against 32.9, with
+// 115 thousand tokens, sixteen CTAs each: 29.5 us for the call against 32.9, with
 // the first digit's 256 bins read by every CTA instead of shared out).
 // The counts of heavier and of equal tokens in the lower shares then give every
 // CTA its place in the list, and ballots keep the order within it. No atomic
@@ -49,7 +49,7 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins0 = 256, kBins = 4096;   // bins of the first digit, and of the two others
 constexpr int kFew = 256;       // tokens left after two digits that are compared with each other instead of a third
-static_assert(2 * kFew + 2 <= kBins && kFew <= kSelThreads, "their keys lie where the third digit's counts would");
+static_assert(3 * kFew + 2 <= kBins && kFew <= kSelThreads, "their keys lie where the third digit's counts would");
 constexpr int kKeyCap = 36864;  // keys a CTA keeps in shared memory (144 KB); later ones are read again from the pool
 
 __device__ __forceinline__ int page_index(int t, int page_size, int log2_page) {
@@ -227,9 +227,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
         }
     };
 
+    // each warp has a contiguous run of this CTA's share, 128 keys at a time
+    const int per = (n + kSelWarps * 128 - 1) / (kSelWarps * 128) * 128;
+    const int w0 = (int)min((int64_t)n, (int64_t)warp * per), w1 = min(n, w0 + per);
+
     // digits of 8, 12 and 12 bits, highest first
     uint32_t prefix = 0, mask = 0, local_above = 0, at = (uint32_t)M;
-    uint32_t gt_before = 0, eq_before = 0;   // tokens above / at the last kept key in the lower shares
+    uint32_t gt_before = 0, eq_before = 0;   // tokens above / at the last kept key in the lower shares (and runs)
     bool few = false;
 #pragma unroll
     for (int d = 0; d < 3; ++d) {
@@ -238,20 +242,38 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
         uint32_t *hist = d == 0 ? s.hist0 : s.hist[d - 1];
         if (d == 2 && at <= (uint32_t)kFew) {
             // few tokens are left in the row: their keys are brought together (in any order, only counts are taken
-            // from them), and each is compared with all
-            uint32_t *own = s.hist[1], *all = kC > 1 ? own + kFew : own, *head = own + 2 * kFew;   // head: count, above
-            for (int i = 4 * tid; i < n; i += 4 * kSelThreads) {
+            // from them), and each is compared with all; what is above them is counted run by run on the way
+            uint32_t *own = s.hist[1], *all = kC > 1 ? own + kFew : own, *run = own + 2 * kFew;
+            uint32_t *head = own + 3 * kFew;   // this CTA's count of them, and of the tokens above them
+            uint32_t gt = 0;
+            for (int i = w0 + 4 * lane; i < w1; i += 128) {
                 uint32_t k[4];
                 keys4(i, k);
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (i + u < n && (k[u] & mask) == prefix) own[atomicAdd(head, 1u)] = k[u];
+                for (int u = 0; u < 4; ++u) {
+                    const bool in = i + u < w1;
+                    gt += in && (k[u] & mask) > prefix;
+                    if (in && (k[u] & mask) == prefix) {
+                        const uint32_t slot = atomicAdd(head, 1u);
+                        own[slot] = k[u];
+                        run[slot] = warp;
+                    }
+                }
             }
-            if (tid == 0) head[1] = local_above;
+            gt = __reduce_add_sync(0xffffffffu, gt);
+            if (lane == 0) s.wgt[warp] = gt;
+            __syncthreads();
             uint32_t lower = 0;                          // of them, those of lower shares
             if constexpr (kC > 1) {
-                __syncwarp();
+                if (warp == 0) {
+                    gt = sum_below(s.wgt, kSelWarps, lane);
+                    if (lane == 0) head[1] = gt;
+                    __syncwarp();
+                }
                 cluster_sync_all();  // every CTA's keys and counts
+                static_assert(kC <= kSelWarps, "a warp copies the keys of one rank");
+                uint32_t first = 0;                      // (as if there were 32: one latency instead of two)
+                if (warp < kC) first = ld_cluster_u32(mapa_shared(smem_u32(own + lane), warp));
                 uint32_t count = 0, above = 0;           // lane r: rank r's
                 if (lane < kC) {
                     count = ld_cluster_u32(mapa_shared(smem_u32(head), lane));
@@ -259,15 +281,17 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
                 }
                 gt_before = __reduce_add_sync(0xffffffffu, lane < rank ? above : 0u);
                 lower = __reduce_add_sync(0xffffffffu, lane < rank ? count : 0u);
-                static_assert(kC <= kSelWarps, "a warp copies the keys of one rank");
                 const uint32_t to = __reduce_add_sync(0xffffffffu, lane < warp ? count : 0u);
                 const int from = __shfl_sync(0xffffffffu, count, warp);
-                if (warp < kC)
-                    for (int i = lane; i < from; i += 32) all[to + i] = ld_cluster_u32(mapa_shared(smem_u32(own + i), warp));
+                if (warp < kC) {
+                    if (lane < from) all[to + lane] = first;
+                    for (int i = lane + 32; i < from; i += 32)
+                        all[to + i] = ld_cluster_u32(mapa_shared(smem_u32(own + i), warp));
+                }
                 __syncwarp();
                 cluster_arrive_all();  // done with the other CTAs' memory; waited for before the exit
+                __syncthreads();
             }
-            __syncthreads();
             if (tid < (int)at) {
                 const uint32_t k = all[tid];
                 uint32_t over = 0, same = 0;
@@ -284,11 +308,17 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
             prefix = s.digit;
             want -= s.above;
             uint32_t over = 0, same = 0;
-            for (int i = lane; i < (int)lower; i += 32) {
-                over += all[i] > prefix;
-                same += all[i] == prefix;
+            if (kC > 1) {
+                for (int i = lane; i < (int)lower; i += 32) {
+                    over += all[i] > prefix;
+                    same += all[i] == prefix;
+                }
             }
-            gt_before += __reduce_add_sync(0xffffffffu, over);
+            for (int i = lane; i < (int)head[0]; i += 32) {
+                over += run[i] < warp && own[i] > prefix;
+                same += run[i] < warp && own[i] == prefix;
+            }
+            gt_before += __reduce_add_sync(0xffffffffu, over) + sum_below(s.wgt, warp, lane);
             eq_before = __reduce_add_sync(0xffffffffu, same);
             few = true;
             break;
@@ -402,7 +432,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
         const uint32_t digit = s.digit;
         want -= s.above;
         at = s.at;
-        if (kC > 1) {  // this CTA's tokens above the digit
+        if (kC > 1 && (d != 1 || at > (uint32_t)kFew)) {  // this CTA's tokens above the digit
             uint32_t mine = 0;
             for (int i = digit + 1 + tid; i < bins; i += kSelThreads) mine += hist[i];
             mine = __reduce_add_sync(0xffffffffu, mine);
@@ -429,28 +459,28 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
         eq_before = __reduce_add_sync(0xffffffffu, eq_before);
         cluster_arrive_all();  // done with the other CTAs' memory; waited for before the exit
     }
-    // each warp counts, then lists, a contiguous run of this CTA's share, 128 keys at a time
-    const int per = (n + kSelWarps * 128 - 1) / (kSelWarps * 128) * 128;
-    const int w0 = (int)min((int64_t)n, (int64_t)warp * per), w1 = min(n, w0 + per);
-    uint32_t gt = 0, eq = 0;
-    for (int i = w0 + 4 * lane; i < w1; i += 128) {
-        uint32_t k[4];
-        keys4(i, k);
+    if (!few) {
+        uint32_t gt = 0, eq = 0;
+        for (int i = w0 + 4 * lane; i < w1; i += 128) {
+            uint32_t k[4];
+            keys4(i, k);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            gt += i + u < w1 && k[u] > T;
-            eq += i + u < w1 && k[u] == T;
+            for (int u = 0; u < 4; ++u) {
+                gt += i + u < w1 && k[u] > T;
+                eq += i + u < w1 && k[u] == T;
+            }
         }
+        gt = __reduce_add_sync(0xffffffffu, gt);
+        eq = __reduce_add_sync(0xffffffffu, eq);
+        if (lane == 0) {
+            s.wgt[warp] = gt;
+            s.weq[warp] = eq;
+        }
+        __syncthreads();
+        gt_before += sum_below(s.wgt, warp, lane);
+        eq_before += sum_below(s.weq, warp, lane);
     }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) {
-        s.wgt[warp] = gt;
-        s.weq[warp] = eq;
-    }
-    __syncthreads();
-    gt_before += sum_below(s.wgt, warp, lane);
-    eq_before += sum_below(s.weq, warp, lane);
+    // the runs' kept tokens, in order
     const uint32_t below = (1u << lane) - 1u;
     for (int i0 = w0; i0 < w1; i0 += 128) {
         const int i = i0 + 4 * lane;
