@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D,
     const int r8 = lane >> 2, c4 = lane & 3, lrow = lane & 7, lmat = lane >> 3;
     float sl2[HP];
 #pragma unroll
-    for (int e = 0; e < HP; ++e) sl2[e] = p.scale_log2 * (FP8 ? __ldg(p.k_scale + h + e) : 1.f);
+    for (int e = 0; e < HP; ++e) sl2[e] = p.scale_log2 * (FP8 ? p.k_scale[h + e] : 1.f);
     // tokens whose weights this lane updates: 16 c4 + r8 of a chunk, and the eighth one after it
     const int own = 16 * c4 + r8;
     while (next_segment()) {
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D,
         const auto page_of = [&](int chunk, int k) -> int {
             const int t = chunk * kChunk + own + 8 * k;
             if (chunk >= sg.lc1 || t >= L) return -1;
-            return __ldg(table + (p.log2_page >= 0 ? t >> p.log2_page : t / p.page_size));
+            return ld_unwritten(table + (p.log2_page >= 0 ? t >> p.log2_page : t / p.page_size));
         };
         const auto weight_at = [&](int chunk, int k, int pg) -> float * {
             const int t = chunk * kChunk + own + 8 * k;

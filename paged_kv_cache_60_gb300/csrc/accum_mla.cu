@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) accum_mla_kernel(const __grid_con
         __syncthreads();
         const int32_t *table = p.block_table + (size_t)ps.b * p.max_pages;
         const auto page_at = [&](int t) -> int {
-            return t < ps.end ? __ldg(table + (p.log2_page >= 0 ? t >> p.log2_page : t / P)) : -2;
+            return t < ps.end ? table[p.log2_page >= 0 ? t >> p.log2_page : t / P] : -2;
         };
         const auto slot_at = [&](int t) { return p.log2_page >= 0 ? t & (P - 1) : t % P; };
         if (warp == 0) {

@@ -42,13 +42,13 @@ constexpr int kThreads = 256;
 // Shared prologue of both kernels: where request b's token goes, or -1 when
 // it is skipped (negative position) or invalid (error bit set by `reporter`).
 __device__ __forceinline__ int64_t slot_of(const AppendParams &p, int b, bool reporter) {
-    const int t = __ldg(p.positions + b);
+    const int t = p.positions[b];
     if (t < 0) return -1;
     if ((int64_t)t >= (int64_t)p.max_pages * p.page_size) {
         if (reporter && p.error) atomicOr(p.error, DA_DEV_SEQ_TOO_LONG);
         return -1;
     }
-    const int page = __ldg(p.block_table + (int64_t)b * p.max_pages + t / p.page_size);
+    const int page = p.block_table[(int64_t)b * p.max_pages + t / p.page_size];
     if (page < 0 || page >= p.num_pages) {
         if (reporter && p.error) atomicOr(p.error, DA_DEV_BAD_PAGE);
         return -1;
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 6) append_gqa_kernel(const AppendPar
             }
         } else {
             const int h = e / vpr;
-            const Recip dk = recip_of(__ldg(p.k_scale + h)), dv = recip_of(__ldg(p.v_scale + h));
+            const Recip dk = recip_of(p.k_scale[h]), dv = recip_of(p.v_scale[h]);
             if constexpr (NV == 2) {
                 const uint2 k0 = quant8(xk[0], dk), k1 = quant8(xk[1], dk);
                 const uint2 v0 = quant8(xv[0], dv), v1 = quant8(xv[1], dv);

@@ -79,12 +79,12 @@ __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t caddr) {
 }
 // One token's key; 0 for a token on a page outside the pool.
 __device__ __noinline__ uint32_t weight_key(const EvictParams &p, const int32_t *table, int h, int t) {
-    const int pi = page_index(t, p.page_size, p.log2_page), page = __ldg(table + pi);
+    const int pi = page_index(t, p.page_size, p.log2_page), page = ld_unwritten(table + pi);
     if (page < 0 || page >= p.num_pages) {
         if (p.error) atomicOr(p.error, DA_DEV_BAD_PAGE);
         return 0u;
     }
-    return key_of(__ldg(p.weights + ((int64_t)page * p.H_kv + h) * p.page_size + (t - pi * p.page_size)));
+    return key_of(ld_unwritten(p.weights + ((int64_t)page * p.H_kv + h) * p.page_size + (t - pi * p.page_size)));
 }
 
 struct SelSmem {
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
     pdl_launch_dependents();
 
     const int64_t max_len = (int64_t)p.max_pages * p.page_size;
-    int L = __ldg(p.seqlens + b);
+    int L = p.seqlens[b];
     if (h == 0 && rank == 0 && tid == 0 && p.error) {
         if (L < 0) atomicOr(p.error, DA_DEV_NEG_LEN);
         if (L > max_len) atomicOr(p.error, DA_DEV_SEQ_TOO_LONG);
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
     const int share = (int)((((int64_t)M + kC - 1) / kC + 127) / 128 * 128);
     const int m0 = (int)min((int64_t)M, (int64_t)rank * share), n = min(share, M - m0);
     const int t0 = F + m0;
-    const int32_t *table = p.src_table + (int64_t)b * p.max_pages;
+    const int32_t *table = known_from_here(p.src_table + (int64_t)b * p.max_pages);
     __syncthreads();  // the histograms are clear
     // kBatch pages, then their weights: two latencies for kBatch * kSelThreads keys
     constexpr int kBatch = 8;
@@ -177,13 +177,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
             const int t = t0 + min(i0 + u * kSelThreads + tid, nc - 1);
             const int pi = page_index(t, p.page_size, p.log2_page);
             slot[u] = t - pi * p.page_size;
-            page[u] = __ldg(table + pi);
+            page[u] = ld_unwritten(table + pi);
         }
         float w[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const bool ok = (uint32_t)page[u] < (uint32_t)p.num_pages;
-            w[u] = __ldg(head + (ok ? page[u] : 0) * page_stride + slot[u]);
+            w[u] = ld_unwritten(head + (ok ? page[u] : 0) * page_stride + slot[u]);
             if (!ok) slot[u] = -1;
         }
 #pragma unroll
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_c
         const int h = k / n, i = k - h * n;
         const int t = p.kept[((int64_t)b * H + h) * p.budget + i0 + i];
         const int si = page_index(t, p.page_size, p.log2_page), di = page_index(i0 + i, p.page_size, p.log2_page);
-        const int sp = __ldg(st + si), dp = __ldg(dt + di);
+        const int sp = st[si], dp = dt[di];
         const bool ok = sp >= 0 && sp < p.num_pages && dp >= 0 && dp < p.num_pages;
         if (!ok && p.error) atomicOr(p.error, DA_DEV_BAD_PAGE);
         const int ss = t - si * p.page_size, ds = i0 + i - di * p.page_size;

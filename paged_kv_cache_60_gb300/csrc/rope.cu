@@ -87,9 +87,9 @@ constexpr int64_t kNowhere = -1;  // invalid request, position or page: no K / V
 
 // Pool slot of token n (page * page_size + slot), or one of the above.
 __device__ __forceinline__ int64_t slot_of(const RopeParams &p, int n, bool reporter) {
-    const int t = __ldg(p.positions + n);
+    const int t = p.positions[n];
     if (t < 0) return kSkip;
-    const int b = p.requests ? __ldg(p.requests + n) : n / p.s_q;
+    const int b = p.requests ? p.requests[n] : n / p.s_q;
     if (b < 0 || b >= p.B) {
         if (reporter && p.error) atomicOr(p.error, DA_DEV_BAD_REQUEST);
         return kNowhere;
@@ -98,7 +98,7 @@ __device__ __forceinline__ int64_t slot_of(const RopeParams &p, int n, bool repo
         if (reporter && p.error) atomicOr(p.error, DA_DEV_SEQ_TOO_LONG);
         return kNowhere;
     }
-    const int page = __ldg(p.block_table + (int64_t)b * p.max_pages + t / p.page_size);
+    const int page = p.block_table[(int64_t)b * p.max_pages + t / p.page_size];
     if (page < 0 || page >= p.num_pages) {
         if (reporter && p.error) atomicOr(p.error, DA_DEV_BAD_PAGE);
         return kNowhere;
@@ -157,9 +157,9 @@ __device__ __forceinline__ void latent_token(const RopeParams &p, int n, int lan
     const int half = p.rot / 2;
     const bool turn = lane < half;
     const int i = kAdjacent || !turn ? 2 * lane : lane, j = kAdjacent || !turn ? i + 1 : lane + half;
-    const float a = __uint_as_float((uint32_t)__ldg(src + kLatentNope + i) << 16);
-    const float b = __uint_as_float((uint32_t)__ldg(src + kLatentNope + j) << 16);
-    const float2 cs = turn ? cos_sin(__ldg(p.rope_pos + (int64_t)axis * p.N + n), F, finite) : make_float2(1.f, 0.f);
+    const float a = __uint_as_float((uint32_t)src[kLatentNope + i] << 16);
+    const float b = __uint_as_float((uint32_t)src[kLatentNope + j] << 16);
+    const float2 cs = turn ? cos_sin(p.rope_pos[(int64_t)axis * p.N + n], F, finite) : make_float2(1.f, 0.f);
     const int64_t slot = slot_of(p, n, lane == 0);  // uniform over the warp
     if (slot < 0) return;
     uint8_t *row = p.k_pool + slot * kLatentRow;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
     if (kLatent && (int)blockIdx.x >= p.q_blocks) {
         const int lane = tid & 31;
         const bool turn = lane < pairs;
-        const float f = turn ? __ldg(p.inv_freq + lane) : 0.f;
+        const float f = turn ? p.inv_freq[lane] : 0.f;
         const bool finite = fabsf(f) < INFINITY;
         const uint64_t F = finite ? turns_of(f) : 0;
         const int axis = turn ? axis_of(p, lane) : 0;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
     bool finite = true;
     const int32_t *apos = p.rope_pos;
     if (ta < at) {
-        const float f = __ldg(p.inv_freq + ia);
+        const float f = p.inv_freq[ia];
         finite = fabsf(f) < INFINITY;
         F = finite ? turns_of(f) : 0;
         apos += (int64_t)axis_of(p, ia) * p.N;
@@ -218,12 +218,12 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
         const int n0 = tile * p.tokens, nt = min(p.tokens, p.N - n0);
         if (ta < at) {
             float2 *cs = reinterpret_cast<float2 *>(smem) + (size_t)buf * p.tokens * pairs + cs_at;
-            for (int t = ta; t < nt; t += at) cs[t * pairs] = cos_sin(__ldg(apos + n0 + t), F, finite);
+            for (int t = ta; t < nt; t += at) cs[t * pairs] = cos_sin(apos[n0 + t], F, finite);
         }
         const int t = tid - (kThreads - 32);
         if (t >= 0 && t < nt)
             s_slot[buf][t] = !kLatent                           ? slot_of(p, n0 + t, part == 0)
-                             : __ldg(p.positions + n0 + t) < 0 ? kSkip
+                             : p.positions[n0 + t] < 0 ? kSkip
                                                                : kNowhere;
     };
 
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
                 unpack8(x0[u], x);
                 unpack8(x1[u], x + 8);
                 if (turn) rotate16<kAdjacent>(x, cs, j, turned);
-                quot_rn(x, recip_of(__ldg((is_k ? p.k_scale : p.v_scale) + kh)), q);
+                quot_rn(x, recip_of((is_k ? p.k_scale : p.v_scale)[kh]), q);
                 uint32_t c[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) c[i] = e4m3x2(q[2 * i], q[2 * i + 1]);

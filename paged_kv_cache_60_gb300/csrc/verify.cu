@@ -143,21 +143,21 @@ __device__ __forceinline__ uint64_t tile_sum(const Row<T> &r, int v0, int V, int
             uint32_t y[U][8];                     // the vector of q at p's, and what is needed of the next one
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                x[i] = __ldg(p + (g + i) * 32);
+                x[i] = ld_unwritten(p + (g + i) * 32);
                 if constexpr (kHasQ) {
                     const uint4 *qi = q + (g + i) * 32;
-                    const uint4 u = __ldg(qi);
+                    const uint4 u = ld_unwritten(qi);
                     y[i][0] = u.x, y[i][1] = u.y, y[i][2] = u.z, y[i][3] = u.w;
                     y[i][4] = y[i][5] = y[i][6] = y[i][7] = 0u;
                     if constexpr (kShift == 0 && kHalf) {
-                        if (half) y[i][4] = __ldg(reinterpret_cast<const uint32_t *>(qi + 1));
+                        if (half) y[i][4] = ld_unwritten(reinterpret_cast<const uint32_t *>(qi + 1));
                     } else if constexpr (kShift == 1 && !kHalf) {
-                        y[i][4] = __ldg(reinterpret_cast<const uint32_t *>(qi + 1));
+                        y[i][4] = ld_unwritten(reinterpret_cast<const uint32_t *>(qi + 1));
                     } else if constexpr (kShift == 1 || (kShift == 2 && !kHalf)) {
-                        const uint2 z = __ldg(reinterpret_cast<const uint2 *>(qi + 1));
+                        const uint2 z = ld_unwritten(reinterpret_cast<const uint2 *>(qi + 1));
                         y[i][4] = z.x, y[i][5] = z.y;
                     } else if constexpr (kShift > 0) {
-                        const uint4 z = __ldg(qi + 1);
+                        const uint4 z = ld_unwritten(qi + 1);
                         y[i][4] = z.x, y[i][5] = z.y, y[i][6] = z.z, y[i][7] = z.w;
                     }
                 }
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     const float *u = p.uniform + (int64_t)b * (K + 1);
 
     // read ahead of their use at the end
-    const float u_last = __ldg(u + K);
+    const float u_last = u[K];
     const int len = p.seqlens ? p.seqlens[b] : 0;
     // how many drafts are accepted (two lanes' worth of drafts: K <= 63)
     if (warp == 0) {
