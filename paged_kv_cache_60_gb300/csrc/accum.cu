@@ -74,6 +74,9 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D,
             mbar_init(&empty[i], 1);
         }
         *abort_flag = 0;
+#ifdef DA_PAGE_TRACE
+        mbar_init(reinterpret_cast<uint64_t *>(smem + C::OFF_FLAG + 8), 1);  // never arrived at
+#endif
         fence_barrier_init();
         fence_proxy_async_smem();
     }
@@ -164,11 +167,10 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D,
                 }
             }
         }
-        if (aborted) {
-            // let copies already in flight land before the CTA exits (ignoring the abort flag)
-            for (int k = max(0, i - C::NS); k < i; ++k)
-                mbar_wait_timed(&full[k % C::NS], (k / C::NS) & 1, 100000000ull);
-        }
+        // Copies in flight land before the CTA exits, whoever gives up (ignoring the abort flag): a consumer may after
+        // this warp has issued its last copy. Where nobody does, the consumers wait for the same copies.
+        for (int k = max(0, i - C::NS); k < i; ++k)
+            mbar_wait_timed(&full[k % C::NS], (k / C::NS) & 1, 100000000ull);
         return;
     }
 
@@ -266,6 +268,17 @@ __global__ void __launch_bounds__(AccumCfg<D, FP8, NQ, HP>::THREADS, AccumCfg<D,
         }
         for (i += skip; i < i1; i += C::NCW, c += C::NCW * Z) {
             const int stage = i % C::NS;
+#ifdef DA_PAGE_TRACE
+            // test build: a wait on a barrier that nothing completes runs out
+            if (p.debug_stall &&
+                !mbar_wait_warp(reinterpret_cast<uint64_t *>(smem + C::OFF_FLAG + 8), 0, abort_flag, p.wait_limit_ns)) {
+                if (lane == 0) {
+                    atomicOr(&p.meta.header[kHError], DA_DEV_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                return;
+            }
+#endif
             if (!mbar_wait_warp(&full[stage], (i / C::NS) & 1, abort_flag, p.wait_limit_ns)) {
                 if (lane == 0) {
                     atomicOr(&p.meta.header[kHError], DA_DEV_TIMEOUT);

@@ -712,6 +712,7 @@ int decode_attn_accum_weights(const da_desc *desc, const void *q, const void *k_
     p.boxes_per_chunk = kChunk / p.box_tokens;
     p.log2_page = log2_of(desc->page_size);
     p.wait_limit_ns = g_wait_limit_ns ? g_wait_limit_ns : kWaitLimitNs;
+    p.debug_stall = g_debug_stall;
     if (is_mla(desc)) return launch_accum_mla(p, sms, stream, true) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
     CUtensorMap tk;
     p.heads_per_cta = accum_heads(desc->D_qk * (fp8 ? 1 : 2), desc->H_kv, p.s_q);
@@ -865,8 +866,9 @@ extern "C" int decode_attn_debug_wait_limit(uint64_t ns) {
     return DA_OK;
 }
 
-// Test build only: with `on` != 0, the GQA kernel's consumer warps first wait
-// on a barrier that nothing completes, so that wait runs out.
+// Test build only: with `on` != 0, the consumer warps of the attention kernels
+// and of the accumulation first wait on a barrier that nothing completes, so
+// that wait runs out.
 extern "C" int decode_attn_debug_stall(int32_t on) {
     g_debug_stall = on;
     return DA_OK;

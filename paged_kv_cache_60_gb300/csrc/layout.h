@@ -201,6 +201,7 @@ struct AccumParams {
     int32_t log2_page;             // log2(page_size) when it is a power of two, else -1
     int32_t parts_per_cta, heads_per_cta;
     uint64_t wait_limit_ns;
+    int32_t debug_stall;           // test build only: the warps that sum first wait on a barrier nothing completes
 };
 
 // Eviction by weight (evict.cu).
