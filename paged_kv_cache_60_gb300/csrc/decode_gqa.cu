@@ -330,10 +330,9 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
                 }
             }
         }
-        if (aborted) {
-            // let copies already in flight land before the CTA exits (ignoring the abort flag)
-            for (int k = max(0, i - C::NS); k < i; ++k) mbar_wait_timed(&full[k % C::NS], (k / C::NS) & 1, 100000000ull);
-        }
+        // Copies in flight land before the CTA exits, whoever gives up (ignoring the abort flag): a consumer may after
+        // this warp has issued its last copy. Where nobody does, the consumers wait for the same copies.
+        for (int k = max(0, i - C::NS); k < i; ++k) mbar_wait_timed(&full[k % C::NS], (k / C::NS) & 1, 100000000ull);
         return;
     }
 
