@@ -134,6 +134,9 @@ __global__ void __launch_bounds__(kThreads, 1) accum_mla_kernel(const __grid_con
         }
         mbar_init(bar.drain, 1);
         *abort_flag = 0;
+#ifdef DA_PAGE_TRACE
+        mbar_init(reinterpret_cast<uint64_t *>(smem + kOffTmem + 8), 1);  // never arrived at
+#endif
         fence_barrier_init();
         fence_proxy_async_smem();
     }
@@ -147,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1) accum_mla_kernel(const __grid_con
 
     const bool meta_ok =
         meta_header_ok(load_meta_header(p.meta.header), p.B, p.H_kv, p.G, p.splits, p.num_parts, p.s_q, 0, 0);
-    // the query tiles' swizzle needs a 1024-byte aligned base (dynamic shared memory without static starts there)
+    // the query tiles' swizzle needs a 1024-byte aligned base (the declaration asks for it, and dynamic shared memory
+    // without static starts there; were it not so, the call would do nothing and report a wait that ran out)
     const bool aligned = (smem_u32(smem) & 1023u) == 0;
     if (tid == 0 && !meta_ok) atomicOr(&p.meta.header[kHError], DA_DEV_META_MISMATCH);
     if (tid == 0 && !aligned) atomicOr(&p.meta.header[kHError], DA_DEV_TIMEOUT);
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) accum_mla_kernel(const __grid_con
         __syncthreads();
         const int32_t *table = p.block_table + (size_t)ps.b * p.max_pages;
         const auto page_at = [&](int t) -> int {
-            return t < ps.end ? table[p.log2_page >= 0 ? t >> p.log2_page : t / P] : -2;
+            return t < ps.end ? ld_unwritten(table + (p.log2_page >= 0 ? t >> p.log2_page : t / P)) : -2;
         };
         const auto slot_at = [&](int t) { return p.log2_page >= 0 ? t & (P - 1) : t % P; };
         if (warp == 0) {
@@ -259,7 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1) accum_mla_kernel(const __grid_con
             }
             // every product has read its operands before the query rows are replaced or the tensor memory goes away
             umma_commit_w(bar.drain);
-            if (!mbar_wait_timed(bar.drain, (uint32_t)pass & 1u, 100000000ull)) give_up();
+            // (the limit of every other wait, and where a test shortens that, time enough for the products all the same)
+            if (!mbar_wait_timed(bar.drain, (uint32_t)pass & 1u, max(p.wait_limit_ns, (uint64_t)100000000))) give_up();
         } else if (warp == 1) {
             // -------------------------------------------------------- rows into the quarters' buffers
             if (lane < nb) {
@@ -314,6 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1) accum_mla_kernel(const __grid_con
                 float *w = weight_at(t, pg);
                 const float old = old_at(t, w);
                 if (k + 1 < ps.units) pg = page_at(unit_base(k + 1) + own);
+#ifdef DA_PAGE_TRACE
+                // test build: a wait on a barrier that nothing completes runs out
+                if (p.debug_stall && !wait(reinterpret_cast<uint64_t *>(smem + kOffTmem + 8), 0)) break;
+#endif
                 if (!wait(&bar.sfull[d], (uint32_t)(n >> 1) & 1u)) break;
                 tc_fence_after();
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};

@@ -54,3 +54,10 @@ def _stalled_then_right(tlib, spec):
 @pytest.mark.parametrize("lens,splits", [([90, 30], 1), ([9000, 4000], 1)])
 def test_wait_that_runs_out_and_the_call_after_it(tlib, kv, H, D, s_q, lens, splits):
     _stalled_then_right(tlib, _spec(kv, 2, H, D, 32, lens, s_q, splits, seed=91))
+
+
+@pytest.mark.parametrize("s_q", [1, 2])
+@pytest.mark.parametrize("lens,splits", [([90, 30], 1), ([5000, 2500], 1), ([700, 1, 333], 0)])
+def test_latent_wait_that_runs_out_and_the_call_after_it(tlib, lens, splits, s_q):
+    """The products that have been issued end before the tensor memory is given back."""
+    _stalled_then_right(tlib, _spec(KV_MLA656, len(lens), 1, 576, 32, lens, s_q, splits, seed=92))
