@@ -329,7 +329,8 @@ int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_
  * and no sparse decode (DA_ERR_UNSUPPORTED). On the 656-byte format
  * max_pages_per_seq * page_size may be 2^31 - 257 at most.
  *   desc, q, k_pool, k_scale, block_table, cache_seqlens, sched_meta, lse: those
- *     of the step's decode_attn_fwd call, with the same requirements; sinks
+ *     of the step's decode_attn_fwd call, with the same requirements and the
+ *     lengths as they were then (not new_seqlens of a verification); sinks
  *     need no argument (they are in lse). Page errors go to sched_meta's word.
  *   num_accepted: device int32 [B] or NULL (all s_q count): of a draft chain
  *     whose verification accepted a drafts, query tokens 0..a count; negative:
@@ -417,9 +418,11 @@ typedef enum {
  *     p_a is drawn from; where none of p_a either, the token is -1 (DA_DEV_BAD_PROBS).
  *   num_accepted: device int32 [B], a. out_tokens: device int32 [B][n_draft + 1]:
  *     the accepted drafts, the next token, then -1.
- *   cache_seqlens, new_seqlens: device int32 [B], both or neither; new = L_b -
- *     n_draft + a, the length that keeps the accepted drafts. They may be the same
- *     buffer.
+ *   cache_seqlens, new_seqlens: device int32 [B], both or neither; new = max(L_b
+ *     - n_draft + a, 0), the length that keeps the accepted drafts (a row that pads
+ *     the batch, of length 0 and without drafts, keeps 0). They may be the same
+ *     buffer, if no later call wants the step's own lengths (decode_attn_accum_weights
+ *     does).
  *   device_error: device int32 or NULL.
  * Launches one kernel on `stream`. No allocation, no sync.
  */

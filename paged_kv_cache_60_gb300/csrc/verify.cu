@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         for (int i = lane; i <= K; i += 32) p.out[(int64_t)b * (K + 1) + i] = i < a ? s_token[i] : i == a ? token : -1;
         if (lane == 0) {
             p.accepted[b] = a;
-            if (p.new_seqlens) p.new_seqlens[b] = len - K + a;
+            if (p.new_seqlens) p.new_seqlens[b] = max(max(len, 0) - K + a, 0);  // (a padded row of length 0 stays one)
             if (p.error && (s_bad || token < 0))
                 atomicOr(p.error, (s_bad ? DA_DEV_BAD_TOKEN : 0) | (token < 0 ? DA_DEV_BAD_PROBS : 0));
         }
