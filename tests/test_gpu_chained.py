@@ -63,40 +63,51 @@ class Loop:
         self.new = rand(B, (H * G + (1 if kv == MLA else 2 * H)) * D).to(torch.bfloat16)
         self.freq = (1000.0 ** (-torch.arange(32) / 32)).float().cuda()
 
-    def run(self, sync):
+    def buffers(self):
+        """What the calls write, and copies of what they change."""
         e = lambda *s, dtype=torch.int32: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
-        B, H, D, HG, scale = self.B, self.H, self.D, self.q.shape[2], self.scale
-        pools, w = [p.clone() for p in self.pools], self.weights.clone()
-        k, v = pools[0], pools[1] if len(pools) > 1 else None
-        meta, meta2 = (e(da.sched_meta_bytes(d), dtype=torch.uint8) for d in (self.desc, self.one))
-        out, lse = e(B, 2, HG, self.Dv, dtype=torch.bfloat16), e(B, 2, HG, dtype=torch.float32)
-        out2, lse2 = e(B, HG, self.Dv, dtype=torch.bfloat16), e(B, HG, dtype=torch.float32)
-        acc, tok, new, cut, err, kept = e(B), e(B, 2), e(B), e(B), e(1), e(B, H, self.budget)
-        q_out, q_len, kv_len = e(B, HG, D, dtype=torch.bfloat16), HG * D, H * D
+        B, HG, bf16, f32 = self.B, self.q.shape[2], torch.bfloat16, torch.float32
+        pools = [p.clone() for p in self.pools]
+        return dict(k=pools[0], v=pools[1] if len(pools) > 1 else None, weights=self.weights.clone(),
+                    meta=e(da.sched_meta_bytes(self.desc), dtype=torch.uint8), meta2=e(da.sched_meta_bytes(self.one), dtype=torch.uint8),
+                    out=e(B, 2, HG, self.Dv, dtype=bf16), lse=e(B, 2, HG, dtype=f32), out2=e(B, HG, self.Dv, dtype=bf16),
+                    lse2=e(B, HG, dtype=f32), accepted=e(B), tokens=e(B, 2), new=e(B), cut=e(B), err=e(1), kept=e(B, self.H, self.budget),
+                    q=e(B, HG, self.D, dtype=bf16))
+
+    def calls(self, s, wait=lambda: None):
+        B, scale, k, v, err = self.B, self.scale, s["k"], s["v"], s["err"]
+        q_len, kv_len = s["q"].shape[1] * self.D, self.H * self.D
         nk, nv = self.new[:, q_len:q_len + kv_len], None if self.kv == MLA else self.new[:, q_len + kv_len:]
-        wait = torch.cuda.synchronize if sync else (lambda: None)
+        da.sched_meta(self.desc, self.lens, s["meta"])
+        wait()
+        da.fwd(self.desc, self.q, k, v, scale, scale, self.table, self.lens, s["meta"], s["out"], s["lse"])
+        wait()
+        da.verify_drafts(self.p, None, self.x, self.u, s["accepted"], s["tokens"], cache_seqlens=self.lens, new_seqlens=s["new"],
+                         device_error=err)
+        wait()
+        da.accum_weights(self.desc, self.q, k, scale, self.table, self.lens, s["meta"], s["lse"], s["weights"],
+                         num_accepted=s["accepted"], weighted_lens=self.weighted, decay=0.5)
+        wait()
+        da.evict(self.one, self.budget, s["new"], self.table, self.into, k, v, s["weights"], s["kept"], s["cut"], keep_first=2,
+                 keep_last=16, device_error=err)
+        wait()
+        da.rope_append(self.one, da.Rope.make(64), self.new[:, :q_len], nk, nv, self.freq, s["cut"].view(1, B), s["accepted"], self.into,
+                       s["q"], k, v, scale, scale, device_error=err)
+        wait()
+        da.sched_meta(self.one, s["cut"], s["meta2"])
+        wait()
+        da.fwd(self.one, s["q"], k, v, scale, scale, self.into, s["cut"], s["meta2"], s["out2"], s["lse2"])
+
+    def results(self, s):
+        assert int(s["err"].item()) == 0 and da.get_error(s["meta"]) == 0 and da.get_error(s["meta2"]) == 0
+        return {n: t for n, t in s.items() if t is not None and not n.startswith("meta")}
+
+    def run(self, sync):
+        s = self.buffers()
         torch.cuda.synchronize()
-        da.sched_meta(self.desc, self.lens, meta)
-        wait()
-        da.fwd(self.desc, self.q, k, v, scale, scale, self.table, self.lens, meta, out, lse)
-        wait()
-        da.verify_drafts(self.p, None, self.x, self.u, acc, tok, cache_seqlens=self.lens, new_seqlens=new, device_error=err)
-        wait()
-        da.accum_weights(self.desc, self.q, k, scale, self.table, self.lens, meta, lse, w, num_accepted=acc,
-                         weighted_lens=self.weighted, decay=0.5)
-        wait()
-        da.evict(self.one, self.budget, new, self.table, self.into, k, v, w, kept, cut, keep_first=2, keep_last=16, device_error=err)
-        wait()
-        da.rope_append(self.one, da.Rope.make(64), self.new[:, :q_len], nk, nv, self.freq, cut.view(1, B), acc, self.into, q_out, k, v,
-                       scale, scale, device_error=err)
-        wait()
-        da.sched_meta(self.one, cut, meta2)
-        wait()
-        da.fwd(self.one, q_out, k, v, scale, scale, self.into, cut, meta2, out2, lse2)
+        self.calls(s, torch.cuda.synchronize if sync else (lambda: None))
         torch.cuda.synchronize()
-        assert int(err.item()) == 0 and da.get_error(meta) == 0 and da.get_error(meta2) == 0
-        return dict(out=out, lse=lse, accepted=acc, tokens=tok, new=new, weights=w, kept=kept, cut=cut, q=q_out, out2=out2, lse2=lse2,
-                    k=k, **({} if v is None else {"v": v}))
+        return self.results(s)
 
 
 @pytest.mark.parametrize("kv,H,D,P", [(BF16, 4, 64, 8), (BF16, 8, 128, 16), (FP8, 4, 128, 8), (MLA, 1, 576, 8)])
@@ -109,3 +120,31 @@ def test_a_loop_without_a_synchronisation_in_it(kv, H, D, P):
         got = loop.run(sync=False)
         for name, t in want.items():
             assert torch.equal(got[name], t), (name, rep)
+
+
+def test_loops_of_three_formats_at_once():
+    """The same loops on three streams, all of their calls enqueued behind one event before any of them can start, so
+    that attention, accumulation, eviction and appends of different formats run beside each other."""
+    loops = [Loop(kv, H, D, P, B=6, seed=3 + kv) for kv, H, D, P in ((BF16, 4, 64, 8), (FP8, 4, 128, 16), (MLA, 1, 576, 16))]
+    want = [loop.run(sync=True) for loop in loops]
+    reps = 4
+    states = [[loop.buffers() for _ in range(reps)] for loop in loops]
+    streams = [torch.cuda.Stream() for _ in loops]
+    busy = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(60):                                   # about 20 ms, the time to enqueue everything else
+        busy.copy_(busy.roll(1))
+    start = torch.cuda.Event()
+    start.record()
+    for st in streams:
+        st.wait_event(start)
+    for rep in range(reps):
+        for loop, st, state in zip(loops, streams, states):
+            with torch.cuda.stream(st):
+                loop.calls(state[rep])
+    torch.cuda.synchronize()
+    for loop, ref, state in zip(loops, want, states):
+        for rep in range(reps):
+            got = loop.results(state[rep])
+            for name, t in ref.items():
+                assert torch.equal(got[name], t), (name, loop.kv, rep)
