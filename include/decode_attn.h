@@ -296,8 +296,10 @@ typedef struct {
  *     vector and v_new is NULL. Strides count bf16 elements (0: packed rows;
  *     else at least the row and a multiple of 8), so the three may be slices of
  *     one projection output.
- *   inv_freq: fp32 [rot_dim / 2], radians per position. Angles are exact to
- *     about 2^-31 of a turn at any int32 position.
+ *   inv_freq: fp32 [rot_dim / 2], radians per position. At any int32 position the
+ *     angle modulo a turn is held to 24 bits: it is off by at most 2^-26 of a turn
+ *     (1e-7 radians), and |position| (|inv_freq| + 1) 2^-64 of a turn besides. An
+ *     infinite or NaN frequency gives NaN.
  *   rope_positions: int32 [n_axes][N]. positions: int32 [N], the token's index
  *     in its request's cache (slot t % page_size of page block_table[b][t /
  *     page_size]); negative: the token is skipped, its q_out row left as it was.

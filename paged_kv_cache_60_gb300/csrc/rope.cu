@@ -14,9 +14,12 @@
 // The angle: positions reach far beyond what an fp32 product keeps of an angle
 // (position 10^6 has an ulp of 0.06 rad), so the phase is kept in turns as a
 // 64-bit fraction, F = inv_freq / (2 pi) mod 1 in units of 2^-64 from the fp32
-// bits of inv_freq, and pos * F wraps modulo one turn in integer arithmetic:
-// the phase error is below |pos| * 2^-63 turns. The top 32 bits, as a signed
-// fraction of half a turn, go to sincospif.
+// bits of inv_freq, and pos * F wraps modulo one turn in integer arithmetic: F
+// is short of inv_freq / (2 pi) by less than |inv_freq| + 1 of its units (the
+// constant's last unit, then the shift's), the phase by |pos| (|inv_freq| + 1)
+// 2^-64 turns. The top 32 bits, as a signed fraction of half a turn, go to
+// sincospif; as an fp32 number they keep 24, an error of at most 2^-26 turns
+// (1e-7 radians), next to the 2 ulp of sincospif.
 //
 // Bound by HBM: every value is read and written once. A block works on a tile
 // of tokens: it computes each token's angles once, into shared memory, and then
@@ -63,7 +66,7 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
     return (u >> 31) ? 0ull - r : r;
 }
 
-// cos and sin of pos * F turns
+// cos and sin of pos * F turns, each within 2^-22 where F is exact: 2 pi 2^-26 from the conversion to float, and 2 ulp
 __device__ __forceinline__ float2 cos_sin(int32_t pos, uint64_t F, bool finite) {
     const uint64_t phase = (uint64_t)(int64_t)pos * F;
     const float half_turns = (float)(int32_t)(phase >> 32) * 0x1p-31f;
