@@ -345,8 +345,11 @@ int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_
  *     slots of tokens t < L_b change. A page that two requests share, or that
  *     one lists twice, would be updated twice at once: give every request pages of
  *     its own.
- * A query row whose lse is -inf adds nothing. Each weight is summed in fp32 in
- * a fixed order. Launches one kernel on `stream`. No allocation, no sync.
+ * A query row whose lse is -inf adds nothing. Scores are products of what the
+ * attention call multiplies, so that they match its lse: on e4m3 pools q goes to
+ * f16 (bf16 values above 65504 become infinite and give NaN, those below 2^-14
+ * lose bits), on the 656-byte format K is bf16(e4m3 * scale); exponentials are the
+ * hardware's ex2 (2 ulp). Each weight is summed in fp32 in a fixed order. Launches one kernel on `stream`. No allocation, no sync.
  */
 int decode_attn_accum_weights(const da_desc *desc, const void *q, const void *k_pool, const float *k_scale,
                               const int32_t *block_table, const int32_t *cache_seqlens, void *sched_meta,
