@@ -62,7 +62,15 @@ typedef enum {
      * Codes 0x7F / 0xFF decode to NaN (and so poison the rows that read
      * them), as in the bf16 and per-tensor formats; the quantiser,
      * decode_attn_append_kv, never writes them: it saturates at +-448. */
-    DA_KV_FP8_MLA656 = 2
+    DA_KV_FP8_MLA656 = 2,
+    /* k_pool, v_pool: 8-bit codes [num_pages][page_size][H_kv][128], e4m3 or
+     * int8; k_scale, v_scale: fp32 [num_pages][H_kv][page_size / 16], one scale
+     * per block of 16 tokens, KV head and tensor. Element value = code * scale
+     * of its block. page_size 16, 32 or a multiple of 64. Attention takes any
+     * scales; those that decode_attn_append_block writes are powers of two. (No
+     * counterpart on the source pages, whose e4m3 scales are per tensor.) */
+    DA_KV_FP8_BLOCK = 3,
+    DA_KV_INT8_BLOCK = 4
 } da_kv_dtype;
 
 /* Problem description (host struct, passed by pointer, not retained). */
@@ -72,7 +80,7 @@ typedef struct {
     int32_t G;                 /* query heads per KV head; H_q = H_kv * G */
     int32_t D_qk;              /* q / K head size */
     int32_t D_v;               /* V / out head size */
-    int32_t page_size;         /* tokens per page P: 8, 16, 32 or a multiple of 64 */
+    int32_t page_size;         /* tokens per page P: 8, 16, 32 or a multiple of 64 (block formats: not 8) */
     int32_t max_pages_per_seq; /* row length of block_table */
     int32_t num_pages;         /* pages in the pool */
     int32_t kv_dtype;          /* da_kv_dtype */
@@ -172,7 +180,7 @@ int decode_attn_sched_meta(const da_desc *desc, const int32_t *cache_seqlens,
  * last s_q tokens are already in the pool (L_b counts them) and draft token
  * j < s_q sees the first L_b - s_q + 1 + j tokens -- the history and the
  * drafts up to itself. A row that sees no token gets out = 0, lse = -inf.
- * Supported: s_q <= 4 for all three formats (on the 656-byte format the
+ * Supported: s_q <= 4 for all formats (on the 656-byte format the
  * sliding window and, when s_q > 1, sparse decode are not offered:
  * DA_ERR_UNSUPPORTED). The rows of q, out and lse below are
  * then [B][s_q][H_kv*G]; the scheduling metadata must be built with the same s_q.
@@ -184,7 +192,7 @@ int decode_attn_sched_meta(const da_desc *desc, const int32_t *cache_seqlens,
  * units of sigma * q.k, that joins each row's softmax denominator and carries
  * no value: lse = ln(e^sink + sum_t e^{s_t}), out = sum_t e^{s_t - lse} v_t;
  * a row that sees no token gets out = 0 and lse = sink. Both are for the
- * bf16 and e4m3 formats (DA_ERR_UNSUPPORTED with the 656-byte format).
+ * formats but the 656-byte one (DA_ERR_UNSUPPORTED).
  *
  * Sparse top-k decode (desc->topk = k > 0, da_launch_opts.indices; the
  * FlashMLA page's decode call with `indices`, ledger rows "FP8 稀疏解码"): for
@@ -197,13 +205,17 @@ int decode_attn_sched_meta(const da_desc *desc, const int32_t *cache_seqlens,
  *
  *   q:            bf16 [B][H_kv*G][D_qk], query head h*G+g belongs to KV head h
  *   k_pool/v_pool: see da_kv_dtype
- *   k_scale/v_scale: fp32 [H_kv] for DA_KV_FP8_PER_TENSOR, else ignored
+ *   k_scale/v_scale: fp32 [H_kv] for DA_KV_FP8_PER_TENSOR, fp32 [num_pages][H_kv]
+ *                 [page_size / 16] for the block formats (only scales of blocks that
+ *                 hold a token below L_b are read), else ignored
  *   block_table:  int32 [B][max_pages_per_seq]; entries past ceil(L_b/P) are never read
  *   cache_seqlens: int32 [B] (must match what sched_meta was built from)
  *   sched_meta:   from decode_attn_sched_meta; its partial buffers are overwritten,
  *                 so two calls sharing one sched_meta must not overlap in time
  *   out:          bf16 [B][H_kv*G][D_v]; lse: fp32 [B][H_kv*G]
  * A request with L_b = 0 gets out = 0 and lse = -inf.
+ * On all formats of 8 bits q and the softmax weights are multiplied as f16: values of
+ * q above 65504 become infinite, those below 2^-14 lose bits.
  */
 int decode_attn_fwd(const da_desc *desc, const void *q, const void *k_pool, const void *v_pool,
                     const float *k_scale, const float *v_scale, const int32_t *block_table,
@@ -267,6 +279,45 @@ int decode_attn_append_kv(const da_desc *desc, const void *k_new, const void *v_
                           const int32_t *positions, const int32_t *block_table, void *k_pool, void *v_pool,
                           const float *k_scale, const float *v_scale, int32_t *device_error, cudaStream_t stream);
 
+/*
+ * Append to a cache with scales per block (DA_KV_FP8_BLOCK, DA_KV_INT8_BLOCK), one
+ * token per request, a draft chain or ragged prompts. (No counterpart on the source
+ * pages.) Request b's new tokens are the rows token_starts[b] .. token_starts[b + 1]
+ * of k_new and v_new, and go to positions[b], positions[b] + 1, ... of its cache. Per
+ * block of 16 positions, KV head and tensor:
+ *   scale = the smallest power of two, at least 2^-126, with max |x| <= 448 scale
+ *     (e4m3) or 127 scale (int8) over the block's new tokens (values that are not
+ *     finite do not count); where the block holds tokens already (positions below
+ *     positions[b]), never below the scale that it has.
+ *   code = nearest to x / scale (the fp32 quotient, which is exact for a power of
+ *     two), ties to even. e4m3: saturating at +-448, NaN ->
+ *     0x7F. int8: saturating at +-127, NaN -> 0.
+ * Where a block's scale grows, the codes of its earlier tokens are rounded to the new
+ * scale (from their values, not from what was appended). A value that is appended with
+ * its whole block is off by at most half a step; one whose block grew later, by less
+ * than a step of the final scale in int8 (halves add up), and in e4m3 by its own
+ * rounding only, as long as its code stays normal (|value| >= scale / 64). The
+ * positions behind the last new one hold nothing afterwards: their codes are left, the
+ * scale may be another.
+ *   desc: B, H_kv, D_qk = D_v = 128, page_size, max_pages_per_seq, num_pages, kv_dtype
+ *     and, without token_starts, s_q are used.
+ *   n_tokens: N in [0, 2^30], rows of k_new and v_new (0: nothing is launched).
+ *   k_new, v_new: bf16 [N][H_kv][128], row n at + n * stride (bf16 elements; 0: packed
+ *     rows; else at least the row and a multiple of 8).
+ *   token_starts: device int32 [B + 1], not descending, within [0, N]; NULL: s_q rows per
+ *     request, and N must be B * s_q.
+ *   positions: device int32 [B]; negative: the request is skipped.
+ *   block_table, device_error: as for decode_attn_append_kv (a token behind the table, or
+ *     on a page outside the pool, is skipped).
+ *   k_pool, v_pool, k_scale, v_scale: written in place.
+ * Two requests that write to one block race: give every request pages of its own (see
+ * decode_attn_reserve_pages). Launches one kernel on `stream`. No allocation, no sync.
+ */
+int decode_attn_append_block(const da_desc *desc, int32_t n_tokens, const void *k_new, int64_t k_stride,
+                             const void *v_new, int64_t v_stride, const int32_t *token_starts,
+                             const int32_t *positions, const int32_t *block_table, void *k_pool, void *v_pool,
+                             float *k_scale, float *v_scale, int32_t *device_error, cudaStream_t stream);
+
 /* Rotary positions with one or several axes (host struct, passed by pointer,
  * not retained). */
 typedef struct {
@@ -327,8 +378,8 @@ int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_
  *     w[t] <- (t < weighted_lens[b] ? decay * w[t] : 0)
  *             + sum_j sum_g exp(sigma * q_{b,j,hG+g} . k_t - lse[b,j,hG+g])
  * over the query tokens j <= num_accepted[b] that see t (t <= L_b - s_q + j).
- * (No counterpart on the source pages.) All three formats; no sliding window
- * and no sparse decode (DA_ERR_UNSUPPORTED). On the 656-byte format
+ * (No counterpart on the source pages.) The bf16, e4m3 (a scale per head) and
+ * 656-byte formats; no sliding window and no sparse decode (DA_ERR_UNSUPPORTED). On the 656-byte format
  * max_pages_per_seq * page_size may be 2^31 - 257 at most.
  *   desc, q, k_pool, k_scale, block_table, cache_seqlens, sched_meta, lse: those
  *     of the step's decode_attn_fwd call, with the same requirements and the

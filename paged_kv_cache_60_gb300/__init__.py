@@ -13,7 +13,7 @@ import raises.
     sched_meta(desc, cache_seqlens, meta)
     fwd(desc, q, k_pool, v_pool, k_scale, v_scale, block_table, cache_seqlens, meta, out, lse)
 
-Around the step: append_kv and rope_append write new tokens, verify_drafts
+Around the step: append_kv, append_block and rope_append write new tokens, verify_drafts
 accepts a chain of drafts, accum_weights gathers the attention weight of cached
 tokens and evict keeps the heaviest. All but append_kv check every
 tensor's dtype, shape, strides and device and raise DecodeAttnError.
@@ -26,6 +26,8 @@ from . import build as _build_mod
 KV_BF16 = 0
 KV_FP8 = 1
 KV_MLA656 = 2
+KV_FP8_BLOCK = 3      # e4m3 or int8 codes with a scale per block of 16 tokens and KV head
+KV_INT8_BLOCK = 4
 
 PROB_F32 = 0
 PROB_BF16 = 1
@@ -114,6 +116,7 @@ def load_library(path: str = LIB_PATH):
     lib.decode_attn_get_error.argtypes = [P, ctypes.POINTER(I32), P]
     lib.decode_attn_append_kv.argtypes = [DP, P, P, ctypes.c_int64, P, P, P, P, P, P, P, P]
     I64, F32 = ctypes.c_int64, ctypes.c_float
+    lib.decode_attn_append_block.argtypes = [DP, I32, P, I64, P, I64, P, P, P, P, P, P, P, P, P]
     lib.decode_attn_rope_append.argtypes = [DP, ctypes.POINTER(Rope), I32, P, I64, P, I64, P, I64, P, P, P, P, P, P,
                                             P, P, P, P, P, P]
     lib.decode_attn_accum_weights.argtypes = [DP, P, P, P, P, P, P, SZ, P, P, P, F32, P, P]
@@ -123,7 +126,7 @@ def load_library(path: str = LIB_PATH):
     lib.decode_attn_strerror.restype = ctypes.c_char_p
     for f in ("decode_attn_sched_meta_bytes", "decode_attn_meta_offsets", "decode_attn_num_parts",
               "decode_attn_sched_meta", "decode_attn_fwd", "decode_attn_fwd_ex", "decode_attn_get_error",
-              "decode_attn_append_kv", "decode_attn_rope_append", "decode_attn_accum_weights", "decode_attn_evict",
+              "decode_attn_append_kv", "decode_attn_append_block", "decode_attn_rope_append", "decode_attn_accum_weights", "decode_attn_evict",
               "decode_attn_verify_drafts"):
         getattr(lib, f).restype = ctypes.c_int
     _libs[path] = lib
@@ -266,6 +269,28 @@ def _pool(dev, name, t, desc):
     return t.data_ptr()
 
 
+def append_block(desc: Desc, k_new, v_new, positions, block_table, k_pool, v_pool, k_scale, v_scale, token_starts=None,
+                 device_error=None, stream=None, lib=None):
+    """Append new tokens to a cache with scales per block (KV_FP8_BLOCK,
+    KV_INT8_BLOCK): request b's rows ``token_starts[b]`` to ``token_starts[b + 1]``
+    (None: ``desc.s_q`` rows each) of ``k_new`` and ``v_new`` [N, H_kv * 128] (or
+    [N, H_kv, 128]; column slices of one projection output will do) go to its
+    positions from ``positions[b]`` on. ``k_scale`` and ``v_scale`` fp32
+    [num_pages, H_kv, page_size / 16] are written. See decode_attn_append_block in
+    the header."""
+    import torch
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
+    dev, B, n, row = _device(), desc.B, k_new.shape[0], desc.H_kv * desc.D_qk
+    scales = (desc.num_pages, desc.H_kv, desc.page_size // 16)
+    kp, ks = _rows(dev, "k_new", k_new, bf16, n, row)
+    vp, vs = _rows(dev, "v_new", v_new, bf16, n, row)
+    _check((lib or load_library()).decode_attn_append_block(
+        ctypes.byref(desc), n, kp, ks, vp, vs, _opt(dev, "token_starts", token_starts, i32, (B + 1,)),
+        _need(dev, "positions", positions, i32, (B,)), _need(dev, "block_table", block_table, i32, (B, desc.max_pages_per_seq)),
+        _pool(dev, "k_pool", k_pool, desc), _pool(dev, "v_pool", v_pool, desc), _need(dev, "k_scale", k_scale, f32, scales),
+        _need(dev, "v_scale", v_scale, f32, scales), _opt(dev, "device_error", device_error, i32), _stream(stream, dev)))
+
+
 def rope_append(desc: Desc, rope: Rope, q, k_new, v_new, inv_freq, rope_positions, positions, block_table, q_out,
                 k_pool, v_pool, k_scale=None, v_scale=None, requests=None, device_error=None, stream=None, lib=None):
     """Rotate the new tokens' q and K by their positions (one or several axes)
@@ -382,6 +407,7 @@ def get_error(meta, stream=None) -> int:
 
 
 __all__ = ["Desc", "LaunchOpts", "DecodeAttnError", "load_library", "strerror", "sched_meta_bytes",
-           "meta_offsets", "num_parts", "sched_meta", "fwd", "fwd_static_scratch", "append_kv", "rope_append",
-           "accum_weights", "evict", "verify_drafts", "get_error", "Rope", "KV_BF16", "KV_FP8", "KV_MLA656", "PROB_F32",
+           "meta_offsets", "num_parts", "sched_meta", "fwd", "fwd_static_scratch", "append_kv", "append_block", "rope_append",
+           "accum_weights", "evict", "verify_drafts", "get_error", "Rope", "KV_BF16", "KV_FP8", "KV_MLA656",
+           "KV_FP8_BLOCK", "KV_INT8_BLOCK", "PROB_F32",
            "PROB_BF16", "PROB_F16"]

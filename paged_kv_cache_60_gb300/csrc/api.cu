@@ -13,11 +13,12 @@
 
 namespace da {
 cudaError_t launch_sched_meta(const SchedParams &p, cudaStream_t stream, bool pdl);
-cudaError_t launch_gqa(int D, bool fp8, const CUtensorMap &tkv, const CUtensorMap &tv, const GqaParams &p,
+cudaError_t launch_gqa(int D, int kv_dtype, const CUtensorMap &tkv, const CUtensorMap &tv, const GqaParams &p,
                        cudaStream_t stream, bool pdl);
 cudaError_t launch_mla(const MlaParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_combine(int DV, const CombineParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_append(int kv_dtype, const AppendParams &p, cudaStream_t stream, bool pdl);
+cudaError_t launch_append_block(bool int8, const AppendBlockParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_rope(int kv_dtype, RopeParams p, int num_sms, cudaStream_t stream, bool pdl);
 int accum_heads(int row_bytes, int H_kv, int s_q);
 cudaError_t launch_accum(int D, bool fp8, const CUtensorMap &tk, const AccumParams &p, int num_sms,
@@ -44,6 +45,8 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 bool is_mla(const da_desc *d) { return d->kv_dtype == DA_KV_FP8_MLA656; }
+// a scale per block of 16 tokens and KV head
+bool has_blocks(const da_desc *d) { return d->kv_dtype == DA_KV_FP8_BLOCK || d->kv_dtype == DA_KV_INT8_BLOCK; }
 
 // query tokens per request (0 in the desc means 1)
 int sq_of(const da_desc *d) { return d->s_q <= 0 ? 1 : d->s_q; }
@@ -75,6 +78,11 @@ int check_desc(const da_desc *d) {
             if (d->G != 8 || d->D_qk != 128 || d->D_v != 128) return DA_ERR_UNSUPPORTED;
             if (sq > kMaxSqD128 || d->topk != 0) return DA_ERR_UNSUPPORTED;
             break;
+        case DA_KV_FP8_BLOCK:
+        case DA_KV_INT8_BLOCK:
+            if (d->G != 8 || d->D_qk != 128 || d->D_v != 128 || P % kScaleBlock != 0) return DA_ERR_UNSUPPORTED;
+            if (sq > kMaxSqD128 || d->topk != 0) return DA_ERR_UNSUPPORTED;
+            break;
         case DA_KV_FP8_MLA656:
             if (d->H_kv != 1 || d->D_qk != 576 || d->D_v != 512 || d->G != 128) return DA_ERR_UNSUPPORTED;
             if (sq > kMaxSqMla || d->window != 0 || (d->topk > 0 && sq != 1)) return DA_ERR_UNSUPPORTED;
@@ -103,7 +111,7 @@ int resolve_sms(const da_desc *d, int *nsm) {
         if (cpc * clusters < *nsm) *nsm = cpc * clusters;
     } else {
         // the GQA builds that run two CTAs per SM count two slots per SM
-        *nsm *= gqa_ctas_per_sm(d->D_qk, d->kv_dtype == DA_KV_FP8_PER_TENSOR, sq_of(d));
+        *nsm *= gqa_ctas_per_sm(d->D_qk, d->kv_dtype != DA_KV_BF16, sq_of(d));
     }
     return DA_OK;
 }
@@ -301,7 +309,7 @@ int da::check_fwd_args(const da_desc *desc, const void *q, const void *k_pool, c
     if (!aligned16(q) || !aligned16(k_pool) || (v_pool && !aligned16(v_pool)) || !aligned16(block_table) ||
         !aligned16(cache_seqlens) || !aligned16(out) || !aligned16(lse))
         return DA_ERR_ALIGN;
-    if (desc->kv_dtype == DA_KV_FP8_PER_TENSOR) {
+    if (desc->kv_dtype == DA_KV_FP8_PER_TENSOR || has_blocks(desc)) {
         if (!k_scale || !v_scale) return DA_ERR_SCALE;
         if ((reinterpret_cast<uintptr_t>(k_scale) & 3u) || (reinterpret_cast<uintptr_t>(v_scale) & 3u))
             return DA_ERR_ALIGN;
@@ -409,8 +417,7 @@ int decode_attn_fwd_ex(const da_desc *desc, const void *q, const void *k_pool, c
 
     const cudaEvent_t ev_begin = opts ? opts->main_begin : nullptr;
     if (!mla) {
-        const bool fp8 = desc->kv_dtype == DA_KV_FP8_PER_TENSOR;
-        const int es = fp8 ? 1 : 2;
+        const int es = desc->kv_dtype == DA_KV_BF16 ? 2 : 1;
         const int P = desc->page_size;
         const int box_tok = P < kChunk ? P : kChunk;
         // one map over both pools when their distance can be a tensor-map
@@ -466,7 +473,7 @@ int decode_attn_fwd_ex(const da_desc *desc, const void *q, const void *k_pool, c
         p.page_trace_cap = g_page_trace_cap;
         p.debug_stall = g_debug_stall;
         if (ev_begin && cudaEventRecord(ev_begin, stream) != cudaSuccess) return DA_ERR_CUDA;
-        if (launch_gqa(desc->D_qk, fp8, tkv, tv, p, stream, pdl) != cudaSuccess) return DA_ERR_CUDA;
+        if (launch_gqa(desc->D_qk, desc->kv_dtype, tkv, tv, p, stream, pdl) != cudaSuccess) return DA_ERR_CUDA;
     } else {
         MlaParams p;
         p.q = q;
@@ -571,6 +578,56 @@ int decode_attn_append_kv(const da_desc *desc, const void *k_new, const void *v_
     return DA_OK;
 }
 
+int decode_attn_append_block(const da_desc *desc, int32_t n_tokens, const void *k_new, int64_t k_stride,
+                             const void *v_new, int64_t v_stride, const int32_t *token_starts,
+                             const int32_t *positions, const int32_t *block_table, void *k_pool, void *v_pool,
+                             float *k_scale, float *v_scale, int32_t *device_error, cudaStream_t stream) {
+    if (!desc) return DA_ERR_NULL;
+    if (desc->B < 1 || desc->B > (1 << 20) || desc->H_kv < 1 || desc->H_kv > 4096 || desc->page_size < 1 ||
+        desc->max_pages_per_seq < 1 || desc->num_pages < 1)
+        return DA_ERR_DIMS;
+    if ((int64_t)desc->max_pages_per_seq * desc->page_size > (int64_t)INT32_MAX - 64 ||
+        (int64_t)desc->B * desc->max_pages_per_seq > (int64_t)INT32_MAX)
+        return DA_ERR_DIMS;
+    if (!has_blocks(desc) || desc->D_qk != 128 || desc->D_v != 128 || desc->page_size % kScaleBlock != 0)
+        return DA_ERR_UNSUPPORTED;
+    if (n_tokens < 0 || n_tokens > (1 << 30) || desc->s_q < 0 || desc->s_q > 64) return DA_ERR_DIMS;
+    const int sq = sq_of(desc);
+    if (!token_starts && n_tokens != 0 && n_tokens != (int64_t)desc->B * sq) return DA_ERR_DIMS;
+    const int64_t row_len = (int64_t)desc->H_kv * desc->D_qk;
+    int rc;
+    if ((rc = check_stride(&k_stride, row_len)) || (rc = check_stride(&v_stride, row_len))) return rc;
+    if (n_tokens == 0) return DA_OK;
+    if (!k_new || !v_new || !positions || !block_table || !k_pool || !v_pool) return DA_ERR_NULL;
+    if (!k_scale || !v_scale) return DA_ERR_SCALE;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned4(token_starts) ||
+        !aligned4(positions) || !aligned4(block_table) || !aligned4(k_scale) || !aligned4(v_scale) ||
+        !aligned4(device_error))
+        return DA_ERR_ALIGN;
+    AppendBlockParams p = {};
+    p.k = static_cast<const uint16_t *>(k_new);
+    p.v = static_cast<const uint16_t *>(v_new);
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.starts = token_starts;
+    p.positions = positions;
+    p.block_table = block_table;
+    p.k_pool = static_cast<uint8_t *>(k_pool);
+    p.v_pool = static_cast<uint8_t *>(v_pool);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.error = device_error;
+    p.N = n_tokens;
+    p.B = desc->B;
+    p.H_kv = desc->H_kv;
+    p.s_q = sq;
+    p.page_size = desc->page_size;
+    p.max_pages = desc->max_pages_per_seq;
+    p.num_pages = desc->num_pages;
+    if (launch_append_block(desc->kv_dtype == DA_KV_INT8_BLOCK, p, stream, true) != cudaSuccess) return DA_ERR_CUDA;
+    return DA_OK;
+}
+
 int decode_attn_rope_append(const da_desc *desc, const da_rope *rope, int32_t n_tokens, const void *q,
                             int64_t q_stride, const void *k_new, int64_t k_stride, const void *v_new,
                             int64_t v_stride, const float *inv_freq, const int32_t *rope_positions,
@@ -669,7 +726,7 @@ int decode_attn_accum_weights(const da_desc *desc, const void *q, const void *k_
     MetaLayout L;
     const int rc = make_layout(desc, &L);
     if (rc) return rc;
-    if (desc->window != 0 || desc->topk != 0) return DA_ERR_UNSUPPORTED;
+    if (desc->window != 0 || desc->topk != 0 || has_blocks(desc)) return DA_ERR_UNSUPPORTED;
     // token indices run past the last one by less than the kernel's unit
     if (is_mla(desc) && (int64_t)desc->max_pages_per_seq * desc->page_size > (int64_t)INT32_MAX - 256) return DA_ERR_DIMS;
     if (!(decay >= 0.f) || std::isinf(decay)) return DA_ERR_DIMS;

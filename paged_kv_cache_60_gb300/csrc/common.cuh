@@ -121,6 +121,14 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t by
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// 4 bytes into shared memory asynchronously; then, once this thread's copies have
+// landed, one arrival on `bar` (one of those that it was initialised to expect).
+__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_mbar_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -291,6 +299,15 @@ __device__ __forceinline__ float ldg_stream4f(const void *ptr) {
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
     uint32_t y;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(x));
+    return y;
+}
+// Two int8 of a word (bytes LO and HI) to two f16 (exact): the bytes c + 128
+// under 0x64 are the f16 values 1024 + 128 + c.
+template <int LO, int HI>
+__device__ __forceinline__ uint32_t int8x2_to_f16x2(uint32_t w) {
+    uint32_t y, off = 0x64806480u;  // 1152, twice
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(y) : "r"(w ^ 0x80808080u), "r"(0x64646464u), "n"(0x4040 | LO | HI << 8));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(off));
     return y;
 }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {

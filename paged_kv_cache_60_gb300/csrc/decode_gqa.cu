@@ -1,5 +1,6 @@
 // Split-KV decode kernel for grouped-query attention with G = 8 query heads
-// per KV head (bf16 KV with D = 64 / 128, e4m3 KV with D = 128).
+// per KV head (bf16 KV with D = 64 / 128; D = 128: e4m3 KV with a scale per head,
+// e4m3 or int8 KV with a scale per block of 16 tokens and head).
 //
 // One CTA per (part, KV head). A part is a list of (request, chunk range)
 // segments from the scheduling metadata; a chunk is 64 tokens.
@@ -29,6 +30,14 @@
 //    two values per cvt; the per-tensor scales are folded into the score scale
 //    (k_scale) and into the output (v_scale) (same page, section
 //    "Hopper 路径上 V 不做显式反量化").
+//  * scales per block of 16 tokens: a block is one 16-token tile of the products, so
+//    a tile's scores take its K scale with the softmax's, and its P V product is made
+//    from zero and added to O times its V scale, in fp32. (The V scale folded into P
+//    would save that multiply-add and lose weights below 2^-14 of the largest scale in
+//    P's f16.) The scales of a chunk, four of K and four of V, come by 4-byte
+//    cp.async of eight producer lanes, whose arrivals the stage's full barrier counts. int8
+//    codes become f16 by a byte permute and one subtraction (0x6400 | c + 128 is
+//    1024 + 128 + c), exactly.
 //  * several query tokens per request (linear speculative-decoding
 //    verification, XQA page, section "投机解码:XQA 的第二个工作负载"): the
 //    s_q draft tokens' G heads become NQ n8 tiles on the N side, so every K/V
@@ -51,9 +60,13 @@
 namespace da {
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kScaleLanes = 2 * kChunk / kScaleBlock;  // scales of a chunk: K, V
+static_assert(kScaleBlock == 16, "a block is one tile of the products");
 
-template <int D, bool FP8, int NQ, int WPC>
+template <int D, int KV, int NQ, int WPC>
 struct GqaCfg {
+    static constexpr bool FP8 = KV != DA_KV_BF16;  // codes of 8 bits
+    static constexpr bool BLK = KV == DA_KV_FP8_BLOCK || KV == DA_KV_INT8_BLOCK;
     static constexpr int G = 8;
     static constexpr int ES = FP8 ? 1 : 2;
     static constexpr int ROW = D * ES;       // bytes of one token's head
@@ -88,7 +101,8 @@ struct GqaCfg {
     static constexpr int OFF_L = OFF_M + NCW * G * 4;
     static constexpr int OFF_W = OFF_L + NCW * G * 4;
     static constexpr int OFF_FIN = OFF_W + NCW * G * 4;
-    static constexpr int OFF_BAR = (OFF_FIN + 4 * G * 4 + 7) / 8 * 8;
+    static constexpr int OFF_SC = OFF_FIN + 4 * G * 4;  // per stage: K scales of its four tiles, V scales
+    static constexpr int OFF_BAR = (OFF_SC + (BLK ? NS * kScaleLanes * 4 : 0) + 7) / 8 * 8;
     static constexpr int OFF_FLAG = OFF_BAR + 2 * NS * 8;
     static constexpr int SMEM = OFF_FLAG + 16 + 1024;  // + alignment slack
     static constexpr int MIN_BLOCKS = ((D == 64 && !FP8 && NQ == 1 && WPC == 1) || TWO_PER_SM) ? 2 : 1;
@@ -189,11 +203,12 @@ __device__ __noinline__ void cluster_merge(const MergeArgs p, float *xo, float *
 // NQ * WPC; warp w of a chunk's group holds tokens [(w % WPC) NQ, (w % WPC + 1)
 // NQ), and tokens j >= s_q are zero rows that are never written). WIN: built
 // with sliding window support (without it, p.window must be 0).
-template <int D, bool FP8, int NQ, int WPC, bool WIN>
-__global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP8, NQ, WPC>::MIN_BLOCKS)
+template <int D, int KV, int NQ, int WPC, bool WIN>
+__global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV, NQ, WPC>::MIN_BLOCKS)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ GqaParams p) {
-    using C = GqaCfg<D, FP8, NQ, WPC>;
+    using C = GqaCfg<D, KV, NQ, WPC>;
+    constexpr bool FP8 = C::FP8, BLK = C::BLK, I8 = KV == DA_KV_INT8_BLOCK;
     // 256-byte rows land half-major in the builds with a window or several
     // query tokens (the host builds the tensor maps to match: p.half_major)
     constexpr bool HM = WIN && C::NX > 1;
@@ -204,6 +219,7 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
     float *sm_l = reinterpret_cast<float *>(smem + C::OFF_L);
     float *sm_w = reinterpret_cast<float *>(smem + C::OFF_W);
     float *sm_fin = reinterpret_cast<float *>(smem + C::OFF_FIN);
+    float *sm_sc = reinterpret_cast<float *>(smem + C::OFF_SC);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *empty = full + C::NS;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
@@ -213,7 +229,7 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&full[i], p.boxes_per_chunk);  // one arrival per producer lane
+            mbar_init(&full[i], p.boxes_per_chunk + (BLK ? kScaleLanes : 0));  // one arrival per box and scale
             mbar_init(&empty[i], WPC);  // every warp of the chunk's group
         }
         *abort_flag = 0;
@@ -256,8 +272,9 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
         // page ids of its next four chunks in registers, loaded four chunks
         // ahead, arrives on the chunk's full barrier with its own byte count
         // and issues its own copy -- no shuffles, no load latency in the loop.
+        // With scales per block, lane t < 8 also brings the K (t < 4) or V scale of tile t & 3.
         const int nb = p.boxes_per_chunk, bt = p.box_tokens, P = p.page_size;
-        if (lane >= nb) return;
+        if (lane >= (BLK ? kScaleLanes : nb)) return;
         const uint64_t pol = policy_evict_first();
         const uint32_t box_bytes = 2u * bt * C::NX * 128u;
         SegWalker wk = make_walker(p.meta, rec0, rec1, p.B, p.seqlens, max_len, p.s_q, WIN ? p.window : 0, 0);
@@ -277,15 +294,29 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
                 const int tok = (fc + lc) * kChunk + lane * bt;
                 return (lc < lc1 && tok < L && tok + bt > start) ? bt_row[tok / P] : -2;
             };
-            int ring[4];
+            // the same of this lane's scale
+            const int st_tok = (lane & (kChunk / kScaleBlock - 1)) * kScaleBlock;
+            auto scale_id_of = [&](int lc) -> int {
+                const int tok = (fc + lc) * kChunk + st_tok;
+                return (lc < lc1 && tok < L && tok + kScaleBlock > start) ? bt_row[tok / P] : -2;
+            };
+            int ring[4], sring[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) ring[k] = id_of(lc0 + k);
+            for (int k = 0; k < 4; ++k) {
+                ring[k] = !BLK || lane < nb ? id_of(lc0 + k) : -2;
+                if constexpr (BLK) sring[k] = scale_id_of(lc0 + k);
+            }
             for (int lc = lc0; lc < lc1 && !aborted; lc += 4) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (lc + k >= lc1) break;
                     int pg = ring[k];
-                    ring[k] = id_of(lc + k + 4);
+                    ring[k] = !BLK || lane < nb ? id_of(lc + k + 4) : -2;
+                    int spg = -2;
+                    if constexpr (BLK) {
+                        spg = sring[k];
+                        sring[k] = scale_id_of(lc + k + 4);
+                    }
                     const int stage = i % C::NS;
                     if (!mbar_wait_bounded(&empty[stage], ((i / C::NS) & 1) ^ 1, abort_flag, p.wait_limit_ns)) {
                         atomicOr(&p.meta.header[kHError], DA_DEV_TIMEOUT);
@@ -297,6 +328,22 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
                         atomicOr(&p.meta.header[kHError], DA_DEV_BAD_PAGE);
                         p.meta.header[kHErrorDetail] = pg;
                         pg = -2;  // skipped: its rows keep stale bytes
+                    }
+                    if constexpr (BLK) {
+                        float *sc = sm_sc + stage * kScaleLanes + lane;
+                        if (spg >= 0 && spg < p.num_pages) {
+                            const int in_page = ((fc + lc + k) * kChunk + st_tok) % P;
+                            cp_async4(sc, (lane < kScaleLanes / 2 ? p.k_scale : p.v_scale) +
+                                              ((size_t)spg * p.H_kv + h) * (P / kScaleBlock) + in_page / kScaleBlock);
+                            cp_async_mbar_arrive(&full[stage]);
+                        } else {  // no token here
+                            *sc = 0.f;
+                            mbar_arrive(&full[stage]);
+                        }
+                        if (lane >= nb) {
+                            ++i;
+                            continue;
+                        }
                     }
 #ifdef DA_PAGE_TRACE
                     if (p.page_trace && i < p.page_trace_cap) {
@@ -341,8 +388,8 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
     const int grp = warp / WPC, jo = (warp % WPC) * NQ;  // this warp's group and first query token
     const int lrow = lane & 7, lmat = lane >> 3;
     const int ctid = threadIdx.x;  // 0 .. NCW*32-1
-    const float kscale = FP8 ? p.k_scale[h] : 1.f;
-    const float vscale = FP8 ? p.v_scale[h] : 1.f;
+    const float kscale = FP8 && !BLK ? p.k_scale[h] : 1.f;
+    const float vscale = FP8 && !BLK ? p.v_scale[h] : 1.f;
     const float sl2 = p.scale_log2 * kscale;
     // Stage layout: box j (tokens [j*bt, (j+1)*bt)) at j*box_bytes holds one
     // pool's rows, then the other's (p.kv_swap tells which pool comes first).
@@ -475,6 +522,13 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
                 if (tail) zero_v(nvalid, kChunk);
                 __syncwarp();
             }
+            [[maybe_unused]] float ksc[4], vsc[4];  // per tile: softmax scale times K scale; V scale
+            if constexpr (BLK) {
+                const float4 a = *reinterpret_cast<const float4 *>(sm_sc + stage * kScaleLanes);
+                const float4 b = *reinterpret_cast<const float4 *>(sm_sc + stage * kScaleLanes + 4);
+                ksc[0] = sl2 * a.x, ksc[1] = sl2 * a.y, ksc[2] = sl2 * a.z, ksc[3] = sl2 * a.w;
+                vsc[0] = b.x, vsc[1] = b.y, vsc[2] = b.z, vsc[3] = b.w;
+            }
             // ---- S^T = K Q^T for four independent 16-token tiles
             float sacc[4][NQ][4];
 #pragma unroll
@@ -509,10 +563,17 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
                         for (int hf = 0; hf < 2; ++hf) {
                             const uint32_t ra = R[hf * 2], rb = R[hf * 2 + 1];
                             uint32_t a[4];
-                            a[0] = e4m3x2_to_f16x2((uint16_t)(ra & 0xffff));
-                            a[1] = e4m3x2_to_f16x2((uint16_t)(rb & 0xffff));
-                            a[2] = e4m3x2_to_f16x2((uint16_t)(ra >> 16));
-                            a[3] = e4m3x2_to_f16x2((uint16_t)(rb >> 16));
+                            if constexpr (I8) {
+                                a[0] = int8x2_to_f16x2<0, 1>(ra);
+                                a[1] = int8x2_to_f16x2<0, 1>(rb);
+                                a[2] = int8x2_to_f16x2<2, 3>(ra);
+                                a[3] = int8x2_to_f16x2<2, 3>(rb);
+                            } else {
+                                a[0] = e4m3x2_to_f16x2((uint16_t)(ra & 0xffff));
+                                a[1] = e4m3x2_to_f16x2((uint16_t)(rb & 0xffff));
+                                a[2] = e4m3x2_to_f16x2((uint16_t)(ra >> 16));
+                                a[3] = e4m3x2_to_f16x2((uint16_t)(rb >> 16));
+                            }
 #pragma unroll
                             for (int j = 0; j < NQ; ++j)
                                 mma_f16(sacc[t][j], a, qf[kk * 2 + hf][j][0], qf[kk * 2 + hf][j][1]);
@@ -533,10 +594,11 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
                 for (int t = 0; t < 4; ++t) {
                     const int ra = 16 * t + r8, rb = ra + 8;
                     const bool va = ra < nv && ra >= lv, vb = rb < nv && rb >= lv;
-                    sv[t][0] = va ? sacc[t][j][0] * sl2 : -INFINITY;
-                    sv[t][1] = va ? sacc[t][j][1] * sl2 : -INFINITY;
-                    sv[t][2] = vb ? sacc[t][j][2] * sl2 : -INFINITY;
-                    sv[t][3] = vb ? sacc[t][j][3] * sl2 : -INFINITY;
+                    const float sc = BLK ? ksc[t] : sl2;
+                    sv[t][0] = va ? sacc[t][j][0] * sc : -INFINITY;
+                    sv[t][1] = va ? sacc[t][j][1] * sc : -INFINITY;
+                    sv[t][2] = vb ? sacc[t][j][2] * sc : -INFINITY;
+                    sv[t][3] = vb ? sacc[t][j][3] * sc : -INFINITY;
                     mx0 = fmaxf(mx0, fmaxf(sv[t][0], sv[t][2]));
                     mx1 = fmaxf(mx1, fmaxf(sv[t][1], sv[t][3]));
                 }
@@ -602,15 +664,32 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
                             // bytes of R: [v(t,d), v(t,d+1), v(t+1,d), v(t+1,d+1)] -> token pairs per d
-                            const uint32_t u = prmt(R[hf * 2], 0u, 0x3120u);
-                            const uint32_t w = prmt(R[hf * 2 + 1], 0u, 0x3120u);
                             uint32_t a[4];
-                            a[0] = e4m3x2_to_f16x2((uint16_t)(u & 0xffff));
-                            a[1] = e4m3x2_to_f16x2((uint16_t)(u >> 16));
-                            a[2] = e4m3x2_to_f16x2((uint16_t)(w & 0xffff));
-                            a[3] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+                            if constexpr (I8) {
+                                a[0] = int8x2_to_f16x2<0, 2>(R[hf * 2]);
+                                a[1] = int8x2_to_f16x2<1, 3>(R[hf * 2]);
+                                a[2] = int8x2_to_f16x2<0, 2>(R[hf * 2 + 1]);
+                                a[3] = int8x2_to_f16x2<1, 3>(R[hf * 2 + 1]);
+                            } else {
+                                const uint32_t u = prmt(R[hf * 2], 0u, 0x3120u);
+                                const uint32_t w = prmt(R[hf * 2 + 1], 0u, 0x3120u);
+                                a[0] = e4m3x2_to_f16x2((uint16_t)(u & 0xffff));
+                                a[1] = e4m3x2_to_f16x2((uint16_t)(u >> 16));
+                                a[2] = e4m3x2_to_f16x2((uint16_t)(w & 0xffff));
+                                a[3] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+                            }
 #pragma unroll
-                            for (int j = 0; j < NQ; ++j) mma_f16(acc[kk * 2 + hf][j], a, pb[t][j][0], pb[t][j][1]);
+                            for (int j = 0; j < NQ; ++j) {
+                                float(&o)[4] = acc[kk * 2 + hf][j];
+                                if constexpr (BLK) {
+                                    float pv[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma_f16(pv, a, pb[t][j][0], pb[t][j][1]);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[e] = fmaf(vsc[t], pv[e], o[e]);
+                                } else {
+                                    mma_f16(o, a, pb[t][j][0], pb[t][j][1]);
+                                }
+                            }
                         }
                     }
                 }
@@ -725,11 +804,11 @@ __global__ void __launch_bounds__(GqaCfg<D, FP8, NQ, WPC>::THREADS, GqaCfg<D, FP
                          *abort_flag != 0);
 }
 
-template <int D, bool FP8, int NQ, int WPC, bool WIN>
+template <int D, int KV, int NQ, int WPC, bool WIN>
 static cudaError_t launch_one(const CUtensorMap &tkv, const CUtensorMap &tv, const GqaParams &p, cudaStream_t stream,
                               bool pdl) {
-    using C = GqaCfg<D, FP8, NQ, WPC>;
-    auto kern = gqa_decode_kernel<D, FP8, NQ, WPC, WIN>;
+    using C = GqaCfg<D, KV, NQ, WPC>;
+    auto kern = gqa_decode_kernel<D, KV, NQ, WPC, WIN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -761,30 +840,28 @@ int gqa_ctas_per_sm(int D, bool fp8, int s_q) {
     return (!fp8 && D == 64 && s_q >= 3 && s_q <= 4) ? 2 : 1;
 }
 
-cudaError_t launch_gqa(int D, bool fp8, const CUtensorMap &tkv, const CUtensorMap &tv, const GqaParams &p,
-                       cudaStream_t stream, bool pdl) {
-    // one token without a window: the lean build; every other shape carries the
-    // window logic. Three or four query tokens: four warps per chunk, one token
-    // each, at D = 64 (8 consumer warps); a pair of warps, two each, at D = 128.
-    if (p.s_q == 1 && p.window == 0) {
-        if (!fp8 && D == 64) return launch_one<64, false, 1, 1, false>(tkv, tv, p, stream, pdl);
-        if (!fp8 && D == 128) return launch_one<128, false, 1, 1, false>(tkv, tv, p, stream, pdl);
-        if (fp8 && D == 128) return launch_one<128, true, 1, 1, false>(tkv, tv, p, stream, pdl);
-    } else if (p.s_q == 1) {
-        if (!fp8 && D == 64) return launch_one<64, false, 1, 1, true>(tkv, tv, p, stream, pdl);
-        if (!fp8 && D == 128) return launch_one<128, false, 1, 1, true>(tkv, tv, p, stream, pdl);
-        if (fp8 && D == 128) return launch_one<128, true, 1, 1, true>(tkv, tv, p, stream, pdl);
-    } else if (p.s_q == 2) {
-        if (!fp8 && D == 64) return launch_one<64, false, 2, 1, true>(tkv, tv, p, stream, pdl);
-        if (!fp8 && D == 128) return launch_one<128, false, 2, 1, true>(tkv, tv, p, stream, pdl);
-        if (fp8 && D == 128) return launch_one<128, true, 2, 1, true>(tkv, tv, p, stream, pdl);
-    } else if (p.s_q <= 4) {
-        if (!fp8 && D == 64) return launch_one<64, false, 1, 4, true>(tkv, tv, p, stream, pdl);
-        if (!fp8 && D == 128) return launch_one<128, false, 2, 2, true>(tkv, tv, p, stream, pdl);
-        if (fp8 && D == 128) return launch_one<128, true, 2, 2, true>(tkv, tv, p, stream, pdl);
-    }
+// one token without a window: the lean build; every other shape carries the
+// window logic. Three or four query tokens: four warps per chunk, one token
+// each, at D = 64 (8 consumer warps); a pair of warps, two each, at D = 128.
+template <int D, int KV>
+static cudaError_t launch_kv(const CUtensorMap &tkv, const CUtensorMap &tv, const GqaParams &p, cudaStream_t stream,
+                             bool pdl) {
+    if (p.s_q == 1 && p.window == 0) return launch_one<D, KV, 1, 1, false>(tkv, tv, p, stream, pdl);
+    if (p.s_q == 1) return launch_one<D, KV, 1, 1, true>(tkv, tv, p, stream, pdl);
+    if (p.s_q == 2) return launch_one<D, KV, 2, 1, true>(tkv, tv, p, stream, pdl);
+    if (p.s_q <= 4) return launch_one<D, KV, D == 64 ? 1 : 2, D == 64 ? 4 : 2, true>(tkv, tv, p, stream, pdl);
     return cudaErrorInvalidValue;
 }
 
+cudaError_t launch_gqa(int D, int kv_dtype, const CUtensorMap &tkv, const CUtensorMap &tv, const GqaParams &p,
+                       cudaStream_t stream, bool pdl) {
+    if (kv_dtype == DA_KV_BF16 && D == 64) return launch_kv<64, DA_KV_BF16>(tkv, tv, p, stream, pdl);
+    if (kv_dtype == DA_KV_BF16 && D == 128) return launch_kv<128, DA_KV_BF16>(tkv, tv, p, stream, pdl);
+    if (kv_dtype == DA_KV_FP8_PER_TENSOR && D == 128)
+        return launch_kv<128, DA_KV_FP8_PER_TENSOR>(tkv, tv, p, stream, pdl);
+    if (kv_dtype == DA_KV_FP8_BLOCK && D == 128) return launch_kv<128, DA_KV_FP8_BLOCK>(tkv, tv, p, stream, pdl);
+    if (kv_dtype == DA_KV_INT8_BLOCK && D == 128) return launch_kv<128, DA_KV_INT8_BLOCK>(tkv, tv, p, stream, pdl);
+    return cudaErrorInvalidValue;
+}
 
 }  // namespace da

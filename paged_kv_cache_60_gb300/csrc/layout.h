@@ -7,6 +7,7 @@
 namespace da {
 
 constexpr int kChunk = 64;                 // tokens per scheduling chunk
+constexpr int kScaleBlock = 16;            // tokens that share a scale (block formats)
 constexpr int kTmaElemBytes = 8;           // element size the pool tensor maps are described with
 constexpr int32_t kMetaMagic = 0x44414d31;  // "DAM1"
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per pipeline wait
@@ -94,7 +95,7 @@ struct GqaParams {
     const void *q;                 // bf16 [B][s_q][H_q][D]
     const int32_t *block_table;    // [B][max_pages]
     const int32_t *seqlens;        // [B]
-    const float *k_scale;          // [H_kv] (fp8) or null
+    const float *k_scale;          // [H_kv] (fp8), [num_pages][H_kv][page_size / 16] (block formats) or null
     const float *v_scale;
     MetaView meta;
     void *out;                     // bf16 [B][s_q][H_q][D]
@@ -156,6 +157,21 @@ struct AppendParams {
     int32_t *error;                // device word, error bits OR-ed in; may be null
     int64_t row_stride;            // bf16 elements between consecutive requests of k_new / v_new
     int32_t B, H_kv, D, page_size, max_pages, num_pages;
+};
+
+// Append to a cache with scales per block (append_block.cu).
+struct AppendBlockParams {
+    const uint16_t *k, *v;         // bf16 rows, token n at + n * stride
+    int64_t k_stride, v_stride;
+    const int32_t *starts;         // [B + 1] first row of each request, or null: s_q rows each
+    const int32_t *positions;      // [B] where the first row goes; < 0: request skipped
+    const int32_t *block_table;    // [B][max_pages]
+    uint8_t *k_pool, *v_pool;
+    float *k_scale, *v_scale;      // [num_pages][H_kv][page_size / 16]
+    int32_t *error;                // may be null
+    int32_t N, B, H_kv, s_q, page_size, max_pages, num_pages;
+    int32_t per_request;           // block slots of a request where starts is null
+    int64_t jobs;                  // block slots x 2 H_kv
 };
 
 // Rotary positions + append (rope.cu).

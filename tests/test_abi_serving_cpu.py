@@ -1,0 +1,81 @@
+"""Host-side checks of the cache with scales per block, the page operators and
+the token probabilities, without a GPU: the C entry points refuse bad arguments
+with the documented codes before any launch, and the Python binding refuses
+tensors that are not what the call reads."""
+import ctypes
+
+import pytest
+import torch
+
+import paged_kv_cache_60_gb300 as da
+from paged_kv_cache_60_gb300 import build as dabuild
+
+P = ctypes.c_void_p
+G = P(0x100000)          # a well-aligned address that nothing may read
+
+
+@pytest.fixture(scope="module")
+def lib():
+    dabuild.build()
+    return da.load_library()
+
+
+def _desc(**kw):
+    base = dict(B=4, H_kv=2, G=8, D_qk=128, D_v=128, page_size=16, max_pages_per_seq=10, num_pages=40, kv_dtype=da.KV_FP8_BLOCK,
+                splits=0, num_sms=152)
+    return da.Desc.make(**{**base, **kw})
+
+
+BLOCKS = [da.KV_FP8_BLOCK, da.KV_INT8_BLOCK]
+
+
+@pytest.mark.parametrize("kv", BLOCKS)
+def test_block_formats_in_the_attention_calls(lib, kv):
+    n = ctypes.c_size_t(0)
+
+    def rc(**kw):
+        return lib.decode_attn_sched_meta_bytes(ctypes.byref(_desc(kv_dtype=kv, **kw)), ctypes.byref(n))
+    assert rc() == 0 and rc(s_q=4) == 0 and rc(window=64) == 0 and rc(page_size=192) == 0
+    assert rc(s_q=5) == -3 and rc(page_size=8) == -3 and rc(D_qk=64, D_v=64) == -3 and rc(topk=8) == -3 and rc(G=4) == -3
+    d = _desc(kv_dtype=kv)
+    size = da.sched_meta_bytes(d)
+
+    def fwd(ks, vs):
+        return lib.decode_attn_fwd(ctypes.byref(d), G, G, G, ks, vs, G, G, G, size, G, G, None)
+    assert fwd(None, G) == -8 and fwd(G, None) == -8 and fwd(P(0x100002), G) == -4
+    # the operators that do not know the format refuse it
+    assert lib.decode_attn_append_kv(ctypes.byref(d), G, G, 0, G, G, G, G, G, G, None, None) == -3
+    r = da.Rope.make(128)
+    assert lib.decode_attn_rope_append(ctypes.byref(d), ctypes.byref(r), 4, G, 0, G, 0, G, 0, G, G, G, G, G, P(0x900000), G, G, G, G, None,
+                                       None) == -3
+    assert lib.decode_attn_accum_weights(ctypes.byref(d), G, G, G, G, G, G, size, G, None, None, 1.0, G, None) == -3
+    assert lib.decode_attn_evict(ctypes.byref(d), 10, 0, 0, G, G, P(0x200000), G, G, G, G, P(0x300000), None, None) == -3
+
+
+@pytest.mark.parametrize("kv", BLOCKS)
+def test_append_block_refusals(lib, kv):
+    def call(d, n=4, k=G, ks=0, v=G, vs=0, starts=G, pos=G, bt=G, kp=G, vp=G, sk=G, sv=G, err=None):
+        return lib.decode_attn_append_block(ctypes.byref(d), n, k, ks, v, vs, starts, pos, bt, kp, vp, sk, sv, err, None)
+    d = _desc(kv_dtype=kv)
+    for name in ("k", "v", "pos", "bt", "kp", "vp"):
+        assert call(d, **{name: None}) == -1, name
+        assert call(d, **{name: P(0x100008 if name in ("k", "v", "kp", "vp") else 0x100002)}) == -4, name
+    for name in ("sk", "sv"):
+        assert call(d, **{name: None}) == -8 and call(d, **{name: P(0x100002)}) == -4
+    assert call(d, starts=P(0x100001)) == -4 and call(d, err=P(0x100002)) == -4
+    assert call(d, n=-1) == -2 and call(d, n=(1 << 30) + 1) == -2
+    assert call(d, n=0) == 0 and call(d, n=0, k=None, sk=None) == 0             # nothing to do
+    assert call(d, starts=None, n=5) == -2                                      # not B * s_q tokens
+    assert call(d, ks=248) == -2 and call(d, vs=260) == -2
+    for bad in (dict(B=0), dict(H_kv=0), dict(H_kv=4097), dict(page_size=0), dict(num_pages=0), dict(max_pages_per_seq=1 << 28), dict(s_q=65)):
+        assert call(_desc(kv_dtype=kv, **bad)) == -2, bad
+    for bad in (dict(D_qk=64, D_v=64), dict(D_v=64), dict(page_size=8), dict(page_size=24), dict(kv_dtype=da.KV_BF16), dict(kv_dtype=da.KV_FP8)):
+        assert call(_desc(**{**dict(kv_dtype=kv), **bad})) == -3, bad
+    assert lib.decode_attn_append_block(None, 4, *[G, 0] * 2, *[G] * 7, None, None) == -1
+
+
+def test_binding_refuses_host_tensors_and_shapes():
+    z, i32 = torch.zeros, torch.int32
+    d = _desc()
+    with pytest.raises(da.DecodeAttnError):
+        da.append_block(d, z(4, 256), z(4, 256), z(4, dtype=i32), z(4, 10, dtype=i32), z(1), z(1), z(40, 2, 1), z(40, 2, 1))
