@@ -115,6 +115,7 @@ typedef struct {
 #define DA_DEV_BAD_TOKEN      32   /* a draft token >= vocab: taken as the end of its chain */
 #define DA_DEV_BAD_PROBS      64   /* a row without a positive probability: the next token is -1 */
 #define DA_DEV_BAD_REQUEST   128   /* a request index outside [0, B): the token's K and V are skipped */
+#define DA_DEV_NO_PAGES      256   /* fewer free pages than a reservation needs: nothing was changed */
 
 /*
  * Library plumbing from here to decode_attn_num_parts: no page defines these
@@ -440,6 +441,97 @@ int decode_attn_evict(const da_desc *desc, int32_t budget, int32_t keep_first, i
                       const int32_t *cache_seqlens, const int32_t *block_table, const int32_t *dst_block_table,
                       void *k_pool, void *v_pool, float *weights, int32_t *kept, int32_t *new_seqlens,
                       int32_t *device_error, cudaStream_t stream);
+
+/*
+ * The pages of a cache, for callers that keep its tables on the device. (No counterpart
+ * on the source pages.) The state is the block table, cache_seqlens, and
+ *   held: int32 [B], the table entries [0, held[b]) that request b holds (at least
+ *     those of its tokens; more after a reservation),
+ *   refs: int32 [num_pages], how many hold each page: table entries, and whoever else
+ *     counts (a prefix cache adds its own). 0: the page is free.
+ * A fork shares pages; a reservation makes what is written next the request's own:
+ *
+ *     fork_pages -> reserve_pages -> copy_pages -> append -> sched_meta -> fwd ...
+ *
+ * One set of tables serves all layers: copies (pairs of pages) are planned once and
+ * decode_attn_copy_pages carries them out in each layer's pools. Of desc these calls read
+ * B (at most 8192), page_size, max_pages_per_seq, num_pages (at most 2^23) and, where
+ * noted, s_q. device_error: device int32 or NULL; DA_DEV_BAD_PAGE (an entry outside
+ * [0, num_pages): skipped) is OR-ed into it by all of them. Pointers are device
+ * pointers, 4-byte aligned (copies: 8). Results do not depend on the order of anything on
+ * the device. Launches on `stream`; no allocation, no sync.
+ *
+ * fork_pages: new row i continues row parents[i] of the old rows (-1: an empty row), a
+ * beam step or parallel samples: the entries of the parent's tokens, ceil(L / P) of them,
+ * are shared, entries that it holds beyond are not. Every old row lets go of what it
+ * holds, so a row that is no one's parent is freed. new_held, new_seqlens: of the new
+ * rows; entries of new_block_table past new_held keep what they were. The new buffers are
+ * not the old ones (DA_ERR_UNSUPPORTED). A parent >= B: DA_DEV_BAD_REQUEST, the row is
+ * empty. A negative length counts as 0 (DA_DEV_NEG_LEN). One kernel.
+ */
+int decode_attn_fork_pages(const da_desc *desc, const int32_t *parents, const int32_t *cache_seqlens,
+                           const int32_t *block_table, const int32_t *held, int32_t *refs, int32_t *new_block_table,
+                           int32_t *new_held, int32_t *new_seqlens, int32_t *device_error, cudaStream_t stream);
+
+/*
+ * free_pages: rows with done[b] != 0 let go of all that they hold, in place; held[b] and
+ * cache_seqlens[b] become 0. One kernel.
+ */
+int decode_attn_free_pages(const da_desc *desc, const int32_t *done, int32_t *cache_seqlens,
+                           const int32_t *block_table, int32_t *held, int32_t *refs, int32_t *device_error,
+                           cudaStream_t stream);
+
+/*
+ * reserve_pages: room for new_tokens[b] more tokens of each request (NULL: s_q each;
+ * <= 0: none, the row is left alone), which nobody else holds. In place:
+ *   - entries are added up to ceil((L_b + n) / P), held[b] follows;
+ *   - where the page of the next token has tokens on it (L_b mod P != 0) and others hold
+ *     it, the row gets a fresh page in its place and copies[b] = (old, new); if every
+ *     holder is a row of this call that asks for room there, the lowest row keeps the page
+ *     without a copy. Rows without a copy: (-1, -1);
+ *   - entries that the row holds past its tokens, if others hold one that it would write
+ *     to, are given back and fresh ones taken.
+ * Fresh pages are the lowest that were free before the call, in the order of the rows, and
+ * in a row the copy's first. copies: int32 [B][2], the copies argument of
+ * decode_attn_copy_pages. missing: int32 [1], 0; or, where the pool has too few free
+ * pages, how many are missing: then nothing is changed (all copies are -1,
+ * DA_DEV_NO_PAGES). A row that would pass max_pages_per_seq * page_size is left alone
+ * (DA_DEV_SEQ_TOO_LONG); a negative length counts as 0 (DA_DEV_NEG_LEN). One kernel.
+ */
+int decode_attn_reserve_pages(const da_desc *desc, const int32_t *new_tokens, const int32_t *cache_seqlens,
+                              int32_t *block_table, int32_t *held, int32_t *refs, int32_t *copies, int32_t *missing,
+                              int32_t *device_error, cudaStream_t stream);
+
+/*
+ * compact_pages: plans the move of all pages in use (refs > 0), N of them, to [0, N): the
+ * i-th page in use at or above N goes to the i-th free one below it. Out of place, so
+ * that the old state is good until the copies are done:
+ *   new_page: int32 [num_pages], where each page goes (itself if it stays, -1 if it is
+ *     free), also for holders outside the table. new_refs: int32 [num_pages].
+ *     new_block_table: the held entries, mapped (the others keep what they were).
+ *   copies: int32 [num_pages / 2][2], the pairs; counts: int32 [2], N and the number of
+ *     pairs (the num_copies of decode_attn_copy_pages is counts + 1).
+ * None of the new buffers is an old one (DA_ERR_UNSUPPORTED). Two kernels.
+ */
+int decode_attn_compact_pages(const da_desc *desc, const int32_t *block_table, const int32_t *held, const int32_t *refs,
+                              int32_t *new_block_table, int32_t *new_refs, int32_t *new_page, int32_t *copies,
+                              int32_t *counts, int32_t *device_error, cudaStream_t stream);
+
+/*
+ * copy_pages: copies whole pages of a cache, all formats: K, V, their scales (block
+ * formats) and, if given, the weights of decode_attn_accum_weights.
+ *   desc: H_kv, D_qk, D_v, page_size, num_pages, kv_dtype; a page of a pool has to be a
+ *     multiple of 16 bytes (DA_ERR_UNSUPPORTED).
+ *   copies: device int32 [max_copies][2] (source, destination), a negative source: none;
+ *     a page outside the pool: skipped (DA_DEV_BAD_PAGE). num_copies: device int32 [1] or
+ *     NULL (all): only the first of them. No destination may be a source, or stand twice.
+ *   k_scale, v_scale: the block formats' scales, else ignored. weights: fp32
+ *     [num_pages][H_kv][page_size] or NULL. v_pool: NULL or k_pool for the 656-byte token.
+ * One kernel.
+ */
+int decode_attn_copy_pages(const da_desc *desc, int32_t max_copies, const int32_t *copies, const int32_t *num_copies,
+                           void *k_pool, void *v_pool, float *k_scale, float *v_scale, float *weights,
+                           int32_t *device_error, cudaStream_t stream);
 
 /* Types of the probabilities of decode_attn_verify_drafts. */
 typedef enum {

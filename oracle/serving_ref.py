@@ -133,3 +133,94 @@ def attend_ref(q, k, v, s_q, sigma, window=0, sinks=None):
                 elif sinks is not None:
                     lse[j, h, g] = sinks[h, g]
     return out, lse, big, pv, sv
+
+
+# ------------------------------------------------------------------ pages
+def fork_ref(parents, lens, table, held, refs, new_table, P):
+    """-> new table, held, lens, refs, error bits (1 bad page, 4 negative length, 128 bad parent)."""
+    B, cols = table.shape
+    refs, new_table, err = refs.copy(), new_table.copy(), 0
+    new_held, new_lens = np.zeros(B, np.int32), np.zeros(B, np.int32)
+    ok = lambda page: 0 <= page < len(refs)  # noqa: E731
+    for b in range(B):
+        for j in range(min(max(held[b], 0), cols)):
+            if ok(table[b, j]):
+                refs[table[b, j]] -= 1
+    for i, r in enumerate(parents):
+        if r >= B:
+            err |= 128
+        if not 0 <= r < B:
+            continue
+        err |= 4 if lens[r] < 0 else 0
+        L = max(lens[r], 0)
+        n = min(-(-L // P), min(max(held[r], 0), cols))
+        for j in range(n):
+            new_table[i, j] = table[r, j]
+            if ok(table[r, j]):
+                refs[table[r, j]] += 1
+        new_held[i], new_lens[i] = n, L
+    return new_table, new_held, new_lens, refs, err
+
+
+def reserve_ref(new_tokens, lens, table, held, refs, P):
+    """-> table, held, refs, copies, missing, error bits (2 too long, 4 negative length, 256 too few pages)."""
+    B, cols = table.shape
+    before = (table.copy(), held.copy(), refs.copy())
+    table, held, refs = table.copy(), held.copy(), refs.copy()
+    free = [p for p in range(len(refs)) if refs[p] == 0]
+    copies, err = np.full((B, 2), -1, np.int32), 0
+    asks, was = {}, refs.copy()
+    for b in range(B):
+        L, n = max(lens[b], 0), new_tokens[b]
+        err |= 4 if lens[b] < 0 else 0
+        if n <= 0:
+            continue
+        if L + n > cols * P:
+            err |= 2
+            continue
+        asks[b] = (L, -(-(L + n) // P))
+    writers = {}                                           # shared last pages with tokens on them
+    for b, (L, need) in asks.items():
+        if L % P and L // P < held[b] and was[table[b, L // P]] > 1:
+            writers.setdefault(int(table[b, L // P]), []).append(b)
+    copied = {}
+    for page, rows in writers.items():
+        movers = rows[1:] if len(rows) == was[page] else rows
+        for b in movers:
+            copied[b] = page
+            refs[page] -= 1
+    fresh = []                                             # (row, entry)
+    for b, (L, need) in asks.items():
+        first, start = -(-L // P), held[b]
+        if any(was[table[b, j]] > 1 for j in range(first, min(held[b], need))):
+            for j in range(first, held[b]):
+                refs[table[b, j]] -= 1
+            start = held[b] = first
+        if b in copied:
+            fresh.append((b, L // P))
+        fresh += [(b, j) for j in range(start, need)]
+        held[b] = max(held[b], need)
+    if len(fresh) > len(free):
+        return (*before, np.full((B, 2), -1, np.int32), len(fresh) - len(free), err | 256)
+    for (b, j), page in zip(fresh, free):
+        table[b, j] = page
+        refs[page] = 1
+    for b, page in copied.items():
+        copies[b] = page, table[b, asks[b][0] // P]
+    return table, held, refs, copies, 0, err
+
+
+def compact_ref(table, held, refs, into):
+    """-> new table, new refs, new_page, pairs, pages in use."""
+    live = [p for p in range(len(refs)) if refs[p] > 0]
+    N = len(live)
+    far, gap = [p for p in live if p >= N], [p for p in range(N) if refs[p] <= 0]
+    new_page = np.full(len(refs), -1, np.int32)
+    new_page[live] = live
+    new_page[far] = gap
+    new_refs = np.zeros_like(refs)
+    new_refs[new_page[live]] = refs[live]
+    into = into.copy()
+    for b in range(len(held)):
+        into[b, :held[b]] = new_page[table[b, :held[b]]]
+    return into, new_refs, new_page, list(zip(far, gap)), N

@@ -51,6 +51,7 @@ DA_DEV_META_MISMATCH = 16
 DA_DEV_BAD_TOKEN = 32
 DA_DEV_BAD_PROBS = 64
 DA_DEV_BAD_REQUEST = 128
+DA_DEV_NO_PAGES = 256
 
 LIB_PATH = _build_mod.LIB_PATH
 
@@ -122,12 +123,18 @@ def load_library(path: str = LIB_PATH):
     lib.decode_attn_accum_weights.argtypes = [DP, P, P, P, P, P, P, SZ, P, P, P, F32, P, P]
     lib.decode_attn_evict.argtypes = [DP, I32, I32, I32, P, P, P, P, P, P, P, P, P, P]
     lib.decode_attn_verify_drafts.argtypes = [I32, I32, I32, I32, P, I64, P, I64, P, P, P, P, P, P, P, P]
+    lib.decode_attn_fork_pages.argtypes = [DP, P, P, P, P, P, P, P, P, P, P]
+    lib.decode_attn_free_pages.argtypes = [DP, P, P, P, P, P, P, P]
+    lib.decode_attn_reserve_pages.argtypes = [DP, P, P, P, P, P, P, P, P, P]
+    lib.decode_attn_compact_pages.argtypes = [DP, P, P, P, P, P, P, P, P, P, P]
+    lib.decode_attn_copy_pages.argtypes = [DP, I32, P, P, P, P, P, P, P, P, P]
     lib.decode_attn_strerror.argtypes = [ctypes.c_int]
     lib.decode_attn_strerror.restype = ctypes.c_char_p
     for f in ("decode_attn_sched_meta_bytes", "decode_attn_meta_offsets", "decode_attn_num_parts",
               "decode_attn_sched_meta", "decode_attn_fwd", "decode_attn_fwd_ex", "decode_attn_get_error",
               "decode_attn_append_kv", "decode_attn_append_block", "decode_attn_rope_append", "decode_attn_accum_weights", "decode_attn_evict",
-              "decode_attn_verify_drafts"):
+              "decode_attn_verify_drafts", "decode_attn_fork_pages", "decode_attn_free_pages", "decode_attn_reserve_pages",
+              "decode_attn_compact_pages", "decode_attn_copy_pages"):
         getattr(lib, f).restype = ctypes.c_int
     _libs[path] = lib
     return lib
@@ -362,6 +369,85 @@ def evict(desc: Desc, budget, cache_seqlens, block_table, dst_block_table, k_poo
         _opt(dev, "device_error", device_error, i32), _stream(stream, dev)))
 
 
+def fork_pages(desc: Desc, parents, cache_seqlens, block_table, held, refs, new_block_table, new_held, new_seqlens,
+               device_error=None, stream=None, lib=None):
+    """New row i continues old row ``parents[i]`` (int32 [B]; -1: empty) and
+    shares its pages; every old row lets go of what it holds (``held`` int32 [B],
+    ``refs`` int32 [num_pages]). See decode_attn_fork_pages in the header."""
+    import torch
+    i32, dev, B = torch.int32, _device(), desc.B
+    table = (B, desc.max_pages_per_seq)
+    _check((lib or load_library()).decode_attn_fork_pages(
+        ctypes.byref(desc), _need(dev, "parents", parents, i32, (B,)), _need(dev, "cache_seqlens", cache_seqlens, i32, (B,)),
+        _need(dev, "block_table", block_table, i32, table), _need(dev, "held", held, i32, (B,)),
+        _need(dev, "refs", refs, i32, (desc.num_pages,)), _need(dev, "new_block_table", new_block_table, i32, table),
+        _need(dev, "new_held", new_held, i32, (B,)), _need(dev, "new_seqlens", new_seqlens, i32, (B,)),
+        _opt(dev, "device_error", device_error, i32), _stream(stream, dev)))
+
+
+def free_pages(desc: Desc, done, cache_seqlens, block_table, held, refs, device_error=None, stream=None, lib=None):
+    """Rows with ``done[b]`` != 0 (int32 [B]) let go of their pages, in place; see
+    decode_attn_free_pages in the header."""
+    import torch
+    i32, dev, B = torch.int32, _device(), desc.B
+    _check((lib or load_library()).decode_attn_free_pages(
+        ctypes.byref(desc), _need(dev, "done", done, i32, (B,)), _need(dev, "cache_seqlens", cache_seqlens, i32, (B,)),
+        _need(dev, "block_table", block_table, i32, (B, desc.max_pages_per_seq)), _need(dev, "held", held, i32, (B,)),
+        _need(dev, "refs", refs, i32, (desc.num_pages,)), _opt(dev, "device_error", device_error, i32), _stream(stream, dev)))
+
+
+def reserve_pages(desc: Desc, cache_seqlens, block_table, held, refs, copies, missing, new_tokens=None, device_error=None,
+                  stream=None, lib=None):
+    """Room for ``new_tokens[b]`` more tokens of each request (int32 [B]; None:
+    ``desc.s_q`` each) on pages that no one else holds; ``copies`` int32 [B, 2] gets the
+    pages to copy before anything is appended, ``missing`` int32 [1] the pages that
+    the pool lacks (then nothing is changed). See decode_attn_reserve_pages in the
+    header."""
+    import torch
+    i32, dev, B = torch.int32, _device(), desc.B
+    _check((lib or load_library()).decode_attn_reserve_pages(
+        ctypes.byref(desc), _opt(dev, "new_tokens", new_tokens, i32, (B,)), _need(dev, "cache_seqlens", cache_seqlens, i32, (B,)),
+        _need(dev, "block_table", block_table, i32, (B, desc.max_pages_per_seq)), _need(dev, "held", held, i32, (B,)),
+        _need(dev, "refs", refs, i32, (desc.num_pages,)), _need(dev, "copies", copies, i32, (B, 2)),
+        _need(dev, "missing", missing, i32, (1,)), _opt(dev, "device_error", device_error, i32), _stream(stream, dev)))
+
+
+def compact_pages(desc: Desc, block_table, held, refs, new_block_table, new_refs, new_page, copies, counts, device_error=None,
+                  stream=None, lib=None):
+    """Plan the move of all pages in use to the front of the pool: ``new_page`` and
+    ``new_refs`` int32 [num_pages], ``copies`` int32 [num_pages // 2, 2], ``counts``
+    int32 [2] (pages in use, pairs to copy: ``copy_pages(..., num_copies=counts[1:])``).
+    See decode_attn_compact_pages in the header."""
+    import torch
+    i32, dev, n = torch.int32, _device(), desc.num_pages
+    table = (desc.B, desc.max_pages_per_seq)
+    _check((lib or load_library()).decode_attn_compact_pages(
+        ctypes.byref(desc), _need(dev, "block_table", block_table, i32, table), _need(dev, "held", held, i32, (desc.B,)),
+        _need(dev, "refs", refs, i32, (n,)), _need(dev, "new_block_table", new_block_table, i32, table),
+        _need(dev, "new_refs", new_refs, i32, (n,)), _need(dev, "new_page", new_page, i32, (n,)),
+        _need(dev, "copies", copies, i32, (n // 2, 2)), _need(dev, "counts", counts, i32, (2,)),
+        _opt(dev, "device_error", device_error, i32), _stream(stream, dev)))
+
+
+def copy_pages(desc: Desc, copies, k_pool, v_pool, k_scale=None, v_scale=None, weights=None, num_copies=None, device_error=None,
+               stream=None, lib=None):
+    """Copy whole pages of a cache: ``copies`` int32 [n, 2] (source, destination;
+    a negative source: none), of which only the first ``num_copies`` (int32 [1]) if
+    given. ``weights``: those of accum_weights. See decode_attn_copy_pages in the
+    header."""
+    import torch
+    i32, f32, dev = torch.int32, torch.float32, _device()
+    scales = (desc.num_pages, desc.H_kv, desc.page_size // 16)
+    blocks = desc.kv_dtype in (KV_FP8_BLOCK, KV_INT8_BLOCK)
+    _check((lib or load_library()).decode_attn_copy_pages(
+        ctypes.byref(desc), copies.shape[0], _need(dev, "copies", copies, i32, (copies.shape[0], 2)),
+        _opt(dev, "num_copies", num_copies, i32, (1,)), _pool(dev, "k_pool", k_pool, desc),
+        None if v_pool is None else _pool(dev, "v_pool", v_pool, desc),
+        _opt(dev, "k_scale", k_scale, f32, scales) if blocks else None, _opt(dev, "v_scale", v_scale, f32, scales) if blocks else None,
+        _opt(dev, "weights", weights, f32, (desc.num_pages, desc.H_kv, desc.page_size)),
+        _opt(dev, "device_error", device_error, i32), _stream(stream, dev)))
+
+
 def _prob_rows(dev, name, t, dtype, shape):
     """Probabilities [B, rows, V], the rows evenly spaced; their address and the distance between rows."""
     B, rows, V = shape
@@ -408,6 +494,6 @@ def get_error(meta, stream=None) -> int:
 
 __all__ = ["Desc", "LaunchOpts", "DecodeAttnError", "load_library", "strerror", "sched_meta_bytes",
            "meta_offsets", "num_parts", "sched_meta", "fwd", "fwd_static_scratch", "append_kv", "append_block", "rope_append",
-           "accum_weights", "evict", "verify_drafts", "get_error", "Rope", "KV_BF16", "KV_FP8", "KV_MLA656",
+           "accum_weights", "evict", "fork_pages", "free_pages", "reserve_pages", "compact_pages", "copy_pages", "verify_drafts", "get_error", "Rope", "KV_BF16", "KV_FP8", "KV_MLA656",
            "KV_FP8_BLOCK", "KV_INT8_BLOCK", "PROB_F32",
            "PROB_BF16", "PROB_F16"]

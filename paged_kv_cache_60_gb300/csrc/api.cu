@@ -25,6 +25,11 @@ cudaError_t launch_accum(int D, bool fp8, const CUtensorMap &tk, const AccumPara
                          cudaStream_t stream, bool pdl);
 cudaError_t launch_accum_mla(AccumParams p, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_fork(const PagesParams &p, cudaStream_t stream, bool pdl);
+cudaError_t launch_free(const PagesParams &p, cudaStream_t stream, bool pdl);
+cudaError_t launch_reserve(PagesParams p, cudaStream_t stream, bool pdl);
+cudaError_t launch_compact(PagesParams p, cudaStream_t stream, bool pdl);
+cudaError_t launch_copy_pages(CopyPagesParams p, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_verify(int prob_dtype, const VerifyParams &p, int num_sms, cudaStream_t stream, bool pdl);
 int mla_ctas_per_part(int s_q);
 bool mla_kernel_available();
@@ -158,6 +163,29 @@ int check_pool_desc(const da_desc *d, int64_t *row_len) {
         default:
             return DA_ERR_UNSUPPORTED;
     }
+}
+
+// The sizes that the page operators read (those of the tables and counts)
+int check_pages(const da_desc *d) {
+    if (!d) return DA_ERR_NULL;
+    if (d->B < 1 || d->B > kMaxPageRows || d->page_size < 1 || d->max_pages_per_seq < 1 || d->num_pages < 1 ||
+        d->num_pages > kMaxPoolPages)
+        return DA_ERR_DIMS;
+    // lengths plus new tokens, and table entries, are counted in 32 bits
+    if ((int64_t)d->max_pages_per_seq * d->page_size > (int64_t)INT32_MAX - 64 ||
+        (int64_t)d->B * d->max_pages_per_seq > (int64_t)INT32_MAX)
+        return DA_ERR_DIMS;
+    return DA_OK;
+}
+PagesParams pages_params(const da_desc *d, int32_t *device_error) {
+    PagesParams p = {};
+    p.error = device_error;
+    p.B = d->B;
+    p.s_q = sq_of(d);
+    p.page_size = d->page_size;
+    p.max_pages = d->max_pages_per_seq;
+    p.num_pages = d->num_pages;
+    return p;
 }
 
 // A row stride in bf16 elements: 0 stands for packed rows
@@ -834,6 +862,147 @@ int decode_attn_evict(const da_desc *desc, int32_t budget, int32_t keep_first, i
     p.last = keep_last;
     if (launch_evict(p, sms, stream, true) != cudaSuccess) return DA_ERR_CUDA;
     return DA_OK;
+}
+
+int decode_attn_fork_pages(const da_desc *desc, const int32_t *parents, const int32_t *cache_seqlens,
+                           const int32_t *block_table, const int32_t *held, int32_t *refs, int32_t *new_block_table,
+                           int32_t *new_held, int32_t *new_seqlens, int32_t *device_error, cudaStream_t stream) {
+    int rc = check_pages(desc);
+    if (rc) return rc;
+    if (!parents || !cache_seqlens || !block_table || !held || !refs || !new_block_table || !new_held || !new_seqlens)
+        return DA_ERR_NULL;
+    if (!aligned4(parents) || !aligned4(cache_seqlens) || !aligned4(block_table) || !aligned4(held) || !aligned4(refs) ||
+        !aligned4(new_block_table) || !aligned4(new_held) || !aligned4(new_seqlens) || !aligned4(device_error))
+        return DA_ERR_ALIGN;
+    if (new_block_table == block_table || new_held == held || new_seqlens == cache_seqlens) return DA_ERR_UNSUPPORTED;
+    PagesParams p = pages_params(desc, device_error);
+    p.parents = parents;
+    p.seqlens_in = cache_seqlens;
+    p.table_in = block_table;
+    p.held_in = held;
+    p.refs = refs;
+    p.table = new_block_table;
+    p.held = new_held;
+    p.seqlens = new_seqlens;
+    return launch_fork(p, stream, true) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+int decode_attn_free_pages(const da_desc *desc, const int32_t *done, int32_t *cache_seqlens,
+                           const int32_t *block_table, int32_t *held, int32_t *refs, int32_t *device_error,
+                           cudaStream_t stream) {
+    int rc = check_pages(desc);
+    if (rc) return rc;
+    if (!done || !cache_seqlens || !block_table || !held || !refs) return DA_ERR_NULL;
+    if (!aligned4(done) || !aligned4(cache_seqlens) || !aligned4(block_table) || !aligned4(held) || !aligned4(refs) ||
+        !aligned4(device_error))
+        return DA_ERR_ALIGN;
+    PagesParams p = pages_params(desc, device_error);
+    p.done = done;
+    p.seqlens = cache_seqlens;
+    p.table_in = block_table;
+    p.held = held;
+    p.refs = refs;
+    return launch_free(p, stream, true) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+int decode_attn_reserve_pages(const da_desc *desc, const int32_t *new_tokens, const int32_t *cache_seqlens,
+                              int32_t *block_table, int32_t *held, int32_t *refs, int32_t *copies, int32_t *missing,
+                              int32_t *device_error, cudaStream_t stream) {
+    int rc = check_pages(desc);
+    if (rc) return rc;
+    if (desc->s_q < 0 || desc->s_q > 64) return DA_ERR_DIMS;
+    if (!cache_seqlens || !block_table || !held || !refs || !copies || !missing) return DA_ERR_NULL;
+    if (!aligned4(new_tokens) || !aligned4(cache_seqlens) || !aligned4(block_table) || !aligned4(held) ||
+        !aligned4(refs) || (reinterpret_cast<uintptr_t>(copies) & 7u) || !aligned4(missing) || !aligned4(device_error))
+        return DA_ERR_ALIGN;
+    PagesParams p = pages_params(desc, device_error);
+    p.new_tokens = new_tokens;
+    p.seqlens_in = cache_seqlens;
+    p.table = block_table;
+    p.held = held;
+    p.refs = refs;
+    p.refs_in = refs;
+    p.copies = copies;
+    p.missing = missing;
+    return launch_reserve(p, stream, true) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+int decode_attn_compact_pages(const da_desc *desc, const int32_t *block_table, const int32_t *held, const int32_t *refs,
+                              int32_t *new_block_table, int32_t *new_refs, int32_t *new_page, int32_t *copies,
+                              int32_t *counts, int32_t *device_error, cudaStream_t stream) {
+    int rc = check_pages(desc);
+    if (rc) return rc;
+    if (!block_table || !held || !refs || !new_block_table || !new_refs || !new_page || !counts ||
+        (!copies && desc->num_pages > 1))  // (one page has nowhere to go)
+        return DA_ERR_NULL;
+    if (!aligned4(block_table) || !aligned4(held) || !aligned4(refs) || !aligned4(new_block_table) ||
+        !aligned4(new_refs) || !aligned4(new_page) || (reinterpret_cast<uintptr_t>(copies) & 7u) || !aligned4(counts) ||
+        !aligned4(device_error))
+        return DA_ERR_ALIGN;
+    if (new_block_table == block_table || new_refs == refs || new_page == refs || new_page == new_refs)
+        return DA_ERR_UNSUPPORTED;
+    PagesParams p = pages_params(desc, device_error);
+    p.table_in = block_table;
+    p.held_in = held;
+    p.refs_in = refs;
+    p.table = new_block_table;
+    p.refs = new_refs;
+    p.new_page = new_page;
+    p.copies = copies;
+    p.counts = counts;
+    return launch_compact(p, stream, true) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+int decode_attn_copy_pages(const da_desc *desc, int32_t max_copies, const int32_t *copies, const int32_t *num_copies,
+                           void *k_pool, void *v_pool, float *k_scale, float *v_scale, float *weights,
+                           int32_t *device_error, cudaStream_t stream) {
+    if (!desc) return DA_ERR_NULL;
+    if (desc->H_kv < 1 || desc->H_kv > 4096 || desc->page_size < 1 || desc->page_size > (1 << 20) ||
+        desc->num_pages < 1 || desc->D_qk < 1 || desc->D_qk > 4096 || max_copies < 0 || max_copies > (1 << 30))
+        return DA_ERR_DIMS;
+    const bool mla = is_mla(desc), blocks = has_blocks(desc);
+    int64_t row;
+    if (mla) {
+        if (desc->H_kv != 1 || desc->D_qk != 576 || desc->D_v != 512) return DA_ERR_UNSUPPORTED;
+        row = 656;
+    } else {
+        if (desc->kv_dtype != DA_KV_BF16 && desc->kv_dtype != DA_KV_FP8_PER_TENSOR && !blocks) return DA_ERR_UNSUPPORTED;
+        if (desc->D_qk != desc->D_v || (blocks && desc->page_size % kScaleBlock != 0)) return DA_ERR_UNSUPPORTED;
+        row = (int64_t)desc->D_qk * (desc->kv_dtype == DA_KV_BF16 ? 2 : 1);
+    }
+    const int64_t page_bytes = row * desc->H_kv * desc->page_size;
+    if (page_bytes % 16 != 0) return DA_ERR_UNSUPPORTED;
+    // values of a page's scales and weights are counted in 32 bits
+    if ((int64_t)desc->H_kv * desc->page_size > (int64_t)INT32_MAX) return DA_ERR_DIMS;
+    if (max_copies == 0) return DA_OK;
+    if (!copies || !k_pool) return DA_ERR_NULL;
+    if (mla) {
+        if (v_pool && v_pool != k_pool) return DA_ERR_UNSUPPORTED;
+    } else if (!v_pool) {
+        return DA_ERR_NULL;
+    }
+    if (blocks && (!k_scale || !v_scale)) return DA_ERR_SCALE;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned4(copies) || !aligned4(num_copies) || !aligned4(k_scale) ||
+        !aligned4(v_scale) || !aligned4(weights) || !aligned4(device_error))
+        return DA_ERR_ALIGN;
+    const int sms = current_sms();
+    if (!sms) return DA_ERR_CUDA;
+    CopyPagesParams p = {};
+    p.copies = copies;
+    p.num_copies = num_copies;
+    p.k_pool = static_cast<uint8_t *>(k_pool);
+    p.v_pool = mla ? nullptr : static_cast<uint8_t *>(v_pool);
+    p.k_scale = blocks ? k_scale : nullptr;
+    p.v_scale = blocks ? v_scale : nullptr;
+    p.weights = weights;
+    p.error = device_error;
+    p.k_units = page_bytes / 16;
+    p.v_units = mla ? 0 : page_bytes / 16;
+    p.max_copies = max_copies;
+    p.num_pages = desc->num_pages;
+    p.scale_len = desc->H_kv * (desc->page_size / kScaleBlock);
+    p.weight_len = desc->H_kv * desc->page_size;
+    return launch_copy_pages(p, sms, stream, true) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 int decode_attn_verify_drafts(int32_t B, int32_t n_draft, int32_t vocab, int32_t prob_dtype,

@@ -234,6 +234,39 @@ struct EvictParams {
     int32_t budget, first, last;
 };
 
+// The pages of a cache (pages.cu).
+constexpr int kMaxPageRows = 8192;         // requests of a page operator
+constexpr int kMaxPoolPages = 1 << 23;     // pages of one
+// shared memory of the planning kernels: a bit per page of an eighth of the pool, three words a request
+constexpr int kPlanSmemMax = kMaxPoolPages / 8 / 8 + 4 * (3 * kMaxPageRows + 1);
+struct PagesParams {
+    const int32_t *parents;        // [B] (fork)
+    const int32_t *done;           // [B] (free)
+    const int32_t *new_tokens;     // [B] or null: s_q each (reserve)
+    const int32_t *seqlens_in;     // [B]
+    const int32_t *table_in;       // [B][max_pages]
+    const int32_t *held_in;        // [B]
+    const int32_t *refs_in;        // [num_pages]
+    int32_t *seqlens, *table, *held, *refs;  // written; `refs` may be refs_in (reserve)
+    int32_t *new_page;             // [num_pages] (compact)
+    int32_t *copies;               // pairs (source page, destination page)
+    int32_t *counts;               // [2]: live pages, pairs (compact)
+    int32_t *missing;              // [1] (reserve)
+    int32_t *error;                // may be null
+    int32_t B, s_q, page_size, max_pages, num_pages;
+    int32_t ctas, share_words;     // of a planning kernel's cluster; words of 32 pages to a CTA
+};
+struct CopyPagesParams {
+    const int32_t *copies;         // [max_copies] pairs; a negative source: none
+    const int32_t *num_copies;     // [1] or null: max_copies
+    uint8_t *k_pool, *v_pool;      // v_pool null: one pool
+    float *k_scale, *v_scale;      // per page scale_len values, or null
+    float *weights;                // per page weight_len values, or null
+    int32_t *error;                // may be null
+    int64_t k_units, v_units;      // 16-byte units of a page
+    int32_t max_copies, num_pages, pieces, scale_len, weight_len;
+};
+
 // Verification of drafted tokens (verify.cu).
 struct VerifyParams {
     const void *target;            // [B][K + 1] rows of V probabilities

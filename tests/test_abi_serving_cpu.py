@@ -74,8 +74,69 @@ def test_append_block_refusals(lib, kv):
     assert lib.decode_attn_append_block(None, 4, *[G, 0] * 2, *[G] * 7, None, None) == -1
 
 
+def test_page_operator_refusals(lib):
+    d = _desc(kv_dtype=99, G=0, D_qk=0)              # the format does not matter to the tables
+    Q = [P(0x100000 * i) for i in range(1, 12)]
+
+    def args(names, kw):
+        return [kw.get(n, Q[i]) for i, n in enumerate(names)]
+
+    def fork(d, **kw):
+        return lib.decode_attn_fork_pages(ctypes.byref(d), *args(("par", "sl", "bt", "held", "refs", "nbt", "nheld", "nsl"), kw), kw.get("err"), None)
+
+    def free(d, **kw):
+        return lib.decode_attn_free_pages(ctypes.byref(d), *args(("done", "sl", "bt", "held", "refs"), kw), kw.get("err"), None)
+
+    def reserve(d, **kw):
+        return lib.decode_attn_reserve_pages(ctypes.byref(d), *args(("new", "sl", "bt", "held", "refs", "copies", "missing"), kw), kw.get("err"), None)
+
+    def compact(d, **kw):
+        return lib.decode_attn_compact_pages(ctypes.byref(d), *args(("bt", "held", "refs", "nbt", "nrefs", "page", "copies", "counts"), kw),
+                                             kw.get("err"), None)
+    calls = {fork: "par sl bt held refs nbt nheld nsl", free: "done sl bt held refs", reserve: "sl bt held refs copies missing",
+             compact: "bt held refs nbt nrefs page copies counts"}
+    for call, names in calls.items():
+        for name in names.split():
+            assert call(d, **{name: None}) == -1, (call, name)
+            assert call(d, **{name: P(0x900002)}) == -4, (call, name)
+        assert call(d, err=P(0x100001)) == -4
+        for bad in (dict(B=0), dict(B=8193), dict(page_size=0), dict(num_pages=0), dict(num_pages=(1 << 23) + 1), dict(max_pages_per_seq=0),
+                    dict(max_pages_per_seq=1 << 28), dict(B=8000, max_pages_per_seq=1 << 20, page_size=1)):
+            assert call(_desc(**bad)) == -2, (call, bad)
+    assert reserve(d, new=P(0x100002)) == -4 and reserve(_desc(s_q=65)) == -2
+    assert reserve(d, copies=P(0x600004)) == -4 and compact(d, copies=P(0x600004)) == -4      # pairs
+    assert fork(d, nbt=Q[2]) == -3 and fork(d, nheld=Q[3]) == -3 and fork(d, nsl=Q[1]) == -3
+    assert compact(d, nbt=Q[0]) == -3 and compact(d, nrefs=Q[2]) == -3 and compact(d, page=Q[2]) == -3
+    assert lib.decode_attn_free_pages(None, *Q[:5], None, None) == -1
+
+
+def test_copy_pages_refusals(lib):
+    def call(d, n=4, c=G, nc=None, kp=G, vp=G, ks=G, vs=G, w=None, err=None):
+        return lib.decode_attn_copy_pages(ctypes.byref(d), n, c, nc, kp, vp, ks, vs, w, err, None)
+    d = _desc()
+    for name in ("c", "kp", "vp"):
+        assert call(d, **{name: None}) == -1 and call(d, **{name: P(0x100002)}) == -4, name
+    for name in ("ks", "vs"):
+        assert call(d, **{name: None}) == -8 and call(d, **{name: P(0x100002)}) == -4, name
+    for name in ("nc", "w", "err"):
+        assert call(d, **{name: P(0x100002)}) == -4, name
+    assert call(d, n=0, c=None, kp=None) == 0 and call(d, n=-1) == -2 and call(d, n=(1 << 30) + 1) == -2
+    assert call(_desc(kv_dtype=9)) == -3 and call(_desc(page_size=8)) == -3 and call(_desc(D_v=64)) == -3
+    assert call(_desc(kv_dtype=da.KV_BF16, D_qk=2, D_v=2, H_kv=1, page_size=3)) == -3          # 12 bytes a page
+    assert call(_desc(kv_dtype=da.KV_BF16, H_kv=0)) == -2 and call(_desc(D_qk=5000, D_v=5000)) == -2
+    m = _desc(kv_dtype=da.KV_MLA656, H_kv=1, G=128, D_qk=576, D_v=512)
+    assert call(m, vp=P(0x200000)) == -3 and call(_desc(kv_dtype=da.KV_MLA656)) == -3
+
+
 def test_binding_refuses_host_tensors_and_shapes():
     z, i32 = torch.zeros, torch.int32
     d = _desc()
     with pytest.raises(da.DecodeAttnError):
         da.append_block(d, z(4, 256), z(4, 256), z(4, dtype=i32), z(4, 10, dtype=i32), z(1), z(1), z(40, 2, 1), z(40, 2, 1))
+    b, t, r = z(4, dtype=i32), z(4, 10, dtype=i32), z(40, dtype=i32)
+    for call in (lambda: da.fork_pages(d, b, b, t, b, r, t, b, b), lambda: da.free_pages(d, b, b, t, b, r),
+                 lambda: da.reserve_pages(d, b, t, b, r, z(4, 2, dtype=i32), z(1, dtype=i32)),
+                 lambda: da.compact_pages(d, t, b, r, t, r, r, z(20, 2, dtype=i32), z(2, dtype=i32)),
+                 lambda: da.copy_pages(d, z(4, 2, dtype=i32), z(1), z(1), z(40, 2, 1), z(40, 2, 1))):
+        with pytest.raises(da.DecodeAttnError):
+            call()
