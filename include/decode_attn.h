@@ -113,7 +113,7 @@ typedef struct {
 #define DA_DEV_TIMEOUT         8   /* a pipeline wait ran out of time: work unit abandoned */
 #define DA_DEV_META_MISMATCH  16   /* sched_meta was built for another desc */
 #define DA_DEV_BAD_TOKEN      32   /* a draft token >= vocab: taken as the end of its chain */
-#define DA_DEV_BAD_PROBS      64   /* a row without a positive probability: the next token is -1 */
+#define DA_DEV_BAD_PROBS      64   /* a row without a positive probability: the next token is -1 (verification), all 0 (token_probs) */
 #define DA_DEV_BAD_REQUEST   128   /* a request index outside [0, B): the token's K and V are skipped */
 #define DA_DEV_NO_PAGES      256   /* fewer free pages than a reservation needs: nothing was changed */
 
@@ -533,12 +533,61 @@ int decode_attn_copy_pages(const da_desc *desc, int32_t max_copies, const int32_
                            void *k_pool, void *v_pool, float *k_scale, float *v_scale, float *weights,
                            int32_t *device_error, cudaStream_t stream);
 
-/* Types of the probabilities of decode_attn_verify_drafts. */
+/* Types of the probabilities of decode_attn_verify_drafts, and of the logits and
+ * probabilities of decode_attn_token_probs. */
 typedef enum {
     DA_PROB_F32 = 0,
     DA_PROB_BF16 = 1,
     DA_PROB_F16 = 2
 } da_prob_dtype;
+
+/* What decode_attn_token_probs does to logits (host struct, passed by pointer, not
+ * retained; its pointers are device pointers, 4-byte aligned, and may each be NULL). */
+typedef struct {
+    const float *temperature;     /* [B]; NULL: 1. Not above 0: greedy */
+    const float *repetition;      /* [B], > 0; NULL: 1 */
+    const float *frequency;       /* [B]; NULL: 0 */
+    const float *presence;        /* [B]; NULL: 0 */
+    const int32_t *history;       /* [B][history_cols]: the request's tokens, prompt first */
+    const int32_t *history_lens;  /* [B]: tokens of each row (needed with history; cut to [0, history_cols]) */
+    const int32_t *prompt_lens;   /* [B]: how many of them are the prompt's; NULL: none */
+    const int32_t *draft_tokens;  /* [B][n_draft], those of decode_attn_verify_drafts */
+    const int32_t *bias_starts;   /* [B + 1]: request b's biases are entries [bias_starts[b], bias_starts[b + 1]) */
+    const int32_t *bias_tokens;   /* [n_bias] */
+    const float *bias_values;     /* [n_bias] */
+    const uint32_t *allowed;      /* row (b, j): ceil(V / 32) words, bit v mod 32 of word v / 32 set: token v is allowed */
+    int64_t allowed_stride;       /* words from row to row; 0: ceil(V / 32) */
+    int32_t history_cols, n_bias;
+} da_token_rules;
+
+/*
+ * Probabilities out of the target's logits: what decode_attn_verify_drafts takes. (No
+ * counterpart on the source pages.) Row (b, j) follows the first j drafts of request b. With
+ * c(v) = how often token v was generated (stands in the history behind the prompt, or
+ * among those j drafts, up to the first negative one):
+ *   x(v) = the logit; where v was generated or is in the prompt: x / repetition if x > 0, else
+ *     x * repetition; then - frequency * c(v), and - presence if c(v) > 0; then + its
+ *     biases, in the list's order (a token may stand there several times);
+ *   p(v) = e^(x(v) / temperature) / sum over the allowed tokens, 0 for the others, whatever
+ *     their logits are; with a temperature that is not above 0, 1 for the largest x (the
+ *     lowest token of equals; a NaN is not the largest) and 0 for the others.
+ * A row without an allowed token whose x is above -infinity is 0 throughout
+ * (DA_DEV_BAD_PROBS). A NaN or +infinity among the allowed x makes a row NaN throughout
+ * (not a greedy one).
+ *   B >= 1, n_draft in [0, 63], vocab V in [1, 2^19 - 7]. logits_dtype, prob_dtype:
+ *     da_prob_dtype, independent of each other.
+ *   logits: row j of request b at (b * (n_draft + 1) + j) * logits_stride elements; probs:
+ *     likewise with probs_stride (0: V, else >= V; rows aligned to their type only). probs may
+ *     be logits itself (same type and stride); else they must not overlap
+ *     (DA_ERR_UNSUPPORTED).
+ *   rules: NULL for none. Tokens outside [0, V) in any of its lists are ignored.
+ * x is fp32 in the order above, each step rounded; exponentials are the hardware's ex2 (2
+ * ulp), sums fp32 in a fixed order; p is rounded once to its type. Launches one kernel on
+ * `stream`. No allocation, no sync.
+ */
+int decode_attn_token_probs(int32_t B, int32_t n_draft, int32_t vocab, int32_t logits_dtype, const void *logits,
+                            int64_t logits_stride, int32_t prob_dtype, void *probs, int64_t probs_stride,
+                            const da_token_rules *rules, int32_t *device_error, cudaStream_t stream);
 
 /*
  * Verification of a chain of drafted tokens against the target's probabilities,

@@ -224,3 +224,50 @@ def compact_ref(table, held, refs, into):
     for b in range(len(held)):
         into[b, :held[b]] = new_page[table[b, :held[b]]]
     return into, new_refs, new_page, list(zip(far, gap)), N
+
+
+# ------------------------------------------------------------------ probabilities out of logits
+def adjusted(logits, dtype, text, prompt, drafts, j, rep, freq, pres, bias, V):
+    """x of row j in `dtype` (float32: each step rounded as the header says; float64: the formula). logits [V], text: the
+    request's tokens, prompt: how many of them are the prompt's, bias: list of (token, value) in order."""
+    f = dtype
+    x = logits.astype(f)
+    said, asked = np.zeros(V, np.int64), np.zeros(V, bool)
+    for i, t in enumerate(text):
+        if 0 <= t < V:
+            if i < prompt:
+                asked[t] = True
+            else:
+                said[t] += 1
+    for t in drafts[:j]:
+        if t < 0:
+            break
+        if t < V:
+            said[t] += 1
+    seen = asked | (said > 0)
+    with np.errstate(all="ignore"):
+        x = np.where(seen, np.where(x > 0, x / f(rep), x * f(rep)), x)
+        x = np.where(said > 0, x - f(freq) * said.astype(f) - f(pres), x)
+        for t, v in bias:
+            if 0 <= t < V:
+                x[t] = x[t] + f(v)
+    return x
+
+
+def probs_ref(x, allowed, T):
+    """p (float64) of adjusted logits (float64); allowed: bool [V]. With T > 0 also |x - max| (0 where nothing is)."""
+    V = len(x)
+    ok = allowed & ~(np.isneginf(x))
+    if not T > 0:
+        p = np.zeros(V)
+        cand = ok & ~np.isnan(x)
+        if cand.any():
+            p[int(np.argmax(np.where(cand, x, -np.inf)))] = 1
+        return p, np.zeros(V)
+    if not ok.any():
+        return np.zeros(V), np.zeros(V)
+    if np.isnan(x[ok]).any() or np.isposinf(x[ok]).any():
+        return np.full(V, np.nan), np.zeros(V)
+    d = np.where(ok, x - x[ok].max(), 0.0)
+    e = np.where(ok, np.exp(d / T), 0.0)
+    return e / e.sum(), np.abs(d)

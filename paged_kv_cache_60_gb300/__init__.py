@@ -90,6 +90,14 @@ class Rope(ctypes.Structure):
         return cls(rot_dim, len(sections), (ctypes.c_int32 * 4)(*sections), int(interleaved), int(adjacent))
 
 
+class TokenRules(ctypes.Structure):
+    """da_token_rules in the header; token_probs fills it."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("temperature", "repetition", "frequency", "presence", "history", "history_lens",
+                                                "prompt_lens", "draft_tokens", "bias_starts", "bias_tokens", "bias_values",
+                                                "allowed")] + [
+        ("allowed_stride", ctypes.c_int64), ("history_cols", ctypes.c_int32), ("n_bias", ctypes.c_int32)]
+
+
 class DecodeAttnError(RuntimeError):
     pass
 
@@ -128,13 +136,14 @@ def load_library(path: str = LIB_PATH):
     lib.decode_attn_reserve_pages.argtypes = [DP, P, P, P, P, P, P, P, P, P]
     lib.decode_attn_compact_pages.argtypes = [DP, P, P, P, P, P, P, P, P, P, P]
     lib.decode_attn_copy_pages.argtypes = [DP, I32, P, P, P, P, P, P, P, P, P]
+    lib.decode_attn_token_probs.argtypes = [I32, I32, I32, I32, P, I64, I32, P, I64, ctypes.POINTER(TokenRules), P, P]
     lib.decode_attn_strerror.argtypes = [ctypes.c_int]
     lib.decode_attn_strerror.restype = ctypes.c_char_p
     for f in ("decode_attn_sched_meta_bytes", "decode_attn_meta_offsets", "decode_attn_num_parts",
               "decode_attn_sched_meta", "decode_attn_fwd", "decode_attn_fwd_ex", "decode_attn_get_error",
               "decode_attn_append_kv", "decode_attn_append_block", "decode_attn_rope_append", "decode_attn_accum_weights", "decode_attn_evict",
               "decode_attn_verify_drafts", "decode_attn_fork_pages", "decode_attn_free_pages", "decode_attn_reserve_pages",
-              "decode_attn_compact_pages", "decode_attn_copy_pages"):
+              "decode_attn_compact_pages", "decode_attn_copy_pages", "decode_attn_token_probs"):
         getattr(lib, f).restype = ctypes.c_int
     _libs[path] = lib
     return lib
@@ -459,6 +468,49 @@ def _prob_rows(dev, name, t, dtype, shape):
     return t.data_ptr(), step
 
 
+def token_probs(logits, probs, temperature=None, repetition=None, frequency=None, presence=None, history=None, history_lens=None,
+                prompt_lens=None, draft_tokens=None, bias=None, allowed=None, device_error=None, stream=None, lib=None):
+    """The probabilities that verify_drafts takes, out of ``logits`` [B, K + 1, V]
+    (``probs``: the same shape, any of the three types; may be ``logits``). Per
+    request, fp32 [B]: ``temperature`` (0: greedy), ``repetition``, ``frequency``,
+    ``presence``, for the tokens of ``history`` int32 [B, n] (the first
+    ``history_lens`` of a row, of which ``prompt_lens`` are the prompt's) and, in row j,
+    the first j of ``draft_tokens`` int32 [B, K]. ``bias``: (starts int32 [B + 1], tokens
+    int32 [n], values fp32 [n]). ``allowed``: int32 [B, K + 1, ceil(V / 32)], bits of the
+    allowed tokens. See decode_attn_token_probs in the header."""
+    import torch
+    i32, f32, dev = torch.int32, torch.float32, _device()
+    if logits.dim() != 3 or logits.shape[1] < 1:
+        raise DecodeAttnError(f"logits: want [B, K + 1, V], got {tuple(logits.shape)}")
+    B, rows, V = logits.shape
+    kinds = {f32: PROB_F32, torch.bfloat16: PROB_BF16, torch.float16: PROB_F16}
+    lp, ls = _prob_rows(dev, "logits", logits, logits.dtype, (B, rows, V))
+    pp, ps = _prob_rows(dev, "probs", probs, probs.dtype, (B, rows, V))
+    rules = TokenRules()
+    for name, t in (("temperature", temperature), ("repetition", repetition), ("frequency", frequency), ("presence", presence)):
+        setattr(rules, name, _opt(dev, name, t, f32, (B,)))
+    if history is not None:
+        if history.dim() != 2 or history.shape[0] != B or history_lens is None:
+            raise DecodeAttnError(f"history: want [{B}, n] and history_lens, got {tuple(history.shape)}")
+        rules.history_cols = history.shape[1]
+        if history.shape[1]:
+            rules.history = _need(dev, "history", history, i32)
+        rules.history_lens = _need(dev, "history_lens", history_lens, i32, (B,))
+        rules.prompt_lens = _opt(dev, "prompt_lens", prompt_lens, i32, (B,))
+    if rows > 1:
+        rules.draft_tokens = _opt(dev, "draft_tokens", draft_tokens, i32, (B, rows - 1))
+    if bias is not None:
+        starts, tokens, values = bias
+        n = rules.n_bias = tokens.numel()
+        rules.bias_starts = _need(dev, "bias starts", starts, i32, (B + 1,))
+        rules.bias_tokens, rules.bias_values = _need(dev, "bias tokens", tokens, i32, (n,)), _need(dev, "bias values", values, f32, (n,))
+    if allowed is not None:
+        rules.allowed, rules.allowed_stride = _prob_rows(dev, "allowed", allowed, i32, (B, rows, -(-V // 32)))
+    _check((lib or load_library()).decode_attn_token_probs(
+        B, rows - 1, V, kinds.get(logits.dtype, -1), lp, ls, kinds.get(probs.dtype, -1), pp, ps, ctypes.byref(rules),
+        _opt(dev, "device_error", device_error, i32), _stream(stream, dev)))
+
+
 def verify_drafts(target_probs, draft_probs, draft_tokens, uniform, num_accepted, out_tokens, cache_seqlens=None,
                   new_seqlens=None, device_error=None, stream=None, lib=None):
     """Accept or refuse the drafts of every request and draw its next token:
@@ -494,6 +546,7 @@ def get_error(meta, stream=None) -> int:
 
 __all__ = ["Desc", "LaunchOpts", "DecodeAttnError", "load_library", "strerror", "sched_meta_bytes",
            "meta_offsets", "num_parts", "sched_meta", "fwd", "fwd_static_scratch", "append_kv", "append_block", "rope_append",
-           "accum_weights", "evict", "fork_pages", "free_pages", "reserve_pages", "compact_pages", "copy_pages", "verify_drafts", "get_error", "Rope", "KV_BF16", "KV_FP8", "KV_MLA656",
+           "accum_weights", "evict", "fork_pages", "free_pages", "reserve_pages", "compact_pages", "copy_pages", "token_probs",
+           "verify_drafts", "get_error", "Rope", "TokenRules", "KV_BF16", "KV_FP8", "KV_MLA656",
            "KV_FP8_BLOCK", "KV_INT8_BLOCK", "PROB_F32",
            "PROB_BF16", "PROB_F16"]

@@ -30,6 +30,7 @@ cudaError_t launch_free(const PagesParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_reserve(PagesParams p, cudaStream_t stream, bool pdl);
 cudaError_t launch_compact(PagesParams p, cudaStream_t stream, bool pdl);
 cudaError_t launch_copy_pages(CopyPagesParams p, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_probs(ProbsParams p, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_verify(int prob_dtype, const VerifyParams &p, int num_sms, cudaStream_t stream, bool pdl);
 int mla_ctas_per_part(int s_q);
 bool mla_kernel_available();
@@ -1003,6 +1004,71 @@ int decode_attn_copy_pages(const da_desc *desc, int32_t max_copies, const int32_
     p.scale_len = desc->H_kv * (desc->page_size / kScaleBlock);
     p.weight_len = desc->H_kv * desc->page_size;
     return launch_copy_pages(p, sms, stream, true) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+int decode_attn_token_probs(int32_t B, int32_t n_draft, int32_t vocab, int32_t logits_dtype, const void *logits,
+                            int64_t logits_stride, int32_t prob_dtype, void *probs, int64_t probs_stride,
+                            const da_token_rules *rules, int32_t *device_error, cudaStream_t stream) {
+    if (B < 1 || B > (1 << 20) || n_draft < 0 || n_draft > 63 || vocab < 1 || vocab > kMaxProbsVocab) return DA_ERR_DIMS;
+    if (logits_dtype < DA_PROB_F32 || logits_dtype > DA_PROB_F16 || prob_dtype < DA_PROB_F32 || prob_dtype > DA_PROB_F16)
+        return DA_ERR_UNSUPPORTED;
+    if (logits_stride == 0) logits_stride = vocab;
+    if (probs_stride == 0) probs_stride = vocab;
+    if (logits_stride < vocab || probs_stride < vocab || logits_stride > ((int64_t)1 << 34) ||
+        probs_stride > ((int64_t)1 << 34))
+        return DA_ERR_DIMS;
+    static const da_token_rules kNone = {};
+    const da_token_rules &r = rules ? *rules : kNone;
+    const int64_t words = (vocab + 31) / 32, allowed_stride = r.allowed_stride ? r.allowed_stride : words;
+    if (r.history && (r.history_cols < 1 || r.history_cols > (1 << 28))) return DA_ERR_DIMS;
+    if (r.bias_starts && r.n_bias < 0) return DA_ERR_DIMS;
+    if (r.allowed && (allowed_stride < words || allowed_stride > ((int64_t)1 << 34))) return DA_ERR_DIMS;
+    if (!logits || !probs) return DA_ERR_NULL;
+    if (r.history && !r.history_lens) return DA_ERR_NULL;
+    if (r.bias_starts && r.n_bias > 0 && (!r.bias_tokens || !r.bias_values)) return DA_ERR_NULL;
+    const uintptr_t ls = logits_dtype == DA_PROB_F32 ? 4 : 2, ps = prob_dtype == DA_PROB_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(logits) % ls || reinterpret_cast<uintptr_t>(probs) % ps || !aligned4(r.temperature) ||
+        !aligned4(r.repetition) || !aligned4(r.frequency) || !aligned4(r.presence) || !aligned4(r.history) ||
+        !aligned4(r.history_lens) || !aligned4(r.prompt_lens) || !aligned4(r.draft_tokens) || !aligned4(r.bias_starts) ||
+        !aligned4(r.bias_tokens) || !aligned4(r.bias_values) || !aligned4(r.allowed) || !aligned4(device_error))
+        return DA_ERR_ALIGN;
+    // rows are held by several CTAs: one would write what another still reads, unless the rows are the same
+    const int64_t rows = (int64_t)B * (n_draft + 1);
+    const bool in_place = logits == probs && logits_dtype == prob_dtype && logits_stride == probs_stride;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(logits), z = reinterpret_cast<uintptr_t>(probs);
+    const uint64_t a_len = ls * ((uint64_t)(rows - 1) * logits_stride + vocab),
+                   z_len = ps * ((uint64_t)(rows - 1) * probs_stride + vocab);
+    if (!in_place && a < z + z_len && z < a + a_len) return DA_ERR_UNSUPPORTED;
+    const int sms = current_sms();
+    if (!sms) return DA_ERR_CUDA;
+    ProbsParams p = {};
+    p.logits = logits;
+    p.probs = probs;
+    p.logits_stride = logits_stride;
+    p.probs_stride = probs_stride;
+    p.logits_dtype = logits_dtype;
+    p.prob_dtype = prob_dtype;
+    p.temperature = r.temperature;
+    p.repetition = r.repetition;
+    p.frequency = r.frequency;
+    p.presence = r.presence;
+    p.history = r.history;
+    p.history_lens = r.history_lens;
+    p.prompt_lens = r.prompt_lens;
+    p.drafts = n_draft > 0 ? r.draft_tokens : nullptr;
+    p.bias_starts = r.n_bias > 0 ? r.bias_starts : nullptr;
+    p.bias_tokens = r.bias_tokens;
+    p.bias_values = r.bias_values;
+    p.allowed = r.allowed;
+    p.allowed_stride = allowed_stride;
+    p.error = device_error;
+    p.history_cols = r.history ? r.history_cols : 0;
+    p.n_bias = r.n_bias;
+    p.B = B;
+    p.K = n_draft;
+    p.V = vocab;
+    if (launch_probs(p, sms, stream, true) != cudaSuccess) return DA_ERR_CUDA;
+    return DA_OK;
 }
 
 int decode_attn_verify_drafts(int32_t B, int32_t n_draft, int32_t vocab, int32_t prob_dtype,

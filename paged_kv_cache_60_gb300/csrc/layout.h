@@ -267,6 +267,28 @@ struct CopyPagesParams {
     int32_t max_copies, num_pages, pieces, scale_len, weight_len;
 };
 
+// Probabilities out of logits (probs.cu). Sixteen CTAs hold 2^19 values in groups of eight; a row's first group may start
+// seven values before it.
+constexpr int kMaxProbsVocab = (1 << 19) - 7;
+struct ProbsParams {
+    const void *logits;            // [B][K + 1] rows of V
+    void *probs;                   // likewise
+    int64_t logits_stride, probs_stride;  // elements between consecutive rows
+    const float *temperature, *repetition, *frequency, *presence;  // [B] or null
+    const int32_t *history;        // [B][history_cols] or null
+    const int32_t *history_lens, *prompt_lens;  // [B]; prompt_lens may be null
+    const int32_t *drafts;         // [B][K] or null
+    const int32_t *bias_starts;    // [B + 1] or null
+    const int32_t *bias_tokens;
+    const float *bias_values;
+    const uint32_t *allowed;       // [B][K + 1] rows of ceil(V / 32) words, or null
+    int64_t allowed_stride;        // words between consecutive rows
+    int32_t *error;                // may be null
+    int32_t logits_dtype, prob_dtype, history_cols, n_bias, B, K, V;
+    int32_t wide;                  // counts of 32 bits instead of 16
+    int32_t ctas, share;           // CTAs of a row; groups of eight values to a CTA
+};
+
 // Verification of drafted tokens (verify.cu).
 struct VerifyParams {
     const void *target;            // [B][K + 1] rows of V probabilities

@@ -128,6 +128,24 @@ def test_copy_pages_refusals(lib):
     assert call(m, vp=P(0x200000)) == -3 and call(_desc(kv_dtype=da.KV_MLA656)) == -3
 
 
+def test_token_probs_refusals(lib):
+    def call(B=2, K=3, V=100, lt=0, x=G, ls=0, pt=0, y=P(0x900000), ps=0, err=None, **rules):
+        r = da.TokenRules(**{k: (v.value if isinstance(v, P) else v) for k, v in rules.items()})
+        return lib.decode_attn_token_probs(B, K, V, lt, x, ls, pt, y, ps, ctypes.byref(r), err, None)
+    assert call(x=None) == -1 and call(y=None) == -1
+    assert call(x=P(0x100002)) == -4 and call(lt=1, x=P(0x100001)) == -4 and call(pt=2, y=P(0x900001)) == -4 and call(err=P(0x100002)) == -4
+    for bad in (dict(B=0), dict(B=(1 << 20) + 1), dict(K=-1), dict(K=64), dict(V=0), dict(V=(1 << 19) - 6), dict(ls=99), dict(ps=99), dict(ls=-1),
+                dict(history=G, history_lens=G, history_cols=0), dict(bias_starts=G, n_bias=-1), dict(allowed=G, allowed_stride=3)):
+        assert call(**bad) == -2, bad
+    for bad in (dict(lt=3), dict(pt=-1)):
+        assert call(**bad) == -3
+    assert call(history=G, history_cols=5) == -1 and call(bias_starts=G, n_bias=2, bias_tokens=G) == -1
+    for name in ("temperature", "repetition", "frequency", "presence", "history_lens", "prompt_lens", "draft_tokens", "bias_starts", "allowed"):
+        assert call(**{name: P(0x100002)}) == -4, name
+    # the probabilities are the logits' own rows, or apart from them
+    assert call(y=P(0x100000 + 400)) == -3 and call(y=G, pt=1) == -3 and call(y=G, ps=200) == -3 and call(y=P(0x100000 - 16)) == -3
+
+
 def test_binding_refuses_host_tensors_and_shapes():
     z, i32 = torch.zeros, torch.int32
     d = _desc()
@@ -140,3 +158,6 @@ def test_binding_refuses_host_tensors_and_shapes():
                  lambda: da.copy_pages(d, z(4, 2, dtype=i32), z(1), z(1), z(40, 2, 1), z(40, 2, 1))):
         with pytest.raises(da.DecodeAttnError):
             call()
+    for bad in (dict(logits=z(2, 10)), dict(history=z(2, 5, dtype=i32)), dict(history=z(3, 5, dtype=i32), history_lens=z(2, dtype=i32)), dict()):
+        with pytest.raises(da.DecodeAttnError):
+            da.token_probs(**{**dict(logits=z(2, 1, 10), probs=z(2, 1, 10)), **bad})
