@@ -121,14 +121,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t by
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// 4 bytes into shared memory asynchronously; then, once this thread's copies have
-// landed, one arrival on `bar` (one of those that it was initialised to expect).
-__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_mbar_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -273,6 +265,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same from zero: D = A * B.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // Transpose an 8x8 matrix of 16-bit elements held one row-pair per lane.
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     uint32_t y;
@@ -330,6 +330,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// (a, b) += s * (x, y), one packed instruction; each lane rounds as fmaf does.
+__device__ __forceinline__ void fma_f32x2(float &a, float &b, float s, float x, float y) {
+    asm("{\n.reg .b64 c, m, v;\nmov.b64 c, {%0, %1};\nmov.b64 m, {%2, %2};\nmov.b64 v, {%3, %4};\n"
+        "fma.rn.f32x2 c, m, v, c;\nmov.b64 {%0, %1}, c;\n}"
+        : "+f"(a), "+f"(b)
+        : "f"(s), "f"(x), "f"(y));
+}
 __device__ __forceinline__ float warp_max_xor_4_8_16(float v) {
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));

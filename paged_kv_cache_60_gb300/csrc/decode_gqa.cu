@@ -34,9 +34,11 @@
 //    a tile's scores take its K scale with the softmax's, and its P V product is made
 //    from zero and added to O times its V scale, in fp32. (The V scale folded into P
 //    would save that multiply-add and lose weights below 2^-14 of the largest scale in
-//    P's f16.) The scales of a chunk, four of K and four of V, come by 4-byte
-//    cp.async of eight producer lanes, whose arrivals the stage's full barrier counts. int8
-//    codes become f16 by a byte permute and one subtraction (0x6400 | c + 128 is
+//    P's f16.) The scales of a chunk, four of K and four of V, are held one a lane and
+//    handed out by shuffles; a warp loads those of its next chunk, and the page ids of
+//    the one after, while it works on this one. (Brought by the producer warp with
+//    4-byte cp.async, they made that warp's loop the limit: 636 us per call of 64 x
+//    32768 tokens.) int8 codes become f16 by a byte permute and one subtraction (0x6400 | c + 128 is
 //    1024 + 128 + c), exactly.
 //  * several query tokens per request (linear speculative-decoding
 //    verification, XQA page, section "投机解码:XQA 的第二个工作负载"): the
@@ -60,8 +62,7 @@
 namespace da {
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kScaleLanes = 2 * kChunk / kScaleBlock;  // scales of a chunk: K, V
-static_assert(kScaleBlock == 16, "a block is one tile of the products");
+static_assert(kScaleBlock == 16 && kChunk == 64, "a block is one of the four tiles of a chunk");
 
 template <int D, int KV, int NQ, int WPC>
 struct GqaCfg {
@@ -101,8 +102,7 @@ struct GqaCfg {
     static constexpr int OFF_L = OFF_M + NCW * G * 4;
     static constexpr int OFF_W = OFF_L + NCW * G * 4;
     static constexpr int OFF_FIN = OFF_W + NCW * G * 4;
-    static constexpr int OFF_SC = OFF_FIN + 4 * G * 4;  // per stage: K scales of its four tiles, V scales
-    static constexpr int OFF_BAR = (OFF_SC + (BLK ? NS * kScaleLanes * 4 : 0) + 7) / 8 * 8;
+    static constexpr int OFF_BAR = (OFF_FIN + 4 * G * 4 + 7) / 8 * 8;
     static constexpr int OFF_FLAG = OFF_BAR + 2 * NS * 8;
     static constexpr int SMEM = OFF_FLAG + 16 + 1024;  // + alignment slack
     static constexpr int MIN_BLOCKS = ((D == 64 && !FP8 && NQ == 1 && WPC == 1) || TWO_PER_SM) ? 2 : 1;
@@ -219,7 +219,6 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
     float *sm_l = reinterpret_cast<float *>(smem + C::OFF_L);
     float *sm_w = reinterpret_cast<float *>(smem + C::OFF_W);
     float *sm_fin = reinterpret_cast<float *>(smem + C::OFF_FIN);
-    float *sm_sc = reinterpret_cast<float *>(smem + C::OFF_SC);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *empty = full + C::NS;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&full[i], p.boxes_per_chunk + (BLK ? kScaleLanes : 0));  // one arrival per box and scale
+            mbar_init(&full[i], p.boxes_per_chunk);  // one arrival per producer lane
             mbar_init(&empty[i], WPC);  // every warp of the chunk's group
         }
         *abort_flag = 0;
@@ -272,9 +271,8 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
         // page ids of its next four chunks in registers, loaded four chunks
         // ahead, arrives on the chunk's full barrier with its own byte count
         // and issues its own copy -- no shuffles, no load latency in the loop.
-        // With scales per block, lane t < 8 also brings the K (t < 4) or V scale of tile t & 3.
         const int nb = p.boxes_per_chunk, bt = p.box_tokens, P = p.page_size;
-        if (lane >= (BLK ? kScaleLanes : nb)) return;
+        if (lane >= nb) return;
         const uint64_t pol = policy_evict_first();
         const uint32_t box_bytes = 2u * bt * C::NX * 128u;
         SegWalker wk = make_walker(p.meta, rec0, rec1, p.B, p.seqlens, max_len, p.s_q, WIN ? p.window : 0, 0);
@@ -294,29 +292,15 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
                 const int tok = (fc + lc) * kChunk + lane * bt;
                 return (lc < lc1 && tok < L && tok + bt > start) ? bt_row[tok / P] : -2;
             };
-            // the same of this lane's scale
-            const int st_tok = (lane & (kChunk / kScaleBlock - 1)) * kScaleBlock;
-            auto scale_id_of = [&](int lc) -> int {
-                const int tok = (fc + lc) * kChunk + st_tok;
-                return (lc < lc1 && tok < L && tok + kScaleBlock > start) ? bt_row[tok / P] : -2;
-            };
-            int ring[4], sring[4];
+            int ring[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                ring[k] = !BLK || lane < nb ? id_of(lc0 + k) : -2;
-                if constexpr (BLK) sring[k] = scale_id_of(lc0 + k);
-            }
+            for (int k = 0; k < 4; ++k) ring[k] = id_of(lc0 + k);
             for (int lc = lc0; lc < lc1 && !aborted; lc += 4) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (lc + k >= lc1) break;
                     int pg = ring[k];
-                    ring[k] = !BLK || lane < nb ? id_of(lc + k + 4) : -2;
-                    int spg = -2;
-                    if constexpr (BLK) {
-                        spg = sring[k];
-                        sring[k] = scale_id_of(lc + k + 4);
-                    }
+                    ring[k] = id_of(lc + k + 4);
                     const int stage = i % C::NS;
                     if (!mbar_wait_bounded(&empty[stage], ((i / C::NS) & 1) ^ 1, abort_flag, p.wait_limit_ns)) {
                         atomicOr(&p.meta.header[kHError], DA_DEV_TIMEOUT);
@@ -328,22 +312,6 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
                         atomicOr(&p.meta.header[kHError], DA_DEV_BAD_PAGE);
                         p.meta.header[kHErrorDetail] = pg;
                         pg = -2;  // skipped: its rows keep stale bytes
-                    }
-                    if constexpr (BLK) {
-                        float *sc = sm_sc + stage * kScaleLanes + lane;
-                        if (spg >= 0 && spg < p.num_pages) {
-                            const int in_page = ((fc + lc + k) * kChunk + st_tok) % P;
-                            cp_async4(sc, (lane < kScaleLanes / 2 ? p.k_scale : p.v_scale) +
-                                              ((size_t)spg * p.H_kv + h) * (P / kScaleBlock) + in_page / kScaleBlock);
-                            cp_async_mbar_arrive(&full[stage]);
-                        } else {  // no token here
-                            *sc = 0.f;
-                            mbar_arrive(&full[stage]);
-                        }
-                        if (lane >= nb) {
-                            ++i;
-                            continue;
-                        }
                     }
 #ifdef DA_PAGE_TRACE
                     if (p.page_trace && i < p.page_trace_cap) {
@@ -480,8 +448,35 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
             for (int mt = 0; mt < C::MT; ++mt) acc[mt][j][0] = acc[mt][j][1] = acc[mt][j][2] = acc[mt][j][3] = 0.f;
         }
 
+        // scales per block: lane l has tile (l & 3)'s of K (l & 4 == 0) or V
+        const int sc_tok = (lane & 3) * kScaleBlock;
+        const float *sc_pool = (lane & 4) ? p.v_scale : p.k_scale;
+        auto scale_page = [&](int lc) -> int {  // its page in local chunk lc; -1: no token there
+            const int tok = (fc + lc) * kChunk + sc_tok;
+            return lc < lc1 && tok < L && tok + kScaleBlock > start
+                       ? p.block_table[(size_t)sb * p.max_pages + tok / p.page_size] : -1;
+        };
+        auto scale_at = [&](int lc, int page) -> float {
+            if (page < 0 || page >= p.num_pages) return 0.f;
+            const int in_page = ((fc + lc) * kChunk + sc_tok) % p.page_size;
+            return sc_pool[((size_t)page * p.H_kv + h) * (p.page_size / kScaleBlock) + in_page / kScaleBlock];
+        };
+        [[maybe_unused]] float sc_next = 0.f;
+        [[maybe_unused]] int sc_page = -1;
+        if constexpr (BLK) {
+            const int lc = lc0 + (grp + C::NG - i % C::NG) % C::NG;  // this group's first chunk
+            sc_next = scale_at(lc, scale_page(lc));
+            sc_page = scale_page(lc + C::NG);
+        }
+
         for (int lc = lc0; lc < lc1; ++lc, ++i) {
             if ((i % C::NG) != grp) continue;  // one warp group per chunk, round robin
+            [[maybe_unused]] float sc = 0.f;
+            if constexpr (BLK) {
+                sc = (lane & 4) ? sc_next : sc_next * sl2;  // K's with the softmax scale
+                sc_next = scale_at(lc + C::NG, sc_page);
+                sc_page = scale_page(lc + 2 * C::NG);
+            }
             const int stage = i % C::NS;
 #ifdef DA_PAGE_TRACE
             // test build: a wait on a barrier that nothing completes runs out
@@ -521,13 +516,6 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
                 if (nskip > 0) zero_v(0, nskip);     // nskip <= nvalid: the ranges do not overlap
                 if (tail) zero_v(nvalid, kChunk);
                 __syncwarp();
-            }
-            [[maybe_unused]] float ksc[4], vsc[4];  // per tile: softmax scale times K scale; V scale
-            if constexpr (BLK) {
-                const float4 a = *reinterpret_cast<const float4 *>(sm_sc + stage * kScaleLanes);
-                const float4 b = *reinterpret_cast<const float4 *>(sm_sc + stage * kScaleLanes + 4);
-                ksc[0] = sl2 * a.x, ksc[1] = sl2 * a.y, ksc[2] = sl2 * a.z, ksc[3] = sl2 * a.w;
-                vsc[0] = b.x, vsc[1] = b.y, vsc[2] = b.z, vsc[3] = b.w;
             }
             // ---- S^T = K Q^T for four independent 16-token tiles
             float sacc[4][NQ][4];
@@ -594,11 +582,11 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
                 for (int t = 0; t < 4; ++t) {
                     const int ra = 16 * t + r8, rb = ra + 8;
                     const bool va = ra < nv && ra >= lv, vb = rb < nv && rb >= lv;
-                    const float sc = BLK ? ksc[t] : sl2;
-                    sv[t][0] = va ? sacc[t][j][0] * sc : -INFINITY;
-                    sv[t][1] = va ? sacc[t][j][1] * sc : -INFINITY;
-                    sv[t][2] = vb ? sacc[t][j][2] * sc : -INFINITY;
-                    sv[t][3] = vb ? sacc[t][j][3] * sc : -INFINITY;
+                    const float st = BLK ? __shfl_sync(0xffffffffu, sc, t) : sl2;
+                    sv[t][0] = va ? sacc[t][j][0] * st : -INFINITY;
+                    sv[t][1] = va ? sacc[t][j][1] * st : -INFINITY;
+                    sv[t][2] = vb ? sacc[t][j][2] * st : -INFINITY;
+                    sv[t][3] = vb ? sacc[t][j][3] * st : -INFINITY;
                     mx0 = fmaxf(mx0, fmaxf(sv[t][0], sv[t][2]));
                     mx1 = fmaxf(mx1, fmaxf(sv[t][1], sv[t][3]));
                 }
@@ -628,12 +616,15 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
                 l1[j] = l1[j] * al1 + ps1;
                 m0[j] = mn0;
                 m1[j] = mn1;
+                // (scales per block: most chunks leave the maxima as they are)
+                if (!BLK || __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
 #pragma unroll
-                for (int mt = 0; mt < C::MT; ++mt) {
-                    acc[mt][j][0] *= al0;
-                    acc[mt][j][1] *= al1;
-                    acc[mt][j][2] *= al0;
-                    acc[mt][j][3] *= al1;
+                    for (int mt = 0; mt < C::MT; ++mt) {
+                        acc[mt][j][0] *= al0;
+                        acc[mt][j][1] *= al1;
+                        acc[mt][j][2] *= al0;
+                        acc[mt][j][3] *= al1;
+                    }
                 }
             }
             // ---- O^T += V^T P^T
@@ -653,42 +644,63 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
                     }
                 }
             } else {
-#pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk) {
+                if constexpr (BLK) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const int chunk16 = kk * 2 + (lmat >> 1);
-                        const uint32_t addr = s_base + rv[t] + ((chunk16 ^ keyv[t]) << 4);
-                        uint32_t R[4];
-                        ldsm_x4_t(addr, R[0], R[1], R[2], R[3]);
+                        const float vs = __shfl_sync(0xffffffffu, sc, 4 + t);
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            // bytes of R: [v(t,d), v(t,d+1), v(t+1,d), v(t+1,d+1)] -> token pairs per d
-                            uint32_t a[4];
-                            if constexpr (I8) {
-                                a[0] = int8x2_to_f16x2<0, 2>(R[hf * 2]);
-                                a[1] = int8x2_to_f16x2<1, 3>(R[hf * 2]);
-                                a[2] = int8x2_to_f16x2<0, 2>(R[hf * 2 + 1]);
-                                a[3] = int8x2_to_f16x2<1, 3>(R[hf * 2 + 1]);
-                            } else {
+                        for (int kk = 0; kk < D / 32; ++kk) {
+                            const int chunk16 = kk * 2 + (lmat >> 1);
+                            const uint32_t addr = s_base + rv[t] + ((chunk16 ^ keyv[t]) << 4);
+                            uint32_t R[4];
+                            ldsm_x4_t(addr, R[0], R[1], R[2], R[3]);
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                uint32_t a[4];  // token pairs per d, as below
+                                if constexpr (I8) {
+                                    a[0] = int8x2_to_f16x2<0, 2>(R[hf * 2]);
+                                    a[1] = int8x2_to_f16x2<1, 3>(R[hf * 2]);
+                                    a[2] = int8x2_to_f16x2<0, 2>(R[hf * 2 + 1]);
+                                    a[3] = int8x2_to_f16x2<1, 3>(R[hf * 2 + 1]);
+                                } else {
+                                    const uint32_t u = prmt(R[hf * 2], 0u, 0x3120u);
+                                    const uint32_t w = prmt(R[hf * 2 + 1], 0u, 0x3120u);
+                                    a[0] = e4m3x2_to_f16x2((uint16_t)(u & 0xffff));
+                                    a[1] = e4m3x2_to_f16x2((uint16_t)(u >> 16));
+                                    a[2] = e4m3x2_to_f16x2((uint16_t)(w & 0xffff));
+                                    a[3] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+                                }
+#pragma unroll
+                                for (int j = 0; j < NQ; ++j) {
+                                    float pv[4];
+                                    mma_f16_zero(pv, a, pb[t][j][0], pb[t][j][1]);
+                                    fma_f32x2(acc[kk * 2 + hf][j][0], acc[kk * 2 + hf][j][1], vs, pv[0], pv[1]);
+                                    fma_f32x2(acc[kk * 2 + hf][j][2], acc[kk * 2 + hf][j][3], vs, pv[2], pv[3]);
+                                }
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < D / 32; ++kk) {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const int chunk16 = kk * 2 + (lmat >> 1);
+                            const uint32_t addr = s_base + rv[t] + ((chunk16 ^ keyv[t]) << 4);
+                            uint32_t R[4];
+                            ldsm_x4_t(addr, R[0], R[1], R[2], R[3]);
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                // bytes of R: [v(t,d), v(t,d+1), v(t+1,d), v(t+1,d+1)] -> token pairs per d
                                 const uint32_t u = prmt(R[hf * 2], 0u, 0x3120u);
                                 const uint32_t w = prmt(R[hf * 2 + 1], 0u, 0x3120u);
+                                uint32_t a[4];
                                 a[0] = e4m3x2_to_f16x2((uint16_t)(u & 0xffff));
                                 a[1] = e4m3x2_to_f16x2((uint16_t)(u >> 16));
                                 a[2] = e4m3x2_to_f16x2((uint16_t)(w & 0xffff));
                                 a[3] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
-                            }
 #pragma unroll
-                            for (int j = 0; j < NQ; ++j) {
-                                float(&o)[4] = acc[kk * 2 + hf][j];
-                                if constexpr (BLK) {
-                                    float pv[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma_f16(pv, a, pb[t][j][0], pb[t][j][1]);
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) o[e] = fmaf(vsc[t], pv[e], o[e]);
-                                } else {
-                                    mma_f16(o, a, pb[t][j][0], pb[t][j][1]);
-                                }
+                                for (int j = 0; j < NQ; ++j) mma_f16(acc[kk * 2 + hf][j], a, pb[t][j][0], pb[t][j][1]);
                             }
                         }
                     }
