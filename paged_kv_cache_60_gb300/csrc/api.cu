@@ -30,7 +30,7 @@ cudaError_t launch_free(const PagesParams &p, cudaStream_t stream, bool pdl);
 cudaError_t launch_reserve(PagesParams p, cudaStream_t stream, bool pdl);
 cudaError_t launch_compact(PagesParams p, cudaStream_t stream, bool pdl);
 cudaError_t launch_copy_pages(CopyPagesParams p, int num_sms, cudaStream_t stream, bool pdl);
-cudaError_t launch_probs(ProbsParams p, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_probs(const ProbsParams &p, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_verify(int prob_dtype, const VerifyParams &p, int num_sms, cudaStream_t stream, bool pdl);
 int mla_ctas_per_part(int s_q);
 bool mla_kernel_available();

@@ -285,7 +285,7 @@ struct ProbsParams {
     int64_t allowed_stride;        // words between consecutive rows
     int32_t *error;                // may be null
     int32_t logits_dtype, prob_dtype, history_cols, n_bias, B, K, V;
-    int32_t wide;                  // counts of 32 bits instead of 16
+    int32_t cap, short_list;       // listed tokens of a share; 16 bits each instead of 32
     int32_t ctas, share;           // CTAs of a row; groups of eight values to a CTA
 };
 

@@ -97,8 +97,8 @@ def _run(c, tin=F32, tout=F32, want_err=0, in_place=False, pad=0):
                 continue
             # x: the quotient or product, two differences and a product, one sum per bias, each 2^-24 of magnitudes up to `big` (its
             # own logit and x, what is taken off, all biases; an infinite one is exact); the exponent: x - max, its scale and their
-            # product, 4 * 2^-24 |x - max| / T; ex2 2 ulp (2^-22) of the value and of two factors; sums of 64 terms a thread, 5 steps
-            # in a warp, 8 + 5 over warps. All of it for the token, for the largest, and (averaged over p) for the total.
+            # product, 4 * 2^-24 |x - max| / T; ex2 2 ulp (2^-22) of the value and of two factors; sums of at most 32 groups of eight a
+            # thread (32 + 3 additions), 5 + 4 over its CTA, 4 over the cluster. All of it for the token, for the largest, and (averaged over p) for the total.
             said = max([1] + [text.count(t) for t in set(text)])
             mag = np.where(ok & np.isfinite(x64), np.maximum(np.abs(held[b, j].astype(np.float64)), np.abs(x64)), 0.0)
             big = 2 * mag + abs(args[5]) * (said + j) + args[6] + sum(abs(v) for _, v in bias if math.isfinite(v))
