@@ -11,11 +11,14 @@
 //
 // A row, or a contiguous share of it where a cluster of CTAs works on one, is walked
 // twice: once for the largest x and the sum of 2^(x - largest), once to write. Shares of
-// at most two groups of eight values a thread stay in registers in between; longer ones are read
-// again, out of L2: a share is at most 256 KB, so that what two CTAs on each SM have
-// begun stays within it. (Rows held in registers throughout, by clusters of eight, took
-// 308 us for 1024 rows of 131072 bf16 logits without a history: 128 warps with 32 values
-// a lane each, whose fixed work was more than the values'.)
+// at most two groups of eight values a thread stay in registers in between. Longer ones stream
+// through a ring of 16 KB pieces in shared memory (bulk copies, issued by one thread as the
+// slots come free); what the ring holds at the first walk's end is written first, the rest
+// comes again, out of L2 for the most part: two CTAs an SM with shares of at most 256 KB.
+// Measured on 1024 rows of 131072 bf16 logits to bf16: 129 us without a history (4.2
+// TB/s; instruction issue is the limit, 19 instructions a value for both walks), 204 with
+// histories of 8192 tokens. (Rows held in registers throughout, by clusters of eight:
+// 308 and 476 us; 128 warps a row, whose fixed work was more than the values'.)
 //
 // The tokens that the history, the drafts and the biases touch are few, and go their own
 // way: a bit per token of the share, a prefix sum over its words, and so a place for each
@@ -35,6 +38,7 @@
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "decode_attn.h"
@@ -46,9 +50,14 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kUnroll = 4;                      // groups of a thread in flight while a share is read
 constexpr int kShareBytes = 256 << 10;
-constexpr int kSmemMax = 224 << 10, kSmemTwo = 110 << 10;  // of a CTA; where two fit an SM
+// groups of a thread in a piece of a share that streams: 16 KB a piece
+template <typename T>
+constexpr int kPerThread = sizeof(T) == 2 ? 2 : 1;
+constexpr int kPieceBytes = 16 << 10;
+constexpr int kMaxSlots = 12;
+constexpr int kAhead = 8, kAbreast = 4;        // tokens of the history, listed tokens that a thread has under way
+constexpr int kSmemMax = 224 << 10, kSmemTwo = 112 << 10;  // of a CTA; where two fit an SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kPrompt = 0x80000000u, kBias = 0x40000000u, kCount = kBias - 1;
 
@@ -62,40 +71,97 @@ template <>
 __device__ __forceinline__ float2 pair_to_f32<__nv_bfloat16>(uint32_t w) {
     return make_float2(bf16_lo(w), bf16_hi(w));
 }
-// eight values: 16 bytes of a two-byte type, 32 of fp32
+// Eight values as they lie in memory: 16 bytes of a two-byte type, 32 of fp32.
 template <typename T>
 struct Raw {
-    uint4 v[sizeof(T) / 2];
-};
-template <typename T>
-__device__ __forceinline__ Raw<T> load_raw(const T *at) {
-    Raw<T> r;
+    static constexpr int kWords = 2 * (int)sizeof(T);
+    static constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : __is_same(T, __half) ? 0xFC00FC00u : 0xFF80FF80u;  // -infinity
+    uint32_t w[kWords];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = *reinterpret_cast<const uint4 *>(at + 4 * i);
-    return r;
-}
-template <typename T>
-__device__ __forceinline__ void widen(const Raw<T> &r, float (&x)[8]) {
-    if constexpr (sizeof(T) == 4) {
+        for (int i = 0; i < kWords; ++i) w[i] = kNone;
+    }
+    __device__ __forceinline__ void load(const T *at) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            x[4 * i] = __uint_as_float(r.v[i].x), x[4 * i + 1] = __uint_as_float(r.v[i].y);
-            x[4 * i + 2] = __uint_as_float(r.v[i].z), x[4 * i + 3] = __uint_as_float(r.v[i].w);
-        }
-    } else {
-        const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = pair_to_f32<T>(w[i]);
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        for (int i = 0; i < kWords; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(at + i * 4 / (int)sizeof(T));
+            w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
         }
     }
-}
-__device__ __forceinline__ void store8(float *at, const float (&x)[8]) {
+    // value by value, those of [0, V); t: the first one's token
+    __device__ __forceinline__ void load_some(const T *row, int t, int V) {
+        clear();
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        st_v4(at + 4 * i, make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]),
-                                     __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3])));
+        for (int i = 0; i < 8; ++i) {
+            if (t + i < 0 || t + i >= V) continue;
+            if constexpr (sizeof(T) == 4) {
+                w[i] = __float_as_uint(row[t + i]);
+            } else {
+                const uint32_t h = *reinterpret_cast<const uint16_t *>(row + t + i);
+                w[i / 2] = i & 1 ? (w[i / 2] & 0xFFFFu) | h << 16 : (w[i / 2] & 0xFFFF0000u) | h;
+            }
+        }
+    }
+    // -infinity where keep's bit is not set
+    __device__ __forceinline__ void drop(uint32_t keep) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            uint32_t m;
+            if constexpr (sizeof(T) == 4)
+                m = keep >> i & 1 ? 0xFFFFFFFFu : 0u;
+            else
+                m = ((keep >> 2 * i & 1u) | (keep >> 2 * i & 2u) << 15) * 0xFFFFu;
+            w[i] = (w[i] & m) | (kNone & ~m);
+        }
+    }
+    __device__ __forceinline__ void widen(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                x[i] = __uint_as_float(w[i]);
+            } else if (i % 2 == 0) {
+                const float2 f = pair_to_f32<T>(w[i / 2]);
+                x[i] = f.x, x[i + 1] = f.y;
+            }
+        }
+    }
+};
+// the larger of two pairs, or of two fp32; NaN where one is
+template <typename T>
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (sizeof(T) == 4)
+        return __float_as_uint(fmax_nan(__uint_as_float(a), __uint_as_float(b)));
+    else if constexpr (__is_same(T, __half))
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+template <typename T, int kN>
+__device__ __forceinline__ float largest_of(const Raw<T> (&r)[kN]) {
+    uint32_t m[kN];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+        m[k] = r[k].w[0];
+#pragma unroll
+        for (int i = 1; i < Raw<T>::kWords; ++i) m[k] = max_word<T>(m[k], r[k].w[i]);
+    }
+#pragma unroll
+    for (int k = 1; k < kN; ++k) m[0] = max_word<T>(m[0], m[k]);
+    if constexpr (sizeof(T) == 4) {
+        return __uint_as_float(m[0]);
+    } else {
+        const float2 f = pair_to_f32<T>(m[0]);
+        return fmax_nan(f.x, f.y);
+    }
+}
+// (32 bytes at once: as two stores of 16, each of which leaves half of every sector out, a row of
+// 131072 took 15.4 us to write instead of 6)
+__device__ __forceinline__ void store8(float *at, const float (&x)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
 }
 __device__ __forceinline__ void store8(__nv_bfloat16 *at, const float (&x)[8]) {
     st_v4(at, make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])));
@@ -107,39 +173,17 @@ __device__ __forceinline__ void store1(float *at, float x) { *at = x; }
 __device__ __forceinline__ void store1(__nv_bfloat16 *at, float x) { *at = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void store1(__half *at, float x) { *at = __float2half_rn(x); }
 
-// The row of probabilities; its type is told apart per store.
-struct OutRow {
-    void *at;
-    int dtype;
-    bool vec;  // aligned to eight values where the logits are
-    template <typename T>
-    __device__ __forceinline__ void group_as(int t, int V, const float (&x)[8]) const {
-        T *o = static_cast<T *>(at) + t;
-        if (vec && t >= 0 && t + 8 <= V) {
-            store8(o, x);
-        } else {
+// A row of probabilities: a group of eight, of which only tokens in [0, V) are there (vec: it is aligned like the logits' group)
+template <typename T>
+__device__ __forceinline__ void store_group(T *row, int t, int V, bool vec, const float (&x)[8]) {
+    if (vec && t >= 0 && t + 8 <= V) {
+        store8(row + t, x);
+    } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (t + i >= 0 && t + i < V) store1(o + i, x[i]);
-        }
+        for (int i = 0; i < 8; ++i)
+            if (t + i >= 0 && t + i < V) store1(row + t + i, x[i]);
     }
-    __device__ __forceinline__ void group(int t, int V, const float (&x)[8]) const {
-        if (dtype == DA_PROB_F32)
-            group_as<float>(t, V, x);
-        else if (dtype == DA_PROB_BF16)
-            group_as<__nv_bfloat16>(t, V, x);
-        else
-            group_as<__half>(t, V, x);
-    }
-    __device__ __forceinline__ void one(int t, float x) const {
-        if (dtype == DA_PROB_F32)
-            store1(static_cast<float *>(at) + t, x);
-        else if (dtype == DA_PROB_BF16)
-            store1(static_cast<__nv_bfloat16 *>(at) + t, x);
-        else
-            store1(static_cast<__half *>(at) + t, x);
-    }
-};
+}
 
 __device__ __forceinline__ float warp_max_nan(float v) {
 #pragma unroll
@@ -151,42 +195,46 @@ __device__ __forceinline__ float warp_add(float v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-// (a, b) <- 2^((a - m) s + c): the differences and products in one packed instruction each
-__device__ __forceinline__ void exp_pair(float &a, float &b, float m, float s, float c) {
-    asm("{\n.reg .b64 x, y;\nmov.b64 x, {%0, %1};\nmov.b64 y, {%2, %2};\nadd.rn.f32x2 x, x, y;\n"
-        "mov.b64 y, {%4, %4};\n.reg .b64 z;\nmov.b64 z, {%3, %3};\nfma.rn.f32x2 x, x, z, y;\nmov.b64 {%0, %1}, x;\n}"
-        : "+f"(a), "+f"(b)
-        : "f"(-m), "f"(s), "f"(c));
-    a = ex2(a);
-    b = ex2(b);
+// 2^((x - from) scale + off) of eight values. (Packed two to an instruction the differences and products cost more
+// moves than they save: 8 instead of 4 instructions a value.)
+struct Exps {
+    float from, scale, off;
+    __device__ __forceinline__ float operator()(float x) const { return ex2(fmaf(x - from, scale, off)); }
+    __device__ __forceinline__ void of(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (*this)(x[i]);
+    }
+};
+__device__ __forceinline__ float sum8(const float (&x)[8]) {
+    return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 }
 
 // A running maximum with the sum of 2^((x - m) s), or the largest x with its token.
 struct Run {
     float m = -INFINITY, sum = 0.f;
     int at = INT32_MAX;
-    // what differences are taken from: finite where nothing has been seen
-    __device__ __forceinline__ float base() const { return m == -INFINITY ? 0.f : m; }
-    __device__ __forceinline__ void raise(float to, float s) {
-        const float n = fmax_nan(m, to);
-        if (n != m) {  // (and where it is NaN)
-            sum = m == -INFINITY ? 0.f : sum * ex2((m - n) * s);
-            m = n;
-        }
+    // raises the maximum to `to` at least; what differences are taken from then (finite where nothing has been seen)
+    __device__ __forceinline__ float raise(float to, float s) {
+        const float n = fmax_nan(m, to), from = n == -INFINITY ? 0.f : n;
+        sum *= ex2((m - from) * s);  // 1 where it stays, 0 where nothing has been seen
+        m = n;
+        return from;
     }
     __device__ __forceinline__ void take(float x, int token) {
         if (x > m || (x == m && token < at && x > -INFINITY)) m = x, at = token;
     }
 };
 
-// kG: groups of eight values that a thread holds between the walks; 0: the share is read again
+// kG: groups of eight values that a thread holds between the walks; 0: the share streams
 template <typename TI, int kG>
-__global__ void __launch_bounds__(kThreads, kG == 0 ? 2 : 1) probs_kernel(const __grid_constant__ ProbsParams p) {
+__global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constant__ ProbsParams p) {
     extern __shared__ uint4 smem_v[];
     __shared__ float2 warp_pair[kWarps];
     __shared__ float2 cta_pair;          // largest, and sum (or the token, as bits)
     __shared__ int warp_sum[kWarps];
     __shared__ int s_listed;
+    __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
+    __shared__ int given_up;
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -197,21 +245,19 @@ __global__ void __launch_bounds__(kThreads, kG == 0 ? 2 : 1) probs_kernel(const 
     const int out_size = p.prob_dtype == DA_PROB_F32 ? 4 : 2;
     uint8_t *out_at = static_cast<uint8_t *>(p.probs) + row * p.probs_stride * out_size;
     const int head = (int)(reinterpret_cast<uintptr_t>(in) / sizeof(TI) & 7);
-    const OutRow out{out_at, p.prob_dtype, (int)(reinterpret_cast<uintptr_t>(out_at) / out_size & 7) == head};
+    const bool vec = (int)(reinterpret_cast<uintptr_t>(out_at) / out_size & 7) == head;
     const int t0 = rank * p.share * 8 - head;  // token of the share's first value; group g holds t0 + 8 g ..
     const int groups = max(min(p.share, (V - t0 + 7) / 8), 0);
     const uint32_t *bits = p.allowed ? p.allowed + row * p.allowed_stride : nullptr;
     const int words = (V + 31) / 32;
 
     // the logits of a group, -infinity where there is none
-    const auto load_group = [&](int g, float (&x)[8]) {
+    const auto load_group = [&](int g, Raw<TI> &r) {
         const int t = t0 + g * 8;
-        if (t >= 0 && t + 8 <= V) {
-            widen(load_raw(in + t), x);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = t + i >= 0 && t + i < V ? static_cast<float>(in[t + i]) : -INFINITY;
-        }
+        if (t >= 0 && t + 8 <= V)
+            r.load(in + t);
+        else
+            r.load_some(in, t, V);
     };
     // bit i: token i of the group is allowed
     const auto allowed_of = [&](int g) -> uint32_t {
@@ -219,19 +265,75 @@ __global__ void __launch_bounds__(kThreads, kG == 0 ? 2 : 1) probs_kernel(const 
         const uint32_t lo = w >= 0 ? bits[w] : 0u, hi = w + 1 < words ? bits[w + 1] : 0u;
         return __funnelshift_r(lo, hi, t & 31) & 0xFFu;
     };
-    const auto drop = [&](uint32_t keep, float (&x)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (!(keep >> i & 1)) x[i] = -INFINITY;
+    // whole groups of the share: [whole0, whole1)
+    const int whole0 = t0 < 0 ? 1 : 0, whole1 = V - t0 >= 8 ? min(groups, (V - t0) / 8) : 0;
+    // a share that streams: its whole groups in pieces, through a ring of slots. Load l (piece l on the first walk; on the second,
+    // piece l - pieces, those that the first has left in the ring are not loaded again) goes to slot l % slots. Thread 0
+    // issues load l + slots once all warps have released what load l's slot held, a piece behind its own reading.
+    constexpr int kPer = kPerThread<TI>, kPiece = kPer * kThreads;
+    static_assert(kPiece * 8 * (int)sizeof(TI) == kPieceBytes, "pieces of 16 KB");
+    const int slots = p.slots, pieces = whole1 > whole0 ? (whole1 - whole0 + kPiece - 1) / kPiece : 0;
+    const auto issue = [&](int l, int slot) {
+        const int g = whole0 + (l < pieces ? l : l - pieces) * kPiece;
+        const uint32_t bytes = (uint32_t)min(kPiece, whole1 - g) * 8u * (uint32_t)sizeof(TI);
+        mbar_arrive_expect_tx(&full[slot], bytes);
+        bulk_load(reinterpret_cast<uint8_t *>(smem_v) + (size_t)slot * kPieceBytes, in + t0 + g * 8, bytes, &full[slot]);
     };
-
-    float x[kG > 0 ? kG : 1][8];
+    if (kG == 0 && tid == 0) {
+        for (int k = 0; k < slots; ++k) {
+            mbar_init(&full[k], 1);
+            mbar_init(&empty[k], kWarps);
+        }
+        given_up = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+        for (int l = 0; l < min(slots, pieces); ++l) issue(l, l);
+    }
+    const auto wait = [&](uint64_t *bar, int phase) -> bool {
+        if (mbar_try_wait(bar, phase & 1)) return true;
+        const uint64_t begin = global_ns();
+        do {  // (asleep, rather than polling: the other warps need the issue slots)
+            if (mbar_try_wait_sleep(bar, phase & 1, 20000u)) return true;
+        } while (*(volatile int *)&given_up == 0 && global_ns() - begin < kWaitLimitNs);
+        *(volatile int *)&given_up = 1;
+        if (p.error) atomicOr(p.error, DA_DEV_TIMEOUT);
+        return false;
+    };
+    // the ring's next slot, and how often it has been round
+    struct Turn {
+        int slot = 0, round = 0;
+        __device__ __forceinline__ void next(int slots) {
+            if (++slot == slots) slot = 0, ++round;
+        }
+    };
+    Turn at_load;   // thread 0: of the next load that a release lets go, load slots + this
+    int load = slots;
+    const auto refill = [&] {
+        if (wait(&empty[at_load.slot], at_load.round)) issue(load, at_load.slot);
+        ++load;
+        at_load.next(slots);
+    };
+    const auto release = [&](int slot) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
+    };
+    // this thread's groups of a piece that starts with group g, in its slot
+    const auto read_slot = [&](int slot, int g, auto &r, auto all) {
+        const TI *at = reinterpret_cast<const TI *>(reinterpret_cast<const uint8_t *>(smem_v) + (size_t)slot * kPieceBytes) + tid * 8;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (all || g + i * kThreads + tid < whole1)
+                r[i].load(at + i * kThreads * 8);
+            else
+                r[i].clear();
+        }
+    };
+    Raw<TI> held[kG > 0 ? kG : 1];
     if constexpr (kG > 0) {
 #pragma unroll
         for (int k = 0; k < kG; ++k) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[k][i] = -INFINITY;
-            if (k * kThreads + tid < groups) load_group(k * kThreads + tid, x[k]);
+            held[k].clear();
+            if (k * kThreads + tid < groups) load_group(k * kThreads + tid, held[k]);
         }
     }
     const float T = p.temperature ? p.temperature[b] : 1.f;
@@ -245,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, kG == 0 ? 2 : 1) probs_kernel(const 
     const int bhi = p.bias_starts ? min(max(p.bias_starts[b + 1], 0), p.n_bias) : 0;
     const bool touched = n_hist > 0 || (p.drafts != nullptr && j > 0) || bhi > blo;  // the same for the whole CTA
     const int share_words = (p.share * 8 + 31) / 32;
-    uint32_t *mark = reinterpret_cast<uint32_t *>(smem_v);   // a bit per token of the share
+    uint32_t *mark = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(smem_v) +
+                                                  (kG == 0 ? (size_t)slots * kPieceBytes : 0));  // a bit per token of the share
     int *place = reinterpret_cast<int *>(mark + share_words);  // marks in the words before
     uint32_t *value = reinterpret_cast<uint32_t *>(place + share_words);  // of each listed token: count and marks, then x
     uint32_t *list = value + p.cap;                          // their tokens, from t0 on (16 bits each where that will do)
@@ -254,38 +357,40 @@ __global__ void __launch_bounds__(kThreads, kG == 0 ? 2 : 1) probs_kernel(const 
     };
     int listed = 0;
     if (touched) {
+        const int cap = min(p.cap, n_hist + j + bhi - blo);
         for (int i = tid; i < share_words; i += kThreads) mark[i] = 0u;
+        for (int i = tid; i < cap; i += kThreads) value[i] = 0u;
         __syncthreads();
         const int prompt = p.prompt_lens ? p.prompt_lens[b] : 0;
         const int32_t *hist = p.history + (int64_t)b * p.history_cols;
-        // f(place in the share, what it adds) for every touch
-        const auto each = [&](auto f) {
-            const auto touch = [&](int token, uint32_t what, bool atomic_add) {
-                const unsigned i = (unsigned)(token - t0);
-                if (token >= 0 && token < V && i < (unsigned)groups * 8u) f((int)i, what, atomic_add);
-            };
-            for (int i0 = tid; i0 < n_hist; i0 += 4 * kThreads) {
-                int tok[4];
+        const int lowest = max(t0, 0), span = min(V - t0, groups * 8) - (lowest - t0);
+        // f(token's place in the share) for every token of the history in [from, to)
+        const auto each = [&](int from, int to, auto f) {
+            for (int i0 = from + tid; i0 < to; i0 += kAhead * kThreads) {
+                int tok[kAhead];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tok[k] = i0 + k * kThreads < n_hist ? hist[i0 + k * kThreads] : -1;
+                for (int k = 0; k < kAhead; ++k) tok[k] = i0 + k * kThreads < to ? hist[i0 + k * kThreads] : -1;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const bool asked = i0 + k * kThreads < prompt;
-                    touch(tok[k], asked ? kPrompt : 1u, !asked);
-                }
+                for (int k = 0; k < kAhead; ++k)
+                    if ((unsigned)(tok[k] - lowest) < (unsigned)span) f(tok[k] - t0);
             }
-            if (p.drafts != nullptr && tid < j) {  // draft tid, unless the chain has ended before it
-                const int32_t *d = p.drafts + (int64_t)b * p.K;
-                bool there = true;
-                for (int i = 0; i <= tid; ++i) there = there && d[i] >= 0;
-                if (there) touch(d[tid], 1u, true);
-            }
-            for (int i = blo + tid; i < bhi; i += kThreads) touch(p.bias_tokens[i], kBias, false);
         };
-        each([&](int i, uint32_t, bool) {
-            const uint32_t bit = 1u << (i & 31);
-            if (!(*(volatile uint32_t *)(mark + i / 32) & bit)) atomicOr(mark + i / 32, bit);
-        });
+        // and for those of the drafts (draft tid, unless the chain has ended before it) and biases
+        const auto drafted = [&](auto f) {
+            if (p.drafts == nullptr || tid >= j) return;
+            const int32_t *d = p.drafts + (int64_t)b * p.K;
+            bool there = true;
+            for (int i = 0; i <= tid; ++i) there = there && d[i] >= 0;
+            if (there && (unsigned)(d[tid] - lowest) < (unsigned)span) f(d[tid] - t0);
+        };
+        const auto biased = [&](auto f) {
+            for (int i = blo + tid; i < bhi; i += kThreads)
+                if ((unsigned)(p.bias_tokens[i] - lowest) < (unsigned)span) f(p.bias_tokens[i] - t0);
+        };
+        const auto touch = [&](int i) { atomicOr(mark + i / 32, 1u << (i & 31)); };
+        each(0, n_hist, touch);
+        drafted(touch);
+        biased(touch);
         __syncthreads();
         // prefix sum over the words: a run of them per thread
         const int per = (share_words + kThreads - 1) / kThreads;
@@ -310,22 +415,22 @@ __global__ void __launch_bounds__(kThreads, kG == 0 ? 2 : 1) probs_kernel(const 
             }
         __syncthreads();
         listed = s_listed;
-        for (int i = tid; i < listed; i += kThreads) value[i] = 0u;
-        __syncthreads();
-        each([&](int i, uint32_t what, bool atomic_add) {
+        const auto enlist = [&](int i) -> uint32_t * {  // its place in the list
             const int at = place[i / 32] + __popc(mark[i / 32] & ((1u << (i & 31)) - 1));
-            if (atomic_add)
-                atomicAdd(value + at, what);
-            else
-                atomicOr(value + at, what);
             if (p.short_list)
                 reinterpret_cast<uint16_t *>(list)[at] = (uint16_t)i;
             else
                 list[at] = (uint32_t)i;
-        });
+            return value + at;
+        };
+        each(0, min(prompt, n_hist), [&](int i) { atomicOr(enlist(i), kPrompt); });
+        each(max(prompt, 0), n_hist, [&](int i) { atomicAdd(enlist(i), 1u); });
+        drafted([&](int i) { atomicAdd(enlist(i), 1u); });
+        biased([&](int i) { atomicOr(enlist(i), kBias); });
         __syncthreads();
     }
 
+    if (kG == 0) __syncthreads();  // the ring's barriers are initialised
     // ------------------------------------------------ the first walk: all tokens but those
     Run run;
     const auto keep_of = [&](int g) -> uint32_t {
@@ -333,77 +438,135 @@ __global__ void __launch_bounds__(kThreads, kG == 0 ? 2 : 1) probs_kernel(const 
         if (listed > 0) keep &= ~(uint32_t) reinterpret_cast<const uint8_t *>(mark)[g];
         return keep;
     };
-    const auto walk = [&](int g, const float (&v)[8]) {
+    // of a thread's whole groups in a piece, read before the piece is waited for
+    const auto keeps = [&](int g, bool marked, uint32_t (&keep)[kPer]) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) keep[i] = 0xFFu;
+        if (bits) {  // the byte with the group's first bit, and the one with its last
+            const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bits);
+            uint32_t lo[kPer], hi[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int t = t0 + (g + i * kThreads) * 8;
+                const bool there = g + i * kThreads < whole1;
+                lo[i] = there ? bytes[t >> 3] : 0u;
+                hi[i] = there ? bytes[(t + 7) >> 3] : 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) keep[i] = (lo[i] | hi[i] << 8) >> (t0 & 7) & 0xFFu;
+        }
+        if (marked && listed > 0) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (g + i * kThreads < whole1) keep[i] &= ~(uint32_t) reinterpret_cast<const uint8_t *>(mark)[g + i * kThreads];
+        }
+    };
+    // groups g, g + kThreads, ..
+    const auto walk = [&](int g, const auto &r) {
+        constexpr int kN = (int)(sizeof(r) / sizeof(r[0]));
         if (warm) {
-            float m = v[0];
+            const Exps exps{run.raise(largest_of(r), scale), scale, 0.f};
 #pragma unroll
-            for (int i = 1; i < 8; ++i) m = fmax_nan(m, v[i]);
-            run.raise(m, scale);
-            const float from = run.base();
-            float e[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = v[i];
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) exp_pair(e[i], e[i + 1], from, scale, 0.f);
-            run.sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+            for (int k = 0; k < kN; ++k) {
+                float e[8];
+                r[k].widen(e);
+                exps.of(e);
+                run.sum += sum8(e);
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) run.take(v[i], t0 + g * 8 + i);
+            for (int k = 0; k < kN; ++k) {
+                float v[8];
+                r[k].widen(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) run.take(v[i], t0 + (g + k * kThreads) * 8 + i);
+            }
+        }
+    };
+    const auto drop_untaken = [&](int g, auto &r) {
+        constexpr int kN = (int)(sizeof(r) / sizeof(r[0]));
+        if (!bits && listed == 0) return;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            if (g + k * kThreads >= groups) continue;
+            const uint32_t keep = keep_of(g + k * kThreads);
+            if (keep != 0xFFu) r[k].drop(keep);
         }
     };
     if constexpr (kG > 0) {
-#pragma unroll
-        for (int k = 0; k < kG; ++k) {
-            const int g = k * kThreads + tid;
-            if (g >= groups) continue;
-            const uint32_t keep = keep_of(g);
-            if (keep != 0xFFu) drop(keep, x[k]);
-            walk(g, x[k]);
-        }
+        drop_untaken(tid, held);
+        walk(tid, held);
     } else {
-        for (int g0 = tid; g0 < groups; g0 += kUnroll * kThreads) {
-            Raw<TI> r[kUnroll];
+        const auto edge = [&](int g) {
+            Raw<TI> r[1];
+            load_group(g, r[0]);
+            r[0].drop(keep_of(g));
+            walk(g, r);
+        };
+        if (tid == 0 && whole0 > 0 && groups > 0) edge(0);
+        if (tid == 32 && whole1 < groups && (whole1 > 0 || whole0 == 0)) edge(groups - 1);
+        Turn now;
+        for (int k = 0; k < pieces; ++k, now.next(slots)) {
+            const int g = whole0 + k * kPiece;
+            uint32_t keep[kPer];
+            if (bits || listed > 0) keeps(g + tid, true, keep);
+            if (tid == 0 && k > 0 && k - 1 + slots < pieces) refill();
+            wait(&full[now.slot], now.round);
+            Raw<TI> r[kPer];
+            const auto part = [&](auto all, auto untouched) {  // (all: whole pieces; untouched: no token is left out)
+                read_slot(now.slot, g, r, all);
+                if (k + slots < pieces) release(now.slot);
+                if (!untouched && (bits || listed > 0)) {
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                const int g = g0 + k * kThreads, t = t0 + g * 8;
-                if (g < groups && t >= 0 && t + 8 <= V) r[k] = load_raw(in + t);
-            }
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                const int g = g0 + k * kThreads, t = t0 + g * 8;
-                if (g >= groups) continue;
-                float v[8];
-                if (t >= 0 && t + 8 <= V)
-                    widen(r[k], v);
-                else
-                    load_group(g, v);
-                const uint32_t keep = keep_of(g);
-                if (keep != 0xFFu) drop(keep, v);
-                walk(g, v);
-            }
+                    for (int i = 0; i < kPer; ++i)
+                        if (keep[i] != 0xFFu) r[i].drop(keep[i]);
+                }
+                walk(g + tid, r);
+            };
+            if (g + kPiece <= whole1 && !bits && listed == 0)
+                part(std::true_type(), std::true_type());
+            else if (g + kPiece <= whole1)
+                part(std::true_type(), std::false_type());
+            else
+                part(std::false_type(), std::false_type());
         }
     }
     // the listed tokens
     if (listed > 0) {
         const float rep = p.repetition ? p.repetition[b] : 1.f, freq = p.frequency ? p.frequency[b] : 0.f;
         const float pres = p.presence ? p.presence[b] : 0.f;
-        for (int i = tid; i < listed; i += kThreads) {
-            const int t = token_at(i);
-            const uint32_t c = value[i], n = c & kCount;
-            float v = static_cast<float>(in[t]);
-            if (n > 0 || (c & kPrompt)) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
-            v = __fsub_rn(v, __fmul_rn(freq, (float)n));
-            if (n > 0) v = __fsub_rn(v, pres);
-            if (c & kBias)
-                for (int e = blo; e < bhi; ++e)
-                    if (p.bias_tokens[e] == t) v = __fadd_rn(v, p.bias_values[e]);
-            if (bits && !(bits[t >> 5] >> (t & 31) & 1)) v = -INFINITY;
-            value[i] = __float_as_uint(v);
+        for (int i0 = tid; i0 < listed; i0 += kAbreast * kThreads) {
+            int t[kAbreast];
+            float v[kAbreast];
+#pragma unroll
+            for (int k = 0; k < kAbreast; ++k) {
+                const int i = i0 + k * kThreads;
+                t[k] = i < listed ? token_at(i) : 0;
+                v[k] = i < listed ? static_cast<float>(in[t[k]]) : -INFINITY;
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kAbreast; ++k) {
+                const int i = i0 + k * kThreads;
+                if (i >= listed) continue;
+                const uint32_t c = value[i], n = c & kCount;
+                float y = v[k];
+                if (n > 0 || (c & kPrompt)) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+                y = __fsub_rn(y, __fmul_rn(freq, (float)n));
+                if (n > 0) y = __fsub_rn(y, pres);
+                if (c & kBias)
+                    for (int e = blo; e < bhi; ++e)
+                        if (p.bias_tokens[e] == t[k]) y = __fadd_rn(y, p.bias_values[e]);
+                v[k] = !bits || (bits[t[k] >> 5] >> (t[k] & 31) & 1) ? y : -INFINITY;
+                value[i] = __float_as_uint(v[k]);
+                if (!warm) run.take(v[k], t[k]);
+                top = fmax_nan(top, v[k]);
+            }
             if (warm) {
-                run.raise(v, scale);
-                run.sum += ex2((v - run.base()) * scale);
-            } else {
-                run.take(v, t);
+                const float from = run.raise(top, scale);
+#pragma unroll
+                for (int k = 0; k < kAbreast; ++k)
+                    if (i0 + k * kThreads < listed) run.sum += ex2((v[k] - from) * scale);
             }
         }
     }
@@ -446,66 +609,107 @@ __global__ void __launch_bounds__(kThreads, kG == 0 ? 2 : 1) probs_kernel(const 
 
     // ------------------------------------------------ the second walk: 2^((x - largest) s - log2(sum))
     // (without a token: everything 0, by an exponent of -infinity; a NaN or +infinity has left no sum: NaN everywhere)
-    const bool empty = best.x == -INFINITY;
-    const float from = empty ? 0.f : best.x, off = empty ? -INFINITY : -log2f(best.y);
-    const bool bad = warm && !empty && !(best.y < INFINITY);  // (largest NaN or infinite)
-    const auto probability = [&](int g, float (&v)[8]) {
-        if (warm) {
+    const bool nothing = best.x == -INFINITY;
+    const float from = nothing ? 0.f : best.x, off = nothing ? -INFINITY : -log2f(best.y);
+    const bool bad = warm && !nothing && !(best.y < INFINITY);  // (largest NaN or infinite)
+    const Exps exps{from, scale, off};
+    const bool ordinary = warm && !bits && !bad && !nothing && vec;
+    const auto second = [&](auto *row) {  // of the probabilities, as what they are
+        const auto probabilities = [&](int g, const Raw<TI> &r, float (&v)[8]) {
+            if (warm) {
+                r.widen(v);
+                exps.of(v);
+                if (bad || nothing) {
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) exp_pair(v[i], v[i + 1], from, scale, off);
-            if (bad || empty) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = bad ? NAN : 0.f;
-            }
-        } else {
-            const int t = t0 + g * 8, at = __float_as_int(best.y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = t + i == at ? 1.f : 0.f;
-        }
-        out.group(t0 + g * 8, V, v);
-    };
-    if constexpr (kG > 0) {
-#pragma unroll
-        for (int k = 0; k < kG; ++k)
-            if (k * kThreads + tid < groups) probability(k * kThreads + tid, x[k]);
-    } else {
-        for (int g0 = tid; g0 < groups; g0 += kUnroll * kThreads) {
-            Raw<TI> r[kUnroll];
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                const int g = g0 + k * kThreads, t = t0 + g * 8;
-                if (warm && g < groups && t >= 0 && t + 8 <= V) r[k] = load_raw(in + t);
-            }
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                const int g = g0 + k * kThreads, t = t0 + g * 8;
-                if (g >= groups) continue;
-                float v[8];
-                if (!warm) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                } else {
-                    if (t >= 0 && t + 8 <= V)
-                        widen(r[k], v);
-                    else
-                        load_group(g, v);
-                    if (bits) {
-                        const uint32_t keep = allowed_of(g);
-                        if (keep != 0xFFu) drop(keep, v);
-                    }
+                    for (int i = 0; i < 8; ++i) v[i] = bad ? NAN : 0.f;
                 }
-                probability(g, v);
+            } else {
+                const int t = t0 + g * 8, at = __float_as_int(best.y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = t + i == at ? 1.f : 0.f;
+            }
+        };
+        const auto write = [&](int g, const Raw<TI> &r) {
+            float v[8];
+            probabilities(g, r, v);
+            store_group(row, t0 + g * 8, V, vec, v);
+        };
+        if constexpr (kG > 0) {
+#pragma unroll
+            for (int k = 0; k < kG; ++k)
+                if (k * kThreads + tid < groups) write(k * kThreads + tid, held[k]);
+        } else {
+            const auto edge = [&](int g) {
+                Raw<TI> r;
+                load_group(g, r);
+                if (bits) r.drop(allowed_of(g));
+                write(g, r);
+            };
+            if (tid == 0 && whole0 > 0 && groups > 0) edge(0);
+            if (tid == 32 && whole1 < groups && (whole1 > 0 || whole0 == 0)) edge(groups - 1);
+            // first the pieces that the ring still has, the last ones; then the others, loaded again behind them
+            const int left = min(pieces, slots);
+            Turn now;
+            if (pieces > slots) now.slot = pieces % slots, now.round = pieces / slots;
+            for (int k = 0; k < pieces; ++k, now.next(slots)) {
+                const int g = whole0 + (k < left ? pieces - left + k : k - left) * kPiece;
+                auto *at = row + t0 + (int64_t)(g + tid) * 8;
+                uint32_t keep[kPer];
+                if (bits && warm) keeps(g + tid, false, keep);
+                const auto part = [&](auto all, auto plain) {  // (all: a whole piece; plain: nothing but the formula)
+                    Raw<TI> r[kPer];
+                    if (plain || warm) {
+                        if (tid == 0 && k > 0 && k - 1 < pieces - left) refill();
+                        if (k >= left) wait(&full[now.slot], now.round - 1);
+                        read_slot(now.slot, g, r, all);
+                        if (k < pieces - left) release(now.slot);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        const int gi = g + i * kThreads + tid;
+                        if (!all && gi >= whole1) continue;
+                        float v[8];
+                        if (plain) {
+                            r[i].widen(v);
+                            exps.of(v);
+                            store8(at + i * kThreads * 8, v);
+                            continue;
+                        }
+                        if (bits && warm && keep[i] != 0xFFu) r[i].drop(keep[i]);
+                        probabilities(gi, r[i], v);
+                        if (vec) {
+                            store8(at + i * kThreads * 8, v);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) store1(at + i * kThreads * 8 + e, v[e]);
+                        }
+                    }
+                };
+                if (g + kPiece <= whole1 && ordinary)
+                    part(std::true_type(), std::true_type());
+                else
+                    part(std::false_type(), std::false_type());
             }
         }
-    }
-    if (listed > 0 && warm) {
-        __syncthreads();  // over what the walk has left at the listed tokens
-        for (int i = tid; i < listed; i += kThreads) {
-            float v = __uint_as_float(value[i]), w = 0.f;
-            exp_pair(v, w, from, scale, off);
-            out.one(token_at(i), bad ? NAN : empty ? 0.f : v);
+        if (listed > 0 && warm) {
+            __syncthreads();  // over what the walk has left at the listed tokens
+            for (int i0 = tid; i0 < listed; i0 += kAbreast * kThreads) {
+#pragma unroll
+                for (int k = 0; k < kAbreast; ++k) {
+                    const int i = i0 + k * kThreads;
+                    if (i >= listed) continue;
+                    const float v = exps(__uint_as_float(value[i]));
+                    store1(row + token_at(i), bad ? NAN : nothing ? 0.f : v);
+                }
+            }
         }
-    }
+    };
+    if (p.prob_dtype == DA_PROB_F32)
+        second(reinterpret_cast<float *>(out_at));
+    else if (p.prob_dtype == DA_PROB_BF16)
+        second(reinterpret_cast<__nv_bfloat16 *>(out_at));
+    else
+        second(reinterpret_cast<__half *>(out_at));
     if (p.ctas > 1) cluster_wait_all();  // this CTA's pair stays until all have read it
 }
 
@@ -555,13 +759,26 @@ cudaError_t launch_types(ProbsParams p, int num_sms, cudaStream_t stream, bool p
         if (touches == 0) return 0;
         return 8 * ((size_t)p.share * 8 / 32 + 1) + (size_t)p.cap * (p.short_list ? 6 : 8);
     };
-    // as few CTAs as hold a row; where that leaves SMs idle, more, down to eight values a thread
+    // As few CTAs as hold a row, with two slots beside what the listed tokens need, twice on an SM; where that leaves SMs
+    // idle, more, down to eight values a thread: two or four as long as all have a place at once (64 rows of 128259: 18.0 us
+    // with four, 28.0 with one), eight or sixteen for half the SMs at most (32 rows: 12.9 us with four, 15.2 with eight, as
+    // clusters of eight do not fill the chip; one row: 9.1 with sixteen, 12.0 with four).
+    const int64_t piece = kPieceBytes;
     int c = 1;
-    while (c < kMaxCluster && ((int64_t)((groups + c - 1) / c) * 8 * (int)sizeof(TI) > kShareBytes || split(c) > kSmemTwo)) c *= 2;
-    while (c < kMaxCluster && rows * c * 2 <= num_sms && groups > c * kThreads) c *= 2;
-    const size_t smem = split(c);
-    if (smem > (size_t)kSmemMax) return cudaErrorInvalidConfiguration;
+    while (c < kMaxCluster && ((int64_t)((groups + c - 1) / c) * 8 * (int)sizeof(TI) > kShareBytes || (int64_t)split(c) + 2 * piece > kSmemTwo)) c *= 2;
+    while (c < kMaxCluster && rows * c * 2 <= (c < 4 ? 2 * num_sms : num_sms / 2) && groups > c * kThreads) c *= 2;
+    size_t smem = split(c);
     const int need = (p.share + kThreads - 1) / kThreads;
+    p.slots = 0;
+    if (need > 2) {
+        const int64_t all = ((int64_t)p.share * 8 * sizeof(TI) + piece - 1) / piece, given = (int64_t)smem + 2 * piece <= kSmemTwo ? kSmemTwo : kSmemMax;
+        const int64_t room = (given - (int64_t)smem) / piece;
+        p.slots = (int)(room < all ? room : all);
+        if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+        if (p.slots < 1) return cudaErrorInvalidConfiguration;
+        smem += (size_t)p.slots * piece;
+    }
+    if (smem > (size_t)kSmemMax) return cudaErrorInvalidConfiguration;
     return need <= 1   ? launch_one<TI, 1>(p, smem, stream, pdl)
            : need <= 2 ? launch_one<TI, 2>(p, smem, stream, pdl)
                        : launch_one<TI, 0>(p, smem, stream, pdl);
