@@ -286,7 +286,7 @@ struct ProbsParams {
     int32_t *error;                // may be null
     int32_t logits_dtype, prob_dtype, history_cols, n_bias, B, K, V;
     int32_t slots;                 // pieces of a streaming share that shared memory holds
-    int32_t cap, short_list;       // listed tokens of a share; 16 bits each instead of 32
+    int32_t cap;                   // listed tokens of a share at most
     int32_t ctas, share;           // CTAs of a row; groups of eight values to a CTA
 };
 

@@ -15,9 +15,9 @@
 // through a ring of 16 KB pieces in shared memory (bulk copies, issued by one thread as the
 // slots come free); what the ring holds at the first walk's end is written first, the rest
 // comes again, out of L2 for the most part: two CTAs an SM with shares of at most 256 KB.
-// Measured on 1024 rows of 131072 bf16 logits to bf16: 129 us without a history (4.2
-// TB/s; instruction issue is the limit, 19 instructions a value for both walks), 204 with
-// histories of 8192 tokens. (Rows held in registers throughout, by clusters of eight:
+// Measured on 1024 rows of 131072 bf16 logits to bf16: 126 us without a history (4.3
+// TB/s; instruction issue is the limit, 19 instructions a value for both walks), 190 with
+// histories of 1024 to 8192 tokens. (Rows held in registers throughout, by clusters of eight:
 // 308 and 476 us; 128 warps a row, whose fixed work was more than the values'.)
 //
 // The tokens that the history, the drafts and the biases touch are few, and go their own
@@ -50,7 +50,7 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kShareBytes = 256 << 10;
+constexpr int kShareBytes = 256 << 10;          // of a CTA at most: 2^17 values
 // groups of a thread in a piece of a share that streams: 16 KB a piece
 template <typename T>
 constexpr int kPerThread = sizeof(T) == 2 ? 2 : 1;
@@ -349,12 +349,12 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
     const int share_words = (p.share * 8 + 31) / 32;
     uint32_t *mark = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(smem_v) +
                                                   (kG == 0 ? (size_t)slots * kPieceBytes : 0));  // a bit per token of the share
-    int *place = reinterpret_cast<int *>(mark + share_words);  // marks in the words before
-    uint32_t *value = reinterpret_cast<uint32_t *>(place + share_words);  // of each listed token: count and marks, then x
-    uint32_t *list = value + p.cap;                          // their tokens, from t0 on (16 bits each where that will do)
-    const auto token_at = [&](int i) -> int {
-        return t0 + (int)(p.short_list ? reinterpret_cast<const uint16_t *>(list)[i] : list[i]);
-    };
+    // of each listed token: count and marks, then x
+    uint32_t *value = mark + share_words;
+    uint16_t *place = reinterpret_cast<uint16_t *>(value + p.cap);  // marks in the words before
+    uint16_t *list = place + share_words;  // the listed tokens, from t0 on, without 65536: they ascend, `upper` and up have it
+    int upper = INT32_MAX;
+    const auto token_at = [&](int i) -> int { return t0 + list[i] + (i >= upper ? 65536 : 0); };
     int listed = 0;
     if (touched) {
         const int cap = min(p.cap, n_hist + j + bhi - blo);
@@ -410,17 +410,15 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
         if (tid == kThreads - 1) s_listed = at + mine;
         for (int k = 0; k < per; ++k)
             if (tid * per + k < share_words) {
-                place[tid * per + k] = at;
+                place[tid * per + k] = (uint16_t)at;
                 at += __popc(mark[tid * per + k]);
             }
         __syncthreads();
         listed = s_listed;
+        if (share_words > 65536 / 32) upper = place[65536 / 32];
         const auto enlist = [&](int i) -> uint32_t * {  // its place in the list
             const int at = place[i / 32] + __popc(mark[i / 32] & ((1u << (i & 31)) - 1));
-            if (p.short_list)
-                reinterpret_cast<uint16_t *>(list)[at] = (uint16_t)i;
-            else
-                list[at] = (uint32_t)i;
+            list[at] = (uint16_t)i;
             return value + at;
         };
         each(0, min(prompt, n_hist), [&](int i) { atomicOr(enlist(i), kPrompt); });
@@ -754,10 +752,9 @@ cudaError_t launch_types(ProbsParams p, int num_sms, cudaStream_t stream, bool p
         p.ctas = c;
         p.share = (groups + c - 1) / c;
         const int64_t tokens = (int64_t)p.share * 8;
-        p.short_list = tokens <= 65536;
         p.cap = (int)((touches < tokens ? touches : tokens) + 3) / 4 * 4;
         if (touches == 0) return 0;
-        return 8 * ((size_t)p.share * 8 / 32 + 1) + (size_t)p.cap * (p.short_list ? 6 : 8);
+        return ((size_t)p.share * 8 / 32 + 1) * 6 + (size_t)p.cap * 6 + 16;
     };
     // As few CTAs as hold a row, with two slots beside what the listed tokens need, twice on an SM; where that leaves SMs
     // idle, more, down to eight values a thread: two or four as long as all have a place at once (64 rows of 128259: 18.0 us

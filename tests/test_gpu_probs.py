@@ -134,6 +134,33 @@ def test_many_rows():
     _run(_case(40, 3, 16384, 5, hist=100), BF16, BF16)
 
 
+@pytest.mark.parametrize("tin", [BF16, F32])
+def test_many_long_rows_with_long_histories(tin):
+    """Rows enough for one CTA each, whose shares stream and list tokens past 2^16; against float64 on the device."""
+    B, V, n = 170, 130999, 5000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = (torch.randn(B, 1, V, device="cuda", generator=g) * 2.5).to(tin)
+    hist = torch.randint(0, V, (B, n), device="cuda", generator=g, dtype=torch.int32)
+    lens = torch.randint(0, n + 1, (B,), device="cuda", generator=g, dtype=torch.int32)
+    prompt = lens // 2
+    rep, freq, pres, T = (torch.rand(B, device="cuda", generator=g) + 0.5 for _ in range(4))
+    out = torch.empty(B, 1, V, device="cuda")
+    da.token_probs(x, out, temperature=T, repetition=rep, frequency=freq, presence=pres, history=hist, history_lens=lens, prompt_lens=prompt)
+    i = torch.arange(n, device="cuda")
+    there, asked = i < lens[:, None], i < prompt[:, None]
+    z = torch.zeros(B, V, dtype=torch.float64, device="cuda")
+    said = z.scatter_add(1, hist.long(), (there & ~asked).double())
+    seen = z.scatter_add(1, hist.long(), there.double()) > 0
+    c = lambda v: v.double()[:, None]  # noqa: E731
+    y = x[:, 0].double()
+    y = torch.where(seen, torch.where(y > 0, y / c(rep), y * c(rep)), y) - c(freq) * said - torch.where(said > 0, c(pres), 0.0)
+    want = torch.softmax(y / c(T), -1)
+    # as in _run: 5 roundings of magnitudes up to 60 (counts are small) over T >= 0.5, for the token, the largest and the sum;
+    # the exponent's four; 102 more
+    rel = 2.0 ** -24 * (3 * 5 * 60 / 0.5 + 8 * 60 / 0.5 + 102)
+    assert ((out[:, 0].double() - want).abs() <= want * rel + 2.0 ** -126).all()
+
+
 def test_rows_that_start_anywhere_and_results_in_place():
     for pad in (0, 1, 3, 5):
         c = _case(3, 2, 777, 6 + pad, hist=30, mask=0.8)
