@@ -72,6 +72,36 @@ __device__ __forceinline__ uint2 codes8(const float (&q)[8]) {
     return make_uint2(c[0], c[1]);
 }
 
+// Eight codes of eight bf16 values whose scale is the power of two 1 / inv and large enough for all of them: nothing
+// saturates and nothing is NaN. int8: adding 1.5 * 2^23 rounds x inv to a whole number (to nearest even, in the same
+// instruction as the exact product), which is then the sum's lowest byte.
+template <bool I8>
+__device__ __forceinline__ uint2 codes8_fitting(uint4 x, float inv) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (I8) {
+            uint32_t r[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                r[2 * k] = __float_as_uint(fmaf(bf16_lo(w[2 * i + k]), inv, 12582912.f));
+                r[2 * k + 1] = __float_as_uint(fmaf(bf16_hi(w[2 * i + k]), inv, 12582912.f));
+            }
+            c[i] = prmt(prmt(r[0], r[1], 0x0040u), prmt(r[2], r[3], 0x0040u), 0x5410u);
+        } else {
+            uint16_t h[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+                    : "=h"(h[k])
+                    : "f"(bf16_hi(w[2 * i + k]) * inv), "f"(bf16_lo(w[2 * i + k]) * inv));
+            c[i] = (uint32_t)h[0] | (uint32_t)h[1] << 16;
+        }
+    }
+    return make_uint2(c[0], c[1]);
+}
+
 // the values of eight codes, without their scale
 template <bool I8>
 __device__ __forceinline__ void values8(uint2 c, float (&x)[8]) {
@@ -176,7 +206,8 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const __grid_con
     }
     m = max(m & 0xFFFFu, m >> 16);
     m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if (m >= 0x7F80u) {  // some value is not finite: those do not count
+    const bool finite = m < 0x7F80u;
+    if (!finite) {  // the values that are not finite do not count
         m = 0;
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
@@ -199,20 +230,27 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const __grid_con
     uint8_t *rows = (is_v ? p.v_pool : p.k_pool) +
                     (((int64_t)page * p.page_size + in_page) * H + h) * kRow + (lane & 15) * 8;
     const int64_t pitch = (int64_t)H * kRow;  // from one slot to the next
+    if (finite && power) {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        const int slot = 2 * i + (lane >> 4);
-        if (slot < s0 || slot >= s1) continue;
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float q[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            q[2 * k] = bf16_lo(w[k]);
-            q[2 * k + 1] = bf16_hi(w[k]);
+        for (int i = 0; i < kPasses; ++i) {
+            const int slot = 2 * i + (lane >> 4);
+            if (slot >= s0 && slot < s1) st_v2(rows + slot * pitch, codes8_fitting<I8>(x[i], inv));
         }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < kPasses; ++i) {
+            const int slot = 2 * i + (lane >> 4);
+            if (slot < s0 || slot >= s1) continue;
+            const uint4 y = ld_stream_v4(src + (row0 + slot - s0) * stride);
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+            float q[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = power ? q[k] * inv : __fdiv_rn(q[k], scale);
-        st_v2(rows + slot * pitch, codes8<I8>(q));
+            for (int k = 0; k < 4; ++k) {
+                q[2 * k] = __fdiv_rn(bf16_lo(w[k]), scale);
+                q[2 * k + 1] = __fdiv_rn(bf16_hi(w[k]), scale);
+            }
+            st_v2(rows + slot * pitch, codes8<I8>(q));
+        }
     }
     if (s0 == 0 || scale != had) {
         if (lane == 0) *scale_at = scale;
