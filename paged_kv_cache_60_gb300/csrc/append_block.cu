@@ -19,6 +19,10 @@
 // b's start at floor(starts[b] / 16) + 2 b, which leaves room for the blocks that n
 // tokens from any position touch (floor((n + 14) / 16) + 1 at most); a warp finds its
 // request by a search over that sum, 32 requests at a time.
+//
+// Bound by HBM: 32771 tokens of 8 heads in 34.3 us, 201 MB, 0.87 of the measured copy
+// rate (the saturating conversions for every value: 62.6 us, 63 % of the issue slots).
+// Four CTAs an SM, 64 registers a thread: 36.7 us with three, 43.3 with five, which spill.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -126,7 +130,7 @@ __device__ __forceinline__ void values8(uint2 c, float (&x)[8]) {
 }
 
 template <bool I8>
-__global__ void __launch_bounds__(kThreads) append_block_kernel(const __grid_constant__ AppendBlockParams p) {
+__global__ void __launch_bounds__(kThreads, 4) append_block_kernel(const __grid_constant__ AppendBlockParams p) {
     pdl_wait();               // rows, positions, table and scales may come from the kernel before
     pdl_launch_dependents();  // the next kernel waits for this grid before it reads the pool
     const int lane = threadIdx.x & 31;

@@ -86,6 +86,10 @@ struct GqaCfg {
     static constexpr int NCW = WPC == 4 ? 8
                                : WPC > 1 ? 6 : (NQ > 1 ? (D == 128 && !FP8 ? 6 : 7) : (FP8 ? 10 : (D == 64 ? 5 : 6)));
     static constexpr int NG = NCW / WPC;
+    // 16-token tiles of a chunk that a warp takes at once: all four, but two in the int8 builds where each warp has a chunk of
+    // its own, whose conversions are the longest: the loop's code then stays in the instruction cache (32 requests of
+    // 1024 to 8192 tokens, 8 heads, two query tokens: 107 -> 85 us; e4m3 76 -> 78, two warps a chunk 154 -> 156).
+    static constexpr int NT = KV == DA_KV_INT8_BLOCK && WPC == 1 ? 2 : 4;
     // The D = 64 build for three or four query tokens runs two CTAs per SM
     // (four stages each, at most 96 registers a thread): its MMA -> softmax ->
     // MMA chain is latency-bound, and a second CTA's chunks fill the gaps
@@ -517,190 +521,196 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
                 if (tail) zero_v(nvalid, kChunk);
                 __syncwarp();
             }
-            // ---- S^T = K Q^T for four independent 16-token tiles
-            float sacc[4][NQ][4];
+            constexpr int NT = C::NT;  // tiles of a pass
+#pragma unroll 1
+            for (int pass = 0; pass < 4 / NT; ++pass) {
+                // where the pass's tiles lie, from the first ones on
+                const uint32_t po = NT == 4 ? 0u : row_of(16 * NT * pass);
+                // ---- S^T = K Q^T for four independent 16-token tiles
+                float sacc[NT][NQ][4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int j = 0; j < NQ; ++j) sacc[t][j][0] = sacc[t][j][1] = sacc[t][j][2] = sacc[t][j][3] = 0.f;
-            if constexpr (!FP8) {
+                    for (int j = 0; j < NQ; ++j) sacc[t][j][0] = sacc[t][j][1] = sacc[t][j][2] = sacc[t][j][3] = 0.f;
+                if constexpr (!FP8) {
 #pragma unroll
-                for (int ks = 0; ks < C::KS; ++ks) {
+                    for (int ks = 0; ks < C::KS; ++ks) {
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int d = ks * 16 + (lmat >> 1) * 8;
-                        const int x = d >> 6;
-                        const uint32_t addr =
-                            s_base + rk[t] + x * xstride + ((((d & 63) >> 3) ^ (keyk[t] + (HM ? 0 : x))) << 4);
-                        uint32_t a[4];
-                        ldsm_x4(addr, a[0], a[1], a[2], a[3]);
-#pragma unroll
-                        for (int j = 0; j < NQ; ++j) mma_bf16(sacc[t][j], a, qf[ks][j][0], qf[ks][j][1]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int chunk16 = kk * 2 + (lmat >> 1);
-                        const uint32_t addr = s_base + rk[t] + ((chunk16 ^ keyk[t]) << 4);
-                        uint32_t R[4];
-                        ldsm_x4(addr, R[0], R[1], R[2], R[3]);
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const uint32_t ra = R[hf * 2], rb = R[hf * 2 + 1];
+                        for (int t = 0; t < NT; ++t) {
+                            const int d = ks * 16 + (lmat >> 1) * 8;
+                            const int x = d >> 6;
+                            const uint32_t addr =
+                                s_base + rk[t] + po + x * xstride + ((((d & 63) >> 3) ^ (keyk[t] + (HM ? 0 : x))) << 4);
                             uint32_t a[4];
-                            if constexpr (I8) {
-                                a[0] = int8x2_to_f16x2<0, 1>(ra);
-                                a[1] = int8x2_to_f16x2<0, 1>(rb);
-                                a[2] = int8x2_to_f16x2<2, 3>(ra);
-                                a[3] = int8x2_to_f16x2<2, 3>(rb);
-                            } else {
-                                a[0] = e4m3x2_to_f16x2((uint16_t)(ra & 0xffff));
-                                a[1] = e4m3x2_to_f16x2((uint16_t)(rb & 0xffff));
-                                a[2] = e4m3x2_to_f16x2((uint16_t)(ra >> 16));
-                                a[3] = e4m3x2_to_f16x2((uint16_t)(rb >> 16));
-                            }
+                            ldsm_x4(addr, a[0], a[1], a[2], a[3]);
 #pragma unroll
-                            for (int j = 0; j < NQ; ++j)
-                                mma_f16(sacc[t][j], a, qf[kk * 2 + hf][j][0], qf[kk * 2 + hf][j][1]);
-                        }
-                    }
-                }
-            }
-            // ---- online softmax over the chunk's 64 tokens (rows 16t + r8, 16t + r8 + 8)
-            uint32_t pb[4][NQ][2];
-#pragma unroll
-            for (int j = 0; j < NQ; ++j) {
-                const int nv = (NQ * WPC == 1) ? nvalid : L_first + jo + j - cbase;
-                // with a window, draft jo + j sees tokens from L_first + jo + j - window on
-                const int lv = (WIN && p.window > 0) ? L_first + jo + j - p.window - cbase : -1;
-                float sv[4][4];
-                float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int ra = 16 * t + r8, rb = ra + 8;
-                    const bool va = ra < nv && ra >= lv, vb = rb < nv && rb >= lv;
-                    const float st = BLK ? __shfl_sync(0xffffffffu, sc, t) : sl2;
-                    sv[t][0] = va ? sacc[t][j][0] * st : -INFINITY;
-                    sv[t][1] = va ? sacc[t][j][1] * st : -INFINITY;
-                    sv[t][2] = vb ? sacc[t][j][2] * st : -INFINITY;
-                    sv[t][3] = vb ? sacc[t][j][3] * st : -INFINITY;
-                    mx0 = fmaxf(mx0, fmaxf(sv[t][0], sv[t][2]));
-                    mx1 = fmaxf(mx1, fmaxf(sv[t][1], sv[t][3]));
-                }
-                const float mn0 = fmaxf(m0[j], warp_max_xor_4_8_16(mx0));
-                const float mn1 = fmaxf(m1[j], warp_max_xor_4_8_16(mx1));
-                // an earlier draft token may have seen no token yet: keep the
-                // exponent base finite so that 2^(-inf - base) = 0, not NaN
-                const float bs0 = (NQ * WPC > 1 && mn0 == -INFINITY) ? 0.f : mn0;
-                const float bs1 = (NQ * WPC > 1 && mn1 == -INFINITY) ? 0.f : mn1;
-                const float al0 = ex2(m0[j] - bs0), al1 = ex2(m1[j] - bs1);
-                float ps0 = 0.f, ps1 = 0.f;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const float p0 = ex2(sv[t][0] - bs0), p1 = ex2(sv[t][1] - bs1);
-                    const float p2 = ex2(sv[t][2] - bs0), p3 = ex2(sv[t][3] - bs1);
-                    ps0 += p0 + p2;
-                    ps1 += p1 + p3;
-                    if constexpr (!FP8) {
-                        pb[t][j][0] = movmatrix_t(pack_bf16(p0, p1));
-                        pb[t][j][1] = movmatrix_t(pack_bf16(p2, p3));
-                    } else {
-                        pb[t][j][0] = movmatrix_t(pack_f16(p0, p1));
-                        pb[t][j][1] = movmatrix_t(pack_f16(p2, p3));
-                    }
-                }
-                l0[j] = l0[j] * al0 + ps0;
-                l1[j] = l1[j] * al1 + ps1;
-                m0[j] = mn0;
-                m1[j] = mn1;
-                // (scales per block: most chunks leave the maxima as they are)
-                if (!BLK || __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
-#pragma unroll
-                    for (int mt = 0; mt < C::MT; ++mt) {
-                        acc[mt][j][0] *= al0;
-                        acc[mt][j][1] *= al1;
-                        acc[mt][j][2] *= al0;
-                        acc[mt][j][3] *= al1;
-                    }
-                }
-            }
-            // ---- O^T += V^T P^T
-            if constexpr (!FP8) {
-#pragma unroll
-                for (int mt = 0; mt < C::MT; ++mt) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int d = mt * 16 + (lmat & 1) * 8;
-                        const int x = d >> 6;
-                        const uint32_t addr =
-                            s_base + rv[t] + x * xstride + ((((d & 63) >> 3) ^ (keyv[t] + (HM ? 0 : x))) << 4);
-                        uint32_t a[4];
-                        ldsm_x4_t(addr, a[0], a[1], a[2], a[3]);
-#pragma unroll
-                        for (int j = 0; j < NQ; ++j) mma_bf16(acc[mt][j], a, pb[t][j][0], pb[t][j][1]);
-                    }
-                }
-            } else {
-                if constexpr (BLK) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const float vs = __shfl_sync(0xffffffffu, sc, 4 + t);
-#pragma unroll
-                        for (int kk = 0; kk < D / 32; ++kk) {
-                            const int chunk16 = kk * 2 + (lmat >> 1);
-                            const uint32_t addr = s_base + rv[t] + ((chunk16 ^ keyv[t]) << 4);
-                            uint32_t R[4];
-                            ldsm_x4_t(addr, R[0], R[1], R[2], R[3]);
-#pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                uint32_t a[4];  // token pairs per d, as below
-                                if constexpr (I8) {
-                                    a[0] = int8x2_to_f16x2<0, 2>(R[hf * 2]);
-                                    a[1] = int8x2_to_f16x2<1, 3>(R[hf * 2]);
-                                    a[2] = int8x2_to_f16x2<0, 2>(R[hf * 2 + 1]);
-                                    a[3] = int8x2_to_f16x2<1, 3>(R[hf * 2 + 1]);
-                                } else {
-                                    const uint32_t u = prmt(R[hf * 2], 0u, 0x3120u);
-                                    const uint32_t w = prmt(R[hf * 2 + 1], 0u, 0x3120u);
-                                    a[0] = e4m3x2_to_f16x2((uint16_t)(u & 0xffff));
-                                    a[1] = e4m3x2_to_f16x2((uint16_t)(u >> 16));
-                                    a[2] = e4m3x2_to_f16x2((uint16_t)(w & 0xffff));
-                                    a[3] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
-                                }
-#pragma unroll
-                                for (int j = 0; j < NQ; ++j) {
-                                    float pv[4];
-                                    mma_f16_zero(pv, a, pb[t][j][0], pb[t][j][1]);
-                                    fma_f32x2(acc[kk * 2 + hf][j][0], acc[kk * 2 + hf][j][1], vs, pv[0], pv[1]);
-                                    fma_f32x2(acc[kk * 2 + hf][j][2], acc[kk * 2 + hf][j][3], vs, pv[2], pv[3]);
-                                }
-                            }
+                            for (int j = 0; j < NQ; ++j) mma_bf16(sacc[t][j], a, qf[ks][j][0], qf[ks][j][1]);
                         }
                     }
                 } else {
 #pragma unroll
                     for (int kk = 0; kk < D / 32; ++kk) {
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
+                        for (int t = 0; t < NT; ++t) {
                             const int chunk16 = kk * 2 + (lmat >> 1);
-                            const uint32_t addr = s_base + rv[t] + ((chunk16 ^ keyv[t]) << 4);
+                            const uint32_t addr = s_base + rk[t] + po + ((chunk16 ^ keyk[t]) << 4);
                             uint32_t R[4];
-                            ldsm_x4_t(addr, R[0], R[1], R[2], R[3]);
+                            ldsm_x4(addr, R[0], R[1], R[2], R[3]);
 #pragma unroll
                             for (int hf = 0; hf < 2; ++hf) {
-                                // bytes of R: [v(t,d), v(t,d+1), v(t+1,d), v(t+1,d+1)] -> token pairs per d
-                                const uint32_t u = prmt(R[hf * 2], 0u, 0x3120u);
-                                const uint32_t w = prmt(R[hf * 2 + 1], 0u, 0x3120u);
+                                const uint32_t ra = R[hf * 2], rb = R[hf * 2 + 1];
                                 uint32_t a[4];
-                                a[0] = e4m3x2_to_f16x2((uint16_t)(u & 0xffff));
-                                a[1] = e4m3x2_to_f16x2((uint16_t)(u >> 16));
-                                a[2] = e4m3x2_to_f16x2((uint16_t)(w & 0xffff));
-                                a[3] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+                                if constexpr (I8) {
+                                    a[0] = int8x2_to_f16x2<0, 1>(ra);
+                                    a[1] = int8x2_to_f16x2<0, 1>(rb);
+                                    a[2] = int8x2_to_f16x2<2, 3>(ra);
+                                    a[3] = int8x2_to_f16x2<2, 3>(rb);
+                                } else {
+                                    a[0] = e4m3x2_to_f16x2((uint16_t)(ra & 0xffff));
+                                    a[1] = e4m3x2_to_f16x2((uint16_t)(rb & 0xffff));
+                                    a[2] = e4m3x2_to_f16x2((uint16_t)(ra >> 16));
+                                    a[3] = e4m3x2_to_f16x2((uint16_t)(rb >> 16));
+                                }
 #pragma unroll
-                                for (int j = 0; j < NQ; ++j) mma_f16(acc[kk * 2 + hf][j], a, pb[t][j][0], pb[t][j][1]);
+                                for (int j = 0; j < NQ; ++j)
+                                    mma_f16(sacc[t][j], a, qf[kk * 2 + hf][j][0], qf[kk * 2 + hf][j][1]);
+                            }
+                        }
+                    }
+                }
+                // ---- online softmax over the chunk's 64 tokens (rows 16t + r8, 16t + r8 + 8)
+                uint32_t pb[NT][NQ][2];
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    const int nv = (NQ * WPC == 1) ? nvalid : L_first + jo + j - cbase;
+                    // with a window, draft jo + j sees tokens from L_first + jo + j - window on
+                    const int lv = (WIN && p.window > 0) ? L_first + jo + j - p.window - cbase : -1;
+                    float sv[NT][4];
+                    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const int ra = 16 * (pass * NT + t) + r8, rb = ra + 8;
+                        const bool va = ra < nv && ra >= lv, vb = rb < nv && rb >= lv;
+                        const float st = BLK ? __shfl_sync(0xffffffffu, sc, pass * NT + t) : sl2;
+                        sv[t][0] = va ? sacc[t][j][0] * st : -INFINITY;
+                        sv[t][1] = va ? sacc[t][j][1] * st : -INFINITY;
+                        sv[t][2] = vb ? sacc[t][j][2] * st : -INFINITY;
+                        sv[t][3] = vb ? sacc[t][j][3] * st : -INFINITY;
+                        mx0 = fmaxf(mx0, fmaxf(sv[t][0], sv[t][2]));
+                        mx1 = fmaxf(mx1, fmaxf(sv[t][1], sv[t][3]));
+                    }
+                    const float mn0 = fmaxf(m0[j], warp_max_xor_4_8_16(mx0));
+                    const float mn1 = fmaxf(m1[j], warp_max_xor_4_8_16(mx1));
+                    // an earlier draft token, or one whose window starts behind these tiles, may have seen no token yet: keep
+                    // the exponent base finite so that 2^(-inf - base) = 0, not NaN
+                    const float bs0 = ((NQ * WPC > 1 || NT < 4) && mn0 == -INFINITY) ? 0.f : mn0;
+                    const float bs1 = ((NQ * WPC > 1 || NT < 4) && mn1 == -INFINITY) ? 0.f : mn1;
+                    const float al0 = ex2(m0[j] - bs0), al1 = ex2(m1[j] - bs1);
+                    float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const float p0 = ex2(sv[t][0] - bs0), p1 = ex2(sv[t][1] - bs1);
+                        const float p2 = ex2(sv[t][2] - bs0), p3 = ex2(sv[t][3] - bs1);
+                        ps0 += p0 + p2;
+                        ps1 += p1 + p3;
+                        if constexpr (!FP8) {
+                            pb[t][j][0] = movmatrix_t(pack_bf16(p0, p1));
+                            pb[t][j][1] = movmatrix_t(pack_bf16(p2, p3));
+                        } else {
+                            pb[t][j][0] = movmatrix_t(pack_f16(p0, p1));
+                            pb[t][j][1] = movmatrix_t(pack_f16(p2, p3));
+                        }
+                    }
+                    l0[j] = l0[j] * al0 + ps0;
+                    l1[j] = l1[j] * al1 + ps1;
+                    m0[j] = mn0;
+                    m1[j] = mn1;
+                    // (scales per block: most chunks leave the maxima as they are)
+                    if (!BLK || __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
+#pragma unroll
+                        for (int mt = 0; mt < C::MT; ++mt) {
+                            acc[mt][j][0] *= al0;
+                            acc[mt][j][1] *= al1;
+                            acc[mt][j][2] *= al0;
+                            acc[mt][j][3] *= al1;
+                        }
+                    }
+                }
+                // ---- O^T += V^T P^T
+                if constexpr (!FP8) {
+#pragma unroll
+                    for (int mt = 0; mt < C::MT; ++mt) {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const int d = mt * 16 + (lmat & 1) * 8;
+                            const int x = d >> 6;
+                            const uint32_t addr =
+                                s_base + rv[t] + po + x * xstride + ((((d & 63) >> 3) ^ (keyv[t] + (HM ? 0 : x))) << 4);
+                            uint32_t a[4];
+                            ldsm_x4_t(addr, a[0], a[1], a[2], a[3]);
+#pragma unroll
+                            for (int j = 0; j < NQ; ++j) mma_bf16(acc[mt][j], a, pb[t][j][0], pb[t][j][1]);
+                        }
+                    }
+                } else {
+                    if constexpr (BLK) {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const float vs = __shfl_sync(0xffffffffu, sc, 4 + pass * NT + t);
+#pragma unroll
+                            for (int kk = 0; kk < D / 32; ++kk) {
+                                const int chunk16 = kk * 2 + (lmat >> 1);
+                                const uint32_t addr = s_base + rv[t] + po + ((chunk16 ^ keyv[t]) << 4);
+                                uint32_t R[4];
+                                ldsm_x4_t(addr, R[0], R[1], R[2], R[3]);
+#pragma unroll
+                                for (int hf = 0; hf < 2; ++hf) {
+                                    uint32_t a[4];  // token pairs per d, as below
+                                    if constexpr (I8) {
+                                        a[0] = int8x2_to_f16x2<0, 2>(R[hf * 2]);
+                                        a[1] = int8x2_to_f16x2<1, 3>(R[hf * 2]);
+                                        a[2] = int8x2_to_f16x2<0, 2>(R[hf * 2 + 1]);
+                                        a[3] = int8x2_to_f16x2<1, 3>(R[hf * 2 + 1]);
+                                    } else {
+                                        const uint32_t u = prmt(R[hf * 2], 0u, 0x3120u);
+                                        const uint32_t w = prmt(R[hf * 2 + 1], 0u, 0x3120u);
+                                        a[0] = e4m3x2_to_f16x2((uint16_t)(u & 0xffff));
+                                        a[1] = e4m3x2_to_f16x2((uint16_t)(u >> 16));
+                                        a[2] = e4m3x2_to_f16x2((uint16_t)(w & 0xffff));
+                                        a[3] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+                                    }
+#pragma unroll
+                                    for (int j = 0; j < NQ; ++j) {
+                                        float pv[4];
+                                        mma_f16_zero(pv, a, pb[t][j][0], pb[t][j][1]);
+                                        fma_f32x2(acc[kk * 2 + hf][j][0], acc[kk * 2 + hf][j][1], vs, pv[0], pv[1]);
+                                        fma_f32x2(acc[kk * 2 + hf][j][2], acc[kk * 2 + hf][j][3], vs, pv[2], pv[3]);
+                                    }
+                                }
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < D / 32; ++kk) {
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                const int chunk16 = kk * 2 + (lmat >> 1);
+                                const uint32_t addr = s_base + rv[t] + po + ((chunk16 ^ keyv[t]) << 4);
+                                uint32_t R[4];
+                                ldsm_x4_t(addr, R[0], R[1], R[2], R[3]);
+#pragma unroll
+                                for (int hf = 0; hf < 2; ++hf) {
+                                    // bytes of R: [v(t,d), v(t,d+1), v(t+1,d), v(t+1,d+1)] -> token pairs per d
+                                    const uint32_t u = prmt(R[hf * 2], 0u, 0x3120u);
+                                    const uint32_t w = prmt(R[hf * 2 + 1], 0u, 0x3120u);
+                                    uint32_t a[4];
+                                    a[0] = e4m3x2_to_f16x2((uint16_t)(u & 0xffff));
+                                    a[1] = e4m3x2_to_f16x2((uint16_t)(u >> 16));
+                                    a[2] = e4m3x2_to_f16x2((uint16_t)(w & 0xffff));
+                                    a[3] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+#pragma unroll
+                                    for (int j = 0; j < NQ; ++j) mma_f16(acc[kk * 2 + hf][j], a, pb[t][j][0], pb[t][j][1]);
+                                }
                             }
                         }
                     }
