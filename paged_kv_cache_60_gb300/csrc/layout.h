@@ -264,7 +264,7 @@ struct CopyPagesParams {
     float *weights;                // per page weight_len values, or null
     int32_t *error;                // may be null
     int64_t k_units, v_units;      // 16-byte units of a page
-    int32_t max_copies, num_pages, pieces, scale_len, weight_len;
+    int32_t max_copies, num_pages, k_pieces, pieces, scale_len, weight_len;
 };
 
 // Probabilities out of logits (probs.cu). Sixteen CTAs hold 2^19 values in groups of eight; a row's first group may start
