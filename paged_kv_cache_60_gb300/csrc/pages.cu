@@ -36,7 +36,7 @@ constexpr int kBatch = 8;              // words that a warp reads at once
 constexpr int kPagesPerCta = kPlanWarps * kBatch * 32;
 constexpr int kFewRows = kPlanThreads, kSlots = 2 * kFewRows;  // requests with a hash table, and its places
 constexpr int kForkThreads = 256, kForkColumns = 1024;
-constexpr int kCopyThreads = 64, kCopyPiece = 16 << 10, kCopyStages = 6;
+constexpr int kCopyThreads = 64, kCopyPiece = 8 << 10, kCopyStages = 8;
 
 
 __device__ __forceinline__ void report(int32_t *error, int bits) {
@@ -679,7 +679,7 @@ cudaError_t launch_copy_pages(CopyPagesParams p, int num_sms, cudaStream_t strea
     if (kp + vp > INT32_MAX) return cudaErrorInvalidConfiguration;
     p.k_pieces = (int)kp;
     p.pieces = (int)(kp + vp);
-    const int64_t items = (int64_t)p.max_copies * p.pieces, most = (int64_t)num_sms * 2;
+    const int64_t items = (int64_t)p.max_copies * p.pieces, most = (int64_t)num_sms * 3;
     const cudaError_t e = cudaFuncSetAttribute(copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCopyStages * kCopyPiece);
     if (e != cudaSuccess) return e;
     return launch(copy_kernel, items < most ? items : most, kCopyThreads, kCopyStages * kCopyPiece, 0, stream, pdl, p);

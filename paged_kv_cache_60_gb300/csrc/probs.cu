@@ -88,6 +88,16 @@ struct Raw {
             w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
         }
     }
+    // from shared memory that a bulk copy fills again once it is released: volatile, so that the loads stay ahead of the
+    // release (plain ones, released before their values had been used, gave some rows the next piece's values)
+    __device__ __forceinline__ void load_shared(uint32_t at) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "r"(at + i * 4)
+                         : "memory");
+    }
     // value by value, those of [0, V); t: the first one's token
     __device__ __forceinline__ void load_some(const T *row, int t, int V) {
         clear();
@@ -319,11 +329,11 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
     };
     // this thread's groups of a piece that starts with group g, in its slot
     const auto read_slot = [&](int slot, int g, auto &r, auto all) {
-        const TI *at = reinterpret_cast<const TI *>(reinterpret_cast<const uint8_t *>(smem_v) + (size_t)slot * kPieceBytes) + tid * 8;
+        const uint32_t at = smem_u32(smem_v) + (uint32_t)(slot * kPieceBytes + tid * 8 * (int)sizeof(TI));
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (all || g + i * kThreads + tid < whole1)
-                r[i].load(at + i * kThreads * 8);
+                r[i].load_shared(at + i * kThreads * 8 * (int)sizeof(TI));
             else
                 r[i].clear();
         }
@@ -513,7 +523,6 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
             Raw<TI> r[kPer];
             const auto part = [&](auto all, auto untouched) {  // (all: whole pieces; untouched: no token is left out)
                 read_slot(now.slot, g, r, all);
-                if (k + slots < pieces) release(now.slot);
                 if (!untouched && (bits || listed > 0)) {
 #pragma unroll
                     for (int i = 0; i < kPer; ++i)
@@ -527,6 +536,10 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
                 part(std::true_type(), std::false_type());
             else
                 part(std::false_type(), std::false_type());
+            if (k + slots < pieces) {
+                asm volatile("" ::"f"(run.m), "f"(run.sum));  // everything read has been used
+                release(now.slot);
+            }
         }
     }
     // the listed tokens
@@ -660,7 +673,6 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
                         if (tid == 0 && k > 0 && k - 1 < pieces - left) refill();
                         if (k >= left) wait(&full[now.slot], now.round - 1);
                         read_slot(now.slot, g, r, all);
-                        if (k < pieces - left) release(now.slot);
                     }
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) {
@@ -687,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
                     part(std::true_type(), std::true_type());
                 else
                     part(std::false_type(), std::false_type());
+                if (warm && k < pieces - left) release(now.slot);
             }
         }
         if (listed > 0 && warm) {

@@ -161,6 +161,27 @@ def test_many_long_rows_with_long_histories(tin):
     assert ((out[:, 0].double() - want).abs() <= want * rel + 2.0 ** -126).all()
 
 
+def test_streaming_shares_over_and_over():
+    """More rows than fit at once, whose pieces go round a ring of few slots: a slot that is filled again before every warp
+    has read it shows in some row of some run."""
+    B, V, n = 1024, 131072, 8192
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (torch.randn(B, 1, V, device="cuda", generator=g) * 2.5).to(BF16)
+    hist = (torch.rand(B, n, device="cuda", generator=g) ** 3 * V).int()
+    lens = torch.randint(n // 2, n + 1, (B,), device="cuda", generator=g, dtype=torch.int32)
+    out, first = torch.empty_like(x), None
+    for _ in range(25):
+        out.fill_(7)
+        da.token_probs(x, out, history=hist, history_lens=lens)         # no penalties: the listed tokens keep their logits
+        if first is None:
+            first = out.clone()
+            for lo in range(0, B, 128):
+                want = torch.softmax(x[lo:lo + 128].double(), -1)
+                # fp32 as in the tests above (magnitudes up to 20, T = 1), then bf16: half a step
+                assert ((first[lo:lo + 128].double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -24 * (3 * 5 * 40 + 8 * 40 + 102)) + 2.0 ** -126).all()
+        assert torch.equal(out, first)
+
+
 def test_rows_that_start_anywhere_and_results_in_place():
     for pad in (0, 1, 3, 5):
         c = _case(3, 2, 777, 6 + pad, hist=30, mask=0.8)
