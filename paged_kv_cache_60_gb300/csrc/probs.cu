@@ -58,6 +58,7 @@ constexpr int kPieceBytes = 16 << 10;
 constexpr int kMaxSlots = 12;
 constexpr int kAhead = 8, kAbreast = 4;        // tokens of the history, listed tokens that a thread has under way
 constexpr int kSmemMax = 224 << 10, kSmemTwo = 112 << 10;  // of a CTA; where two fit an SM
+constexpr int kBiasRoom = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kPrompt = 0x80000000u, kBias = 0x40000000u, kCount = kBias - 1;
 
@@ -183,15 +184,16 @@ __device__ __forceinline__ void store1(float *at, float x) { *at = x; }
 __device__ __forceinline__ void store1(__nv_bfloat16 *at, float x) { *at = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void store1(__half *at, float x) { *at = __float2half_rn(x); }
 
-// A row of probabilities: a group of eight, of which only tokens in [0, V) are there (vec: it is aligned like the logits' group)
+// A row of probabilities: a group of eight, of which only tokens in [0, V) are there, those in `skip` left as they are (vec: it is
+// aligned like the logits' group)
 template <typename T>
-__device__ __forceinline__ void store_group(T *row, int t, int V, bool vec, const float (&x)[8]) {
-    if (vec && t >= 0 && t + 8 <= V) {
+__device__ __forceinline__ void store_group(T *row, int t, int V, bool vec, uint32_t skip, const float (&x)[8]) {
+    if (vec && t >= 0 && t + 8 <= V && skip == 0) {
         store8(row + t, x);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (t + i >= 0 && t + i < V) store1(row + t + i, x[i]);
+            if (t + i >= 0 && t + i < V && !(skip >> i & 1)) store1(row + t + i, x[i]);
     }
 }
 
@@ -234,6 +236,35 @@ struct Run {
         if (x > m || (x == m && token < at && x > -INFINITY)) m = x, at = token;
     }
 };
+
+// What x becomes of a logit with a count and marks (kPrompt, kBias, kCount).
+__device__ __forceinline__ float adjusted(const ProbsParams &p, int t, float y, uint32_t c, float rep, float freq, float pres,
+                                          int blo, int bhi) {
+    const uint32_t n = c & kCount;
+    if (n > 0 || (c & kPrompt)) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+    y = __fsub_rn(y, __fmul_rn(freq, (float)n));
+    if (n > 0) y = __fsub_rn(y, pres);
+    if (c & kBias)
+        for (int e = blo; e < bhi; ++e)
+            if (p.bias_tokens[e] == t) y = __fadd_rn(y, p.bias_values[e]);
+    return y;
+}
+// x of token t in row j of request b, counted by itself: for requests with more tokens than a list has room for. Out of line: the
+// walks' registers.
+__device__ __noinline__ float counted(const ProbsParams &p, int b, int j, int t, float logit) {
+    const int n_hist = p.history ? min(max(p.history_lens[b], 0), p.history_cols) : 0, prompt = p.prompt_lens ? p.prompt_lens[b] : 0;
+    const int32_t *hist = p.history + (int64_t)b * p.history_cols, *drafts = p.drafts + (int64_t)b * p.K;
+    uint32_t c = kBias;
+    for (int i = 0; i < n_hist; ++i)
+        if (hist[i] == t) c = i < prompt ? c | kPrompt : c + 1;
+    for (int i = 0; p.drafts != nullptr && i < j && drafts[i] >= 0; ++i) c += drafts[i] == t;
+    const int blo = p.bias_starts ? min(max(p.bias_starts[b], 0), p.n_bias) : 0;
+    const int bhi = p.bias_starts ? min(max(p.bias_starts[b + 1], 0), p.n_bias) : 0;
+    const float y = adjusted(p, t, logit, c, p.repetition ? p.repetition[b] : 1.f, p.frequency ? p.frequency[b] : 0.f,
+                             p.presence ? p.presence[b] : 0.f, blo, bhi);
+    const uint32_t *bits = p.allowed ? p.allowed + ((int64_t)b * (p.K + 1) + j) * p.allowed_stride : nullptr;
+    return !bits || (bits[t >> 5] >> (t & 31) & 1) ? y : -INFINITY;
+}
 
 // kG: groups of eight values that a thread holds between the walks; 0: the share streams
 template <typename TI, int kG>
@@ -366,13 +397,15 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
     int upper = INT32_MAX;
     const auto token_at = [&](int i) -> int { return t0 + list[i] + (i >= upper ? 65536 : 0); };
     int listed = 0;
+    bool crowded = false;  // more than the list has room for
+    const int prompt = p.prompt_lens ? p.prompt_lens[b] : 0;
+    const int32_t *hist = p.history + (int64_t)b * p.history_cols;
+    const int32_t *drafts = p.drafts ? p.drafts + (int64_t)b * p.K : nullptr;
     if (touched) {
         const int cap = min(p.cap, n_hist + j + bhi - blo);
         for (int i = tid; i < share_words; i += kThreads) mark[i] = 0u;
         for (int i = tid; i < cap; i += kThreads) value[i] = 0u;
         __syncthreads();
-        const int prompt = p.prompt_lens ? p.prompt_lens[b] : 0;
-        const int32_t *hist = p.history + (int64_t)b * p.history_cols;
         const int lowest = max(t0, 0), span = min(V - t0, groups * 8) - (lowest - t0);
         // f(token's place in the share) for every token of the history in [from, to)
         const auto each = [&](int from, int to, auto f) {
@@ -387,11 +420,10 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
         };
         // and for those of the drafts (draft tid, unless the chain has ended before it) and biases
         const auto drafted = [&](auto f) {
-            if (p.drafts == nullptr || tid >= j) return;
-            const int32_t *d = p.drafts + (int64_t)b * p.K;
+            if (drafts == nullptr || tid >= j) return;
             bool there = true;
-            for (int i = 0; i <= tid; ++i) there = there && d[i] >= 0;
-            if (there && (unsigned)(d[tid] - lowest) < (unsigned)span) f(d[tid] - t0);
+            for (int i = 0; i <= tid; ++i) there = there && drafts[i] >= 0;
+            if (there && (unsigned)(drafts[tid] - lowest) < (unsigned)span) f(drafts[tid] - t0);
         };
         const auto biased = [&](auto f) {
             for (int i = blo + tid; i < bhi; i += kThreads)
@@ -431,13 +463,15 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
             list[at] = (uint16_t)i;
             return value + at;
         };
-        each(0, min(prompt, n_hist), [&](int i) { atomicOr(enlist(i), kPrompt); });
-        each(max(prompt, 0), n_hist, [&](int i) { atomicAdd(enlist(i), 1u); });
-        drafted([&](int i) { atomicAdd(enlist(i), 1u); });
-        biased([&](int i) { atomicOr(enlist(i), kBias); });
+        crowded = listed > p.cap;
+        if (!crowded) {
+            each(0, min(prompt, n_hist), [&](int i) { atomicOr(enlist(i), kPrompt); });
+            each(max(prompt, 0), n_hist, [&](int i) { atomicAdd(enlist(i), 1u); });
+            drafted([&](int i) { atomicAdd(enlist(i), 1u); });
+            biased([&](int i) { atomicOr(enlist(i), kBias); });
+        }
         __syncthreads();
     }
-
     if (kG == 0) __syncthreads();  // the ring's barriers are initialised
     // ------------------------------------------------ the first walk: all tokens but those
     Run run;
@@ -542,8 +576,20 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
             }
         }
     }
-    // the listed tokens
-    if (listed > 0) {
+    // the listed tokens; or, where they are too many for that, the marked ones
+    if (crowded) {
+        for (int w = tid; w < share_words; w += kThreads)
+            for (uint32_t m = mark[w]; m; m &= m - 1) {
+                const int t = t0 + w * 32 + __ffs(m) - 1;
+                const float v = counted(p, b, j, t, static_cast<float>(in[t]));
+                if (warm) {
+                    const float from = run.raise(v, scale);
+                    run.sum += ex2((v - from) * scale);
+                } else {
+                    run.take(v, t);
+                }
+            }
+    } else if (listed > 0) {
         const float rep = p.repetition ? p.repetition[b] : 1.f, freq = p.frequency ? p.frequency[b] : 0.f;
         const float pres = p.presence ? p.presence[b] : 0.f;
         for (int i0 = tid; i0 < listed; i0 += kAbreast * kThreads) {
@@ -560,14 +606,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
             for (int k = 0; k < kAbreast; ++k) {
                 const int i = i0 + k * kThreads;
                 if (i >= listed) continue;
-                const uint32_t c = value[i], n = c & kCount;
-                float y = v[k];
-                if (n > 0 || (c & kPrompt)) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
-                y = __fsub_rn(y, __fmul_rn(freq, (float)n));
-                if (n > 0) y = __fsub_rn(y, pres);
-                if (c & kBias)
-                    for (int e = blo; e < bhi; ++e)
-                        if (p.bias_tokens[e] == t[k]) y = __fadd_rn(y, p.bias_values[e]);
+                const float y = adjusted(p, t[k], v[k], value[i], rep, freq, pres, blo, bhi);
                 v[k] = !bits || (bits[t[k] >> 5] >> (t[k] & 31) & 1) ? y : -INFINITY;
                 value[i] = __float_as_uint(v[k]);
                 if (!warm) run.take(v[k], t[k]);
@@ -624,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
     const float from = nothing ? 0.f : best.x, off = nothing ? -INFINITY : -log2f(best.y);
     const bool bad = warm && !nothing && !(best.y < INFINITY);  // (largest NaN or infinite)
     const Exps exps{from, scale, off};
-    const bool ordinary = warm && !bits && !bad && !nothing && vec;
+    const bool ordinary = warm && !bits && !bad && !nothing && !crowded && vec;
     const auto second = [&](auto *row) {  // of the probabilities, as what they are
         const auto probabilities = [&](int g, const Raw<TI> &r, float (&v)[8]) {
             if (warm) {
@@ -640,11 +679,24 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
                 for (int i = 0; i < 8; ++i) v[i] = t + i == at ? 1.f : 0.f;
             }
         };
+        // of a group, the tokens that have been written before the walk
+        const auto written = [&](int g) -> uint32_t {
+            return crowded && warm ? (uint32_t) reinterpret_cast<const uint8_t *>(mark)[g] : 0u;
+        };
         const auto write = [&](int g, const Raw<TI> &r) {
             float v[8];
             probabilities(g, r, v);
-            store_group(row, t0 + g * 8, V, vec, v);
+            store_group(row, t0 + g * 8, V, vec, written(g), v);
         };
+        if (crowded && warm) {  // ahead of the walk: it may write over the logits
+            for (int w = tid; w < share_words; w += kThreads)
+                for (uint32_t m = mark[w]; m; m &= m - 1) {
+                    const int t = t0 + w * 32 + __ffs(m) - 1;
+                    const float v = exps(counted(p, b, j, t, static_cast<float>(in[t])));
+                    store1(row + t, bad ? NAN : nothing ? 0.f : v);
+                }
+            __syncthreads();
+        }
         if constexpr (kG > 0) {
 #pragma unroll
             for (int k = 0; k < kG; ++k)
@@ -687,12 +739,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
                         }
                         if (bits && warm && keep[i] != 0xFFu) r[i].drop(keep[i]);
                         probabilities(gi, r[i], v);
-                        if (vec) {
-                            store8(at + i * kThreads * 8, v);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) store1(at + i * kThreads * 8 + e, v[e]);
-                        }
+                        store_group(row, t0 + gi * 8, V, vec, written(gi), v);
                     }
                 };
                 if (g + kPiece <= whole1 && ordinary)
@@ -702,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
                 if (warm && k < pieces - left) release(now.slot);
             }
         }
-        if (listed > 0 && warm) {
+        if (listed > 0 && !crowded && warm) {
             __syncthreads();  // over what the walk has left at the listed tokens
             for (int i0 = tid; i0 < listed; i0 += kAbreast * kThreads) {
 #pragma unroll
@@ -760,7 +807,9 @@ cudaError_t launch_types(ProbsParams p, int num_sms, cudaStream_t stream, bool p
     const int head = p.logits_stride % 8 == 0 ? (int)(reinterpret_cast<uintptr_t>(p.logits) / sizeof(TI) & 7) : 7;
     const int groups = (p.V + head + 7) / 8;
     const int64_t rows = (int64_t)p.B * (p.K + 1);
-    const int64_t touches = (int64_t)p.history_cols + (p.drafts ? p.K : 0) + (p.bias_starts ? p.n_bias : 0);
+    // tokens that a list has room for: those of the history and drafts, and of the biases as many as a request has in earnest
+    // (n_bias is all requests'); a request with more counts for each token by itself
+    const int64_t touches = (int64_t)p.history_cols + (p.drafts ? p.K : 0) + (p.bias_starts ? min(p.n_bias, kBiasRoom) : 0);
     const auto split = [&](int c) -> size_t {  // a row over c CTAs: the shared memory of one
         p.ctas = c;
         p.share = (groups + c - 1) / c;

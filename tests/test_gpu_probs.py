@@ -220,6 +220,24 @@ def test_one_token_biased_many_times():
     _run(c)
 
 
+@pytest.mark.parametrize("V,B,K", [(3000, 3, 1), (60000, 2, 0), (20000, 160, 0)])
+def test_more_biases_than_a_list_has_room_for(V, B, K):
+    """One request with thousands of biases beside others with few, in every way that a share is held, in place too."""
+    c = _case(B, K, V, 17, hist=40, bias=3, mask=0.8, temps=(1.0, 0.7, 0.0))
+    g = np.random.RandomState(4)
+    starts, toks, vals = c["bias"]
+    many = 2500
+    c["temperature"][0], c["temperature"][-1] = 0.9, 0.0
+    c["bias"] = (np.concatenate([[0], starts[1:] + many]).astype(np.int32), np.concatenate([g.randint(0, V, many), toks]).astype(np.int32),
+                 np.concatenate([g.randn(many), vals]).astype(np.float32))
+    _run(c)
+    _run(c, F32, F32, in_place=True)
+    if B < 10:                                            # all of them in the one greedy request
+        n = int(c["bias"][0][-1])
+        c["bias"] = (np.array([0] * B + [n], np.int32), *c["bias"][1:])
+        _run(c, BF16, BF16)
+
+
 def test_rows_that_nothing_is_left_of():
     c = _case(3, 1, 500, 10, temps=(1.0, 0.0))
     c["temperature"][:] = [1.0, 0.0, 1.0]
