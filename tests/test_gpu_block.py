@@ -304,3 +304,53 @@ def test_scale_for_is_the_kernels_rule():
         _, s = _check_append(desc, kind, pools, scales, rows, rows, [0, 16 * n], [0], table)
         assert [float(v) for v in s[0][:, 0, 0]] == [scale_for(float(v), kind) for v in x]
         assert values_of(np.array([0x7E], np.uint8), "fp8") == 448
+
+
+def test_pools_beyond_4_gib():
+    """Pages whose codes lie past 2^32 bytes, whose scales' indexes stay apart: append, copy and attention there."""
+    P, H, kv = 64, 8, da.KV_INT8_BLOCK
+    pages = (1 << 32) // (P * H * 128) + 40
+    kp, vp = (torch.empty(pages, P, H, 128, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty(pages, H, P // 16, device="cuda") for _ in range(2))
+    desc = da.Desc.make(B=2, H_kv=H, G=8, D_qk=128, D_v=128, page_size=P, max_pages_per_seq=4, num_pages=pages, kv_dtype=kv)
+    table = _i32([[pages - 1, 3, pages - 2, pages - 3], [5, pages - 4, 7, pages - 5]])
+    g = np.random.RandomState(2)
+    x, y = _rows(g, 400, H), _rows(g, 400, H)
+    da.append_block(desc, x.to(torch.bfloat16).cuda(), y.to(torch.bfloat16).cuda(), _i32([0, 0]), table, kp, vp, ks, vs, token_starts=_i32([0, 200, 400]))
+    moved = _i32([[pages - 1, pages - 10], [3, pages - 11], [pages - 2, 9], [pages - 3, 11]])
+    da.copy_pages(desc, moved, kp, vp, k_scale=ks, v_scale=vs)
+    q = torch.randn(2, 8 * H, 128, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    meta = torch.empty(da.sched_meta_bytes(desc), dtype=torch.uint8, device="cuda")
+    seq, outs = _i32([200, 200]), []
+    for t in (table, torch.cat([moved[:, 1][None], table[1:]]).contiguous()):
+        out, lse = torch.empty(2, 8 * H, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 8 * H, device="cuda")
+        da.sched_meta(desc, seq, meta)
+        da.fwd(desc, q, kp, vp, ks, vs, t, seq, meta, out, lse)
+        outs.append((out, lse))
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    for b in range(2):
+        # int8 with power-of-two scales of whole blocks: at most half a step of up to 2 max / 127
+        for pool, scale, v in ((kp, ks, x), (vp, vs, y)):
+            rows = pool[table[b].long()].view(torch.int8).double().view(256, H, 128)[:200]
+            sc = scale[table[b].long()].double().transpose(1, 2).reshape(16, H).repeat_interleave(16, 0)[:200]
+            assert ((rows * sc[..., None]).cpu() - v[200 * b:200 * b + 200].double()).abs().max() <= 0.5 * sc.max().cpu()
+    assert torch.isfinite(outs[0][0].float()).all()
+
+
+def test_without_a_caller_s_scratch():
+    """The allocation-free call takes the block formats too, with the same bits."""
+    B, P, H, cols, kv = 2, 16, 1, 8, da.KV_FP8_BLOCK
+    kind = "fp8"
+    (kc, ks), (vc, vs) = _filled(kind, B * cols, P, H, 1), _filled(kind, B * cols, P, H, 2)
+    dev = [torch.from_numpy(x).cuda() for x in (kc, vc, ks, vs)]
+    table, seq = torch.from_numpy(_table([cols * P] * B, P, cols, B * cols, 4)).cuda(), _i32([100, 37])
+    desc = da.Desc.make(B=B, H_kv=H, G=8, D_qk=128, D_v=128, page_size=P, max_pages_per_seq=cols, num_pages=B * cols, kv_dtype=kv, splits=4)
+    q = torch.randn(B, 8, 128, device="cuda").to(torch.bfloat16)
+    meta = torch.empty(da.sched_meta_bytes(desc), dtype=torch.uint8, device="cuda")
+    o = [torch.empty(B, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    l = [torch.empty(B, 8, device="cuda") for _ in range(2)]
+    da.sched_meta(desc, seq, meta)
+    da.fwd(desc, q, *dev, table, seq, meta, o[0], l[0])
+    da.fwd_static_scratch(desc, q, *dev, table, seq, o[1], l[1])
+    assert torch.equal(o[0], o[1]) and torch.equal(l[0], l[1])

@@ -155,6 +155,32 @@ def test_random_runs_of_all_of_them(B, P, cols, pages, seed):
         assert np.array_equal(held, s.refs)               # every hold is a table entry
 
 
+def test_many_rows():
+    """More rows than find out by a hash table who keeps a page, and the largest number of them."""
+    g = np.random.RandomState(7)
+    for B in (1024, 1025, 2500, 8192):
+        s = State(B, 4, 12, 6 * B)
+        s.reserve(g.randint(0, 12, size=B).tolist())
+        s.lens = np.maximum(s.held * 4 - g.randint(0, 4, size=B), 0).astype(np.int32)
+        for _ in range(2):
+            s.fork((np.arange(B) - g.randint(0, 3, size=B) % (np.arange(B) + 1)).tolist())
+            copies, missing, _ = s.reserve(g.choice([0, 1, 5], size=B).tolist())
+            assert missing == 0 and (copies[:, 0] >= 0).any()
+        s.free((g.rand(B) < 0.5).astype(int).tolist())
+        s.compact()
+
+
+def test_a_pool_of_one_page():
+    s = State(1, 16, 1, 1)
+    s.reserve([5])
+    s.lens[0] = 5
+    assert s.compact() == []
+    s.fork([0])
+    s.reserve([11])
+    s.fork([-1])
+    assert s.compact() == [] and s.refs[0] == 0
+
+
 def test_every_holder_of_a_page_writes_to_it():
     """Six rows share one partly filled page: the lowest keeps it; when one of them sits out, all writers copy."""
     s = State(6, 16, 4, 12)
