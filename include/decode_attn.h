@@ -525,6 +525,7 @@ int decode_attn_compact_pages(const da_desc *desc, const int32_t *block_table, c
  *   copies: device int32 [max_copies][2] (source, destination), a negative source: none;
  *     a page outside the pool: skipped (DA_DEV_BAD_PAGE). num_copies: device int32 [1] or
  *     NULL (all): only the first of them. No destination may be a source, or stand twice.
+ *     A pipeline wait that runs out sets DA_DEV_TIMEOUT; pages are then missing.
  *   k_scale, v_scale: the block formats' scales, else ignored. weights: fp32
  *     [num_pages][H_kv][page_size] or NULL. v_pool: NULL or k_pool for the 656-byte token.
  * One kernel.
@@ -571,6 +572,7 @@ typedef struct {
  *   p(v) = e^(x(v) / temperature) / sum over the allowed tokens, 0 for the others, whatever
  *     their logits are; with a temperature that is not above 0, 1 for the largest x (the
  *     lowest token of equals; a NaN is not the largest) and 0 for the others.
+ * A pipeline wait that runs out sets DA_DEV_TIMEOUT; the probabilities are then not valid.
  * A row without an allowed token whose x is above -infinity is 0 throughout
  * (DA_DEV_BAD_PROBS). A NaN or +infinity among the allowed x makes a row NaN throughout
  * (not a greedy one).

@@ -999,6 +999,8 @@ int decode_attn_copy_pages(const da_desc *desc, int32_t max_copies, const int32_
     p.error = device_error;
     p.k_units = page_bytes / 16;
     p.v_units = mla ? 0 : page_bytes / 16;
+    p.wait_limit_ns = g_wait_limit_ns ? g_wait_limit_ns : kWaitLimitNs;
+    p.debug_stall = g_debug_stall;
     p.max_copies = max_copies;
     p.num_pages = desc->num_pages;
     p.scale_len = desc->H_kv * (desc->page_size / kScaleBlock);
@@ -1063,6 +1065,8 @@ int decode_attn_token_probs(int32_t B, int32_t n_draft, int32_t vocab, int32_t l
     p.allowed_stride = allowed_stride;
     p.error = device_error;
     p.history_cols = r.history ? r.history_cols : 0;
+    p.wait_limit_ns = g_wait_limit_ns ? g_wait_limit_ns : kWaitLimitNs;
+    p.debug_stall = g_debug_stall;
     p.n_bias = r.n_bias;
     p.B = B;
     p.K = n_draft;

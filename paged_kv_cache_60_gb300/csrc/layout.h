@@ -264,6 +264,8 @@ struct CopyPagesParams {
     float *weights;                // per page weight_len values, or null
     int32_t *error;                // may be null
     int64_t k_units, v_units;      // 16-byte units of a page
+    uint64_t wait_limit_ns;
+    int32_t debug_stall;           // test build only: the first store waits on a barrier nothing completes
     int32_t max_copies, num_pages, k_pieces, pieces, scale_len, weight_len;
 };
 
@@ -287,6 +289,8 @@ struct ProbsParams {
     int32_t logits_dtype, prob_dtype, history_cols, n_bias, B, K, V;
     int32_t slots;                 // pieces of a streaming share that shared memory holds
     int32_t cap;                   // listed tokens of a share at most
+    uint64_t wait_limit_ns;
+    int32_t debug_stall;           // test build only: the walkers first wait on a barrier nothing completes
     int32_t ctas, share;           // CTAs of a row; groups of eight values to a CTA
 };
 

@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kForkThreads) remap_kernel(const __grid_consta
 // bytes a thread and load, four in flight, 2048 threads an SM: 288).
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyPagesParams p) {
     extern __shared__ uint4 ring_v[];
-    __shared__ uint64_t full[kCopyStages];
+    __shared__ uint64_t full[kCopyStages], never;  // (never: a barrier that nothing completes, in the test build)
     __shared__ uint8_t *dst_of[kCopyStages];  // where the stages' pieces go, and their sizes
     __shared__ uint32_t size_of[kCopyStages];
     pdl_wait();
@@ -499,17 +499,29 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     if (warp == 0) {
         uint8_t *ring = reinterpret_cast<uint8_t *>(ring_v);
         if (lane < kCopyStages) mbar_init(&full[lane], 1);
+        if (lane == kCopyStages) mbar_init(&never, 1);
         fence_barrier_init();
         fence_proxy_async_smem();
         __syncwarp();
         const int64_t items = (int64_t)n * p.pieces, mine = items > blockIdx.x ? (items - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
         int loads = 0, stores = 0;          // of this CTA, so far (lane 0)
+        bool lost = false;                  // a wait has run out: nothing more is loaded or stored
         const auto store_next = [&] {
             const int st = stores % kCopyStages;
-            if (mbar_wait_timed(&full[st], (stores / kCopyStages) & 1, kWaitLimitNs))
+            uint64_t *bar = &full[st];
+            uint32_t phase = (stores / kCopyStages) & 1;
+#ifdef DA_PAGE_TRACE
+            if (p.debug_stall) bar = &never, phase = 0;
+#endif
+            if (lost) {
+                mbar_wait_timed(&full[st], (stores / kCopyStages) & 1, 100000000ull);  // lands before the CTA exits
+            } else if (mbar_wait_timed(bar, phase, p.wait_limit_ns)) {
                 bulk_store(dst_of[st], ring + st * kCopyPiece, size_of[st]);
-            else
+            } else {
                 report(p.error, DA_DEV_TIMEOUT);
+                lost = true;
+                return;  // (and is waited for again, as the others)
+            }
             ++stores;
         };
         for (int64_t b = 0; b < mine; b += 32) {
@@ -542,16 +554,18 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
                 const uint8_t *f = reinterpret_cast<const uint8_t *>(__shfl_sync(0xFFFFFFFFu, (unsigned long long)from, l));
                 uint8_t *t = reinterpret_cast<uint8_t *>(__shfl_sync(0xFFFFFFFFu, (unsigned long long)into, l));
                 const uint32_t z = __shfl_sync(0xFFFFFFFFu, bytes, l);
-                if (lane == 0) {
+                if (lane == 0 && !lost) {
                     const int st = loads % kCopyStages;
                     // half of the ring loads, half stores
                     if (loads - stores >= kCopyStages / 2) store_next();
-                    if (loads >= kCopyStages) bulk_wait_read<kCopyStages / 2 - 1>();
-                    dst_of[st] = t;
-                    size_of[st] = z;
-                    mbar_arrive_expect_tx(&full[st], z);
-                    bulk_load(ring + st * kCopyPiece, f, z, &full[st]);
-                    ++loads;
+                    if (!lost) {
+                        if (loads >= kCopyStages) bulk_wait_read<kCopyStages / 2 - 1>();
+                        dst_of[st] = t;
+                        size_of[st] = z;
+                        mbar_arrive_expect_tx(&full[st], z);
+                        bulk_load(ring + st * kCopyPiece, f, z, &full[st]);
+                        ++loads;
+                    }
                 }
                 __syncwarp();
             }

@@ -276,6 +276,9 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
     __shared__ int s_listed;
     __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
     __shared__ int given_up;
+#ifdef DA_PAGE_TRACE
+    __shared__ uint64_t never;  // a barrier that nothing completes
+#endif
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -326,6 +329,9 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
             mbar_init(&empty[k], kWarps);
         }
         given_up = 0;
+#ifdef DA_PAGE_TRACE
+        mbar_init(&never, 1);
+#endif
         fence_barrier_init();
         fence_proxy_async_smem();
         for (int l = 0; l < min(slots, pieces); ++l) issue(l, l);
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
         const uint64_t begin = global_ns();
         do {  // (asleep, rather than polling: the other warps need the issue slots)
             if (mbar_try_wait_sleep(bar, phase & 1, 20000u)) return true;
-        } while (*(volatile int *)&given_up == 0 && global_ns() - begin < kWaitLimitNs);
+        } while (*(volatile int *)&given_up == 0 && global_ns() - begin < p.wait_limit_ns);
         *(volatile int *)&given_up = 1;
         if (p.error) atomicOr(p.error, DA_DEV_TIMEOUT);
         return false;
@@ -348,10 +354,11 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
         }
     };
     Turn at_load;   // thread 0: of the next load that a release lets go, load slots + this
-    int load = slots;
+    int loads = min(slots, pieces);  // issued
     const auto refill = [&] {
-        if (wait(&empty[at_load.slot], at_load.round)) issue(load, at_load.slot);
-        ++load;
+        if (*(volatile int *)&given_up != 0 || !wait(&empty[at_load.slot], at_load.round)) return;
+        issue(loads, at_load.slot);
+        ++loads;
         at_load.next(slots);
     };
     const auto release = [&](int slot) {
@@ -547,6 +554,9 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
         };
         if (tid == 0 && whole0 > 0 && groups > 0) edge(0);
         if (tid == 32 && whole1 < groups && (whole1 > 0 || whole0 == 0)) edge(groups - 1);
+#ifdef DA_PAGE_TRACE
+        if (p.debug_stall) wait(&never, 0);  // test build: a wait that runs out
+#endif
         Turn now;
         for (int k = 0; k < pieces; ++k, now.next(slots)) {
             const int g = whole0 + k * kPiece;
@@ -768,6 +778,11 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
         second(reinterpret_cast<__nv_bfloat16 *>(out_at));
     else
         second(reinterpret_cast<__half *>(out_at));
+    if constexpr (kG == 0) {
+        // where a wait has run out, the copies in flight land before the CTA exits (else all have been waited for)
+        if (__syncthreads_or(*(volatile int *)&given_up) && tid == 0)
+            for (int l = max(loads - slots, 0); l < loads; ++l) mbar_wait_timed(&full[l % slots], (l / slots) & 1, 100000000ull);
+    }
     if (p.ctas > 1) cluster_wait_all();  // this CTA's pair stays until all have read it
 }
 
