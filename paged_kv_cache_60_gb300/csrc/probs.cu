@@ -15,9 +15,9 @@
 // through a ring of 16 KB pieces in shared memory (bulk copies, issued by one thread as the
 // slots come free); what the ring holds at the first walk's end is written first, the rest
 // comes again, out of L2 for the most part: two CTAs an SM with shares of at most 256 KB.
-// Measured on 1024 rows of 131072 bf16 logits to bf16: 126 us without a history (4.3
-// TB/s; instruction issue is the limit, 19 instructions a value for both walks), 190 with
-// histories of 1024 to 8192 tokens. (Rows held in registers throughout, by clusters of eight:
+// Measured on 1024 rows of 131072 bf16 logits to bf16: 131 us without a history (4.1
+// TB/s; instruction issue is the limit, 19 instructions a value for both walks), 191 with
+// histories of 1024 to 8192 tokens, 238 with masks too. (Rows held in registers throughout, by clusters of eight:
 // 308 and 476 us; 128 warps a row, whose fixed work was more than the values'.)
 //
 // The tokens that the history, the drafts and the biases touch are few, and go their own
@@ -113,15 +113,17 @@ struct Raw {
             }
         }
     }
-    // -infinity where keep's bit is not set
+    // -infinity where keep's bit is not set. Four bits at a time become the signs of four bytes (the product's terms meet
+    // nowhere), and those the masks of the words, by a permute that repeats signs: 11 instructions for eight two-byte values.
     __device__ __forceinline__ void drop(uint32_t keep) {
+        constexpr int kHalf = kWords / 2;
+        const uint32_t signs[2] = {(keep & 0xFu) * 0x10204080u, (keep >> 4 & 0xFu) * 0x10204080u};
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
+            const int k = i % kHalf;
+            const uint32_t sel = sizeof(T) == 4 ? 0x8888u + 0x1111u * k : k ? 0xBBAAu : 0x9988u;
             uint32_t m;
-            if constexpr (sizeof(T) == 4)
-                m = keep >> i & 1 ? 0xFFFFFFFFu : 0u;
-            else
-                m = ((keep >> 2 * i & 1u) | (keep >> 2 * i & 2u) << 15) * 0xFFFFu;
+            asm("prmt.b32 %0, %1, 0, %2;" : "=r"(m) : "r"(signs[i / kHalf]), "r"(sel));
             w[i] = (w[i] & m) | (kNone & ~m);
         }
     }
@@ -237,6 +239,10 @@ struct Run {
     }
 };
 
+// Words of a share's marks, a run of eight for each thread that has one: those of a share fit.
+static_assert(kShareBytes / 2 / 32 <= 8 * kThreads, "a run of eight words per thread");
+__host__ __device__ inline int words_of(int share) { return (share * 8 + 255) / 256 * 8; }
+
 // What x becomes of a logit with a count and marks (kPrompt, kBias, kCount).
 __device__ __forceinline__ float adjusted(const ProbsParams &p, int t, float y, uint32_t c, float rep, float freq, float pres,
                                           int blo, int bhi) {
@@ -323,6 +329,19 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
         mbar_arrive_expect_tx(&full[slot], bytes);
         bulk_load(reinterpret_cast<uint8_t *>(smem_v) + (size_t)slot * kPieceBytes, in + t0 + g * 8, bytes, &full[slot]);
     };
+    // what the lists and the walks wait for, read ahead of the rest
+    const int n_hist = p.history ? min(max(p.history_lens[b], 0), p.history_cols) : 0;
+    const int blo = p.bias_starts ? min(max(p.bias_starts[b], 0), p.n_bias) : 0;
+    const int bhi = p.bias_starts ? min(max(p.bias_starts[b + 1], 0), p.n_bias) : 0;
+    const int prompt = p.prompt_lens ? p.prompt_lens[b] : 0;
+    const float T = p.temperature ? p.temperature[b] : 1.f;
+    int draft = -1;  // draft tid, where it stands before this row and the chain has not ended before it
+    if (p.drafts != nullptr && tid < j) {
+        const int32_t *drafts = p.drafts + (int64_t)b * p.K;
+        int signs = 0;
+        for (int i = 0; i < tid; ++i) signs |= drafts[i];
+        draft = signs < 0 ? -1 : drafts[tid];
+    }
     if (kG == 0 && tid == 0) {
         for (int k = 0; k < slots; ++k) {
             mbar_init(&full[k], 1);
@@ -384,17 +403,13 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
             if (k * kThreads + tid < groups) load_group(k * kThreads + tid, held[k]);
         }
     }
-    const float T = p.temperature ? p.temperature[b] : 1.f;
     const bool warm = T > 0.f;
     // (a temperature next to 0: 0 times its reciprocal stays 0; an infinite one: -infinity stays that)
     const float scale = warm ? fmaxf(fminf(__fdiv_rn(kLog2e, T), FLT_MAX), FLT_MIN) : 1.f;
 
     // ------------------------------------------------ the tokens that history, drafts and biases touch
-    const int n_hist = p.history ? min(max(p.history_lens[b], 0), p.history_cols) : 0;
-    const int blo = p.bias_starts ? min(max(p.bias_starts[b], 0), p.n_bias) : 0;
-    const int bhi = p.bias_starts ? min(max(p.bias_starts[b + 1], 0), p.n_bias) : 0;
     const bool touched = n_hist > 0 || (p.drafts != nullptr && j > 0) || bhi > blo;  // the same for the whole CTA
-    const int share_words = (p.share * 8 + 31) / 32;
+    const int share_words = words_of(p.share);
     uint32_t *mark = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(smem_v) +
                                                   (kG == 0 ? (size_t)slots * kPieceBytes : 0));  // a bit per token of the share
     // of each listed token: count and marks, then x
@@ -405,13 +420,12 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
     const auto token_at = [&](int i) -> int { return t0 + list[i] + (i >= upper ? 65536 : 0); };
     int listed = 0;
     bool crowded = false;  // more than the list has room for
-    const int prompt = p.prompt_lens ? p.prompt_lens[b] : 0;
     const int32_t *hist = p.history + (int64_t)b * p.history_cols;
-    const int32_t *drafts = p.drafts ? p.drafts + (int64_t)b * p.K : nullptr;
     if (touched) {
-        const int cap = min(p.cap, n_hist + j + bhi - blo);
-        for (int i = tid; i < share_words; i += kThreads) mark[i] = 0u;
-        for (int i = tid; i < cap; i += kThreads) value[i] = 0u;
+        const int first_bias = blo + tid < bhi ? p.bias_tokens[blo + tid] : -1;
+        const int cap = (min(p.cap, n_hist + j + bhi - blo) + 3) / 4;
+        for (int i = tid; i < share_words / 4; i += kThreads) reinterpret_cast<uint4 *>(mark)[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = tid; i < cap; i += kThreads) reinterpret_cast<uint4 *>(value)[i] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
         const int lowest = max(t0, 0), span = min(V - t0, groups * 8) - (lowest - t0);
         // f(token's place in the share) for every token of the history in [from, to)
@@ -425,27 +439,32 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
                     if ((unsigned)(tok[k] - lowest) < (unsigned)span) f(tok[k] - t0);
             }
         };
-        // and for those of the drafts (draft tid, unless the chain has ended before it) and biases
+        // and for those of the drafts and biases
         const auto drafted = [&](auto f) {
-            if (drafts == nullptr || tid >= j) return;
-            bool there = true;
-            for (int i = 0; i <= tid; ++i) there = there && drafts[i] >= 0;
-            if (there && (unsigned)(drafts[tid] - lowest) < (unsigned)span) f(drafts[tid] - t0);
+            if (draft >= 0 && (unsigned)(draft - lowest) < (unsigned)span) f(draft - t0);
         };
         const auto biased = [&](auto f) {
-            for (int i = blo + tid; i < bhi; i += kThreads)
-                if ((unsigned)(p.bias_tokens[i] - lowest) < (unsigned)span) f(p.bias_tokens[i] - t0);
+            for (int i = blo + tid; i < bhi; i += kThreads) {
+                const int tok = i == blo + tid ? first_bias : p.bias_tokens[i];
+                if ((unsigned)(tok - lowest) < (unsigned)span) f(tok - t0);
+            }
         };
         const auto touch = [&](int i) { atomicOr(mark + i / 32, 1u << (i & 31)); };
         each(0, n_hist, touch);
         drafted(touch);
         biased(touch);
         __syncthreads();
-        // prefix sum over the words: a run of them per thread
-        const int per = (share_words + kThreads - 1) / kThreads;
+        // prefix sum over the words, a run of eight per thread
+        uint32_t m[8];
         int mine = 0;
-        for (int k = 0; k < per; ++k)
-            if (tid * per + k < share_words) mine += __popc(mark[tid * per + k]);
+        const bool has = tid * 8 < share_words;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint4 v = has ? reinterpret_cast<const uint4 *>(mark)[tid * 2 + k] : make_uint4(0u, 0u, 0u, 0u);
+            m[4 * k] = v.x, m[4 * k + 1] = v.y, m[4 * k + 2] = v.z, m[4 * k + 3] = v.w;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mine += __popc(m[k]);
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -455,13 +474,17 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
         if (lane == 31) warp_sum[warp] = incl;
         __syncthreads();
         int at = incl - mine;
-        for (int w = 0; w < warp; ++w) at += warp_sum[w];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) at += w < warp ? warp_sum[w] : 0;
         if (tid == kThreads - 1) s_listed = at + mine;
-        for (int k = 0; k < per; ++k)
-            if (tid * per + k < share_words) {
-                place[tid * per + k] = (uint16_t)at;
-                at += __popc(mark[tid * per + k]);
-            }
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+            const int second = at + __popc(m[k]);
+            const uint32_t both = (uint32_t)at | (uint32_t)second << 16;
+            at = second + __popc(m[k + 1]);
+            m[k / 2] = both;  // (read by now)
+        }
+        if (has) reinterpret_cast<uint4 *>(place)[tid] = make_uint4(m[0], m[1], m[2], m[3]);
         __syncthreads();
         listed = s_listed;
         if (share_words > 65536 / 32) upper = place[65536 / 32];
@@ -523,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
                 run.sum += sum8(e);
             }
         } else {
+            if (largest_of(r) < run.m) return;  // (not where one is NaN)
 #pragma unroll
             for (int k = 0; k < kN; ++k) {
                 float v[8];
@@ -673,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
     const float from = nothing ? 0.f : best.x, off = nothing ? -INFINITY : -log2f(best.y);
     const bool bad = warm && !nothing && !(best.y < INFINITY);  // (largest NaN or infinite)
     const Exps exps{from, scale, off};
-    const bool ordinary = warm && !bits && !bad && !nothing && !crowded && vec;
+    const bool ordinary = warm && !bad && !nothing && !crowded && vec;
     const auto second = [&](auto *row) {  // of the probabilities, as what they are
         const auto probabilities = [&](int g, const Raw<TI> &r, float (&v)[8]) {
             if (warm) {
@@ -729,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
                 auto *at = row + t0 + (int64_t)(g + tid) * 8;
                 uint32_t keep[kPer];
                 if (bits && warm) keeps(g + tid, false, keep);
-                const auto part = [&](auto all, auto plain) {  // (all: a whole piece; plain: nothing but the formula)
+                const auto part = [&](auto all, auto plain, auto masked) {  // (all: a whole piece; plain: nothing but the formula)
                     Raw<TI> r[kPer];
                     if (plain || warm) {
                         if (tid == 0 && k > 0 && k - 1 < pieces - left) refill();
@@ -741,21 +765,24 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
                         const int gi = g + i * kThreads + tid;
                         if (!all && gi >= whole1) continue;
                         float v[8];
+                        if (masked && warm && keep[i] != 0xFFu) r[i].drop(keep[i]);
                         if (plain) {
                             r[i].widen(v);
                             exps.of(v);
                             store8(at + i * kThreads * 8, v);
                             continue;
                         }
-                        if (bits && warm && keep[i] != 0xFFu) r[i].drop(keep[i]);
                         probabilities(gi, r[i], v);
                         store_group(row, t0 + gi * 8, V, vec, written(gi), v);
                     }
                 };
-                if (g + kPiece <= whole1 && ordinary)
-                    part(std::true_type(), std::true_type());
+                const bool whole = g + kPiece <= whole1 && ordinary;
+                if (whole && !bits)
+                    part(std::true_type(), std::true_type(), std::false_type());
+                else if (whole)
+                    part(std::true_type(), std::true_type(), std::true_type());
                 else
-                    part(std::false_type(), std::false_type());
+                    part(std::false_type(), std::false_type(), bits != nullptr);
                 if (warm && k < pieces - left) release(now.slot);
             }
         }
@@ -831,7 +858,7 @@ cudaError_t launch_types(ProbsParams p, int num_sms, cudaStream_t stream, bool p
         const int64_t tokens = (int64_t)p.share * 8;
         p.cap = (int)((touches < tokens ? touches : tokens) + 3) / 4 * 4;
         if (touches == 0) return 0;
-        return ((size_t)p.share * 8 / 32 + 1) * 6 + (size_t)p.cap * 6 + 16;
+        return ((size_t)words_of(p.share) * 6 + (size_t)p.cap * 6 + 15) / 16 * 16;
     };
     // As few CTAs as hold a row, with two slots beside what the listed tokens need, twice on an SM; where that leaves SMs
     // idle, more, down to eight values a thread: two or four as long as all have a place at once (64 rows of 128259: 18.0 us
