@@ -104,7 +104,7 @@ typedef struct {
 #define DA_ERR_SPLITS         -5   /* splits < 0 or too large */
 #define DA_ERR_META_SIZE      -6   /* sched_meta buffer smaller than decode_attn_sched_meta_bytes */
 #define DA_ERR_CUDA           -7   /* a CUDA runtime/driver call failed */
-#define DA_ERR_SCALE          -8   /* FP8 format without k_scale / v_scale */
+#define DA_ERR_SCALE          -8   /* a format of 8 bits without k_scale / v_scale */
 
 /* Device error bits (sched_meta error word). */
 #define DA_DEV_BAD_PAGE        1   /* block_table entry outside [0, num_pages): page skipped */
@@ -170,7 +170,7 @@ int decode_attn_sched_meta(const da_desc *desc, const int32_t *cache_seqlens,
 /*
  * Decode attention forward. Launches the split-KV kernel and the LSE combine
  * kernel (chained with programmatic dependent launch) on `stream`. With a
- * fixed split count of 2-8 (desc->splits) and the bf16 or e4m3 formats, the
+ * fixed split count of 2-8 (desc->splits) and all formats but the 656-byte one, the
  * splits of a (request, KV head) run as one thread-block cluster and merge
  * their partials through distributed shared memory: the split-KV kernel then
  * writes out and lse itself and no combine kernel is launched.

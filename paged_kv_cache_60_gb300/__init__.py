@@ -15,8 +15,11 @@ import raises.
 
 Around the step: append_kv, append_block and rope_append write new tokens, verify_drafts
 accepts a chain of drafts, accum_weights gathers the attention weight of cached
-tokens and evict keeps the heaviest. All but append_kv check every
-tensor's dtype, shape, strides and device and raise DecodeAttnError.
+tokens and evict keeps the heaviest. Around the cache: fork_pages, reserve_pages,
+free_pages, compact_pages and copy_pages keep pages that rows share. token_probs
+turns logits into the probabilities that verify_drafts takes. All of these but
+append_kv check every tensor's dtype, shape, strides and device and raise
+DecodeAttnError.
 """
 import ctypes
 import os

@@ -1134,7 +1134,7 @@ const char *decode_attn_strerror(int code) {
         case DA_ERR_SPLITS: return "splits out of range";
         case DA_ERR_META_SIZE: return "sched_meta buffer too small";
         case DA_ERR_CUDA: return "a CUDA call failed";
-        case DA_ERR_SCALE: return "FP8 KV needs k_scale and v_scale";
+        case DA_ERR_SCALE: return "a KV format of 8 bits needs k_scale and v_scale";
         default: return "unknown error code";
     }
 }

@@ -38,7 +38,6 @@ constexpr int kFewRows = kPlanThreads, kSlots = 2 * kFewRows;  // requests with 
 constexpr int kForkThreads = 256, kForkColumns = 1024;
 constexpr int kCopyThreads = 64, kCopyPiece = 8 << 10, kCopyStages = 8;
 
-
 __device__ __forceinline__ void report(int32_t *error, int bits) {
     if (error) atomicOr(error, bits);
 }
@@ -485,7 +484,7 @@ __global__ void __launch_bounds__(kForkThreads) remap_kernel(const __grid_consta
 // copies, both ways asynchronous: one warp looks 32 pieces up at a time, its first lane issues their
 // loads and, as they arrive, their stores, through a ring of stages. Another warp copies the pages'
 // scales and weights (4-byte values). Three CTAs an SM with eight stages each: 25239 pages of 32 KB
-// in 247 us, 6.7 TB/s or 0.99 of the measured copy rate (pieces of 16 KB, six stages, two CTAs: 274; 16
+// in 247 to 257 us, 6.4 to 6.7 TB/s or 0.95 to 0.99 of the measured copy rate (pieces of 16 KB, six stages, two CTAs: 274; 16
 // bytes a thread and load, four in flight, 2048 threads an SM: 288).
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyPagesParams p) {
     extern __shared__ uint4 ring_v[];
