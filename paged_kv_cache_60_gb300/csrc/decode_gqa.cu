@@ -38,7 +38,7 @@
 //    handed out by shuffles; a warp loads those of its next chunk, and the page ids of
 //    the one after, while it works on this one. (Brought by the producer warp with
 //    4-byte cp.async, they made that warp's loop the limit: 636 us per call of 64 x
-//    32768 tokens.) int8 codes become f16 by a byte permute and one subtraction (0x6400 | c + 128 is
+//    32768 tokens of 4 heads; now 340, 0.93 of the measured copy rate.) int8 codes become f16 by a byte permute and one subtraction (0x6400 | c + 128 is
 //    1024 + 128 + c), exactly.
 //  * several query tokens per request (linear speculative-decoding
 //    verification, XQA page, section "投机解码:XQA 的第二个工作负载"): the
