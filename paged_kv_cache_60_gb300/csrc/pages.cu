@@ -64,39 +64,42 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constan
     pdl_wait();
     pdl_launch_dependents();
     const int b = blockIdx.x / tiles, col0 = blockIdx.x % tiles * kForkColumns, tid = threadIdx.x;
-    int children = 0;
-    for (int i = 0; i < p.B; i += kForkThreads)
-        children += __syncthreads_count(i + tid < p.B && p.parents[i + tid] == b);
     const auto held_of = [&](int row) { return min(max(p.held_in[row], 0), p.max_pages); };
     const auto used_of = [&](int row, int held) {
         return (int)min(((int64_t)max(p.seqlens_in[row], 0) + p.page_size - 1) / p.page_size, (int64_t)held);
     };
-    const int held = held_of(b), used = used_of(b, held);
-    const int32_t *old = p.table_in + (int64_t)b * p.max_pages;
-#pragma unroll
-    for (int k = 0; k < kForkColumns / kForkThreads; ++k) {
-        const int j = col0 + k * kForkThreads + tid;
-        if (j >= held) continue;
-        const int delta = (j < used ? children : 0) - 1;
-        if (delta == 0) continue;
-        const int page = old[j];
-        if (page_ok(page, p.num_pages))
-            atomicAdd(p.refs + page, delta);
-        else
-            report(p.error, DA_DEV_BAD_PAGE);
-    }
+    // both rows are looked up before anything is written: two chains of loads under way at once
     const int parent = p.parents[b];
     const bool has = parent >= 0 && parent < p.B;
+    const int held = held_of(b), used = used_of(b, held);
     const int n = has ? used_of(parent, held_of(parent)) : 0;
+    const int32_t *old = p.table_in + (int64_t)b * p.max_pages;
     const int32_t *from = p.table_in + (int64_t)(has ? parent : 0) * p.max_pages;
     int32_t *to = p.table + (int64_t)b * p.max_pages;
+    int mine[kForkColumns / kForkThreads], taken[kForkColumns / kForkThreads];
 #pragma unroll
     for (int k = 0; k < kForkColumns / kForkThreads; ++k) {
         const int j = col0 + k * kForkThreads + tid;
-        if (j >= n) continue;
-        const int page = from[j];
-        if (!page_ok(page, p.num_pages)) report(p.error, DA_DEV_BAD_PAGE);
-        to[j] = page;
+        mine[k] = j < held ? old[j] : -1;
+        taken[k] = j < n ? from[j] : -1;
+    }
+    int children = 0;
+    for (int i = 0; i < p.B; i += kForkThreads)
+        children += __syncthreads_count(i + tid < p.B && p.parents[i + tid] == b);
+#pragma unroll
+    for (int k = 0; k < kForkColumns / kForkThreads; ++k) {
+        const int j = col0 + k * kForkThreads + tid;
+        const int delta = (j < used ? children : 0) - 1;
+        if (j < held && delta != 0) {
+            if (page_ok(mine[k], p.num_pages))
+                atomicAdd(p.refs + mine[k], delta);
+            else
+                report(p.error, DA_DEV_BAD_PAGE);
+        }
+        if (j < n) {
+            if (!page_ok(taken[k], p.num_pages)) report(p.error, DA_DEV_BAD_PAGE);
+            to[j] = taken[k];
+        }
     }
     if (col0 == 0 && tid == 0) {
         const int L = has ? p.seqlens_in[parent] : 0;
