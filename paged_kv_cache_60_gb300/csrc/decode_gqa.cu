@@ -101,12 +101,16 @@ struct GqaCfg {
     static constexpr int MT = D / 16;
     static constexpr int KS = D / 16;
     static constexpr int UPAD = D + 4;
+    // a segment's end: query tokens of a warp whose states are merged in one pass (as many as there is scratch for: rows of
+    // 8 bits leave room for two), and so rows of a pass
+    static constexpr int PJ = FP8 ? NQ : 1, ROWS = WPC * PJ * G;
     static constexpr int OFF_U = NS * STAGE;
-    static constexpr int OFF_M = OFF_U + NCW * G * UPAD * 4;
-    static constexpr int OFF_L = OFF_M + NCW * G * 4;
-    static constexpr int OFF_W = OFF_L + NCW * G * 4;
-    static constexpr int OFF_FIN = OFF_W + NCW * G * 4;
-    static constexpr int OFF_BAR = (OFF_FIN + 4 * G * 4 + 7) / 8 * 8;
+    static constexpr int OFF_M = OFF_U + NCW * PJ * G * UPAD * 4;
+    static constexpr int OFF_L = OFF_M + NCW * PJ * G * 4;
+    static constexpr int OFF_W = OFF_L + NCW * PJ * G * 4;
+    static constexpr int OFF_FIN = OFF_W + NCW * PJ * G * 4;
+    static constexpr int OFF_BAR = (OFF_FIN + 2 * ROWS * 4 + 7) / 8 * 8;
+    static_assert(ROWS <= NCW * 32, "a thread per row");
     static constexpr int OFF_FLAG = OFF_BAR + 2 * NS * 8;
     static constexpr int SMEM = OFF_FLAG + 16 + 1024;  // + alignment slack
     static constexpr int MIN_BLOCKS = ((D == 64 && !FP8 && NQ == 1 && WPC == 1) || TWO_PER_SM) ? 2 : 1;
@@ -722,101 +726,113 @@ __global__ void __launch_bounds__(GqaCfg<D, KV, NQ, WPC>::THREADS, GqaCfg<D, KV,
         }
 
         // ---------------------------------------------------------- merge warps
-        // one pass per query token of the request (the scratch holds one);
-        // token jj = ow * NQ + jl lives in tile jl of the warps with warp % WPC == ow
+        // token jj = ow * NQ + jl lives in tile jl of the warps with warp % WPC == ow; a pass merges PJ tiles of all warps
+        // (one token a pass before, three barriers each)
         const bool direct = sg.ns == 1;
         const int split = sg.so + ss;
         const bool split_ok = direct || (split >= 0 && split < p.meta.max_splits);
         const size_t rows = (size_t)p.s_q * p.H_q;  // output rows per request: [s_q][H_q]
-        int pass = 0;
 #pragma unroll
-        for (int jl = 0; jl < NQ; ++jl) {
+        for (int j0 = 0; j0 < NQ; j0 += C::PJ) {
+            if (j0 > 0) {
+                if (j0 >= p.s_q) break;
+                named_barrier_sync(1, C::NCW * 32);  // the previous pass has read the scratch
+            }
+            // row of the pass -> its warps' first, its tile within the pass, its token
+            auto first_of = [](int row) -> int { return WPC == 1 ? 0 : row / (C::PJ * C::G); };
+            auto tile_of = [](int row) -> int { return C::PJ == 1 ? 0 : row / C::G % C::PJ; };
+            auto token_of = [&](int row) -> int { return NQ * WPC == 1 ? 0 : first_of(row) * NQ + j0 + tile_of(row); };
+            constexpr int step = WPC * C::PJ * C::G;  // to the row's next warp
+            auto head_of = [](int row) -> int { return C::ROWS == C::G ? row : row % C::G; };
+            auto there = [&](int token) -> bool { return NQ * WPC == 1 || token < p.s_q; };
 #pragma unroll
-            for (int ow = 0; ow < WPC; ++ow) {
-                const int jj = ow * NQ + jl;
-                if (jj >= p.s_q) continue;
-                if (pass++ > 0) named_barrier_sync(1, C::NCW * 32);  // the previous pass has read the scratch
-                if (warp % WPC == ow) {
-                    const float lj0 = warp_sum_xor_4_8_16(l0[jl]);
-                    const float lj1 = warp_sum_xor_4_8_16(l1[jl]);
-                    if (lane < 4) {
-                        sm_m[warp * C::G + 2 * c4] = m0[jl];
-                        sm_m[warp * C::G + 2 * c4 + 1] = m1[jl];
-                        sm_l[warp * C::G + 2 * c4] = lj0;
-                        sm_l[warp * C::G + 2 * c4 + 1] = lj1;
-                    }
-                    float *uw = sm_u + (size_t)warp * C::G * C::UPAD;
+            for (int jt = 0; jt < C::PJ; ++jt) {
+                const int jl = j0 + jt;
+                if (!there(jo + jl)) continue;
+                const float lj0 = warp_sum_xor_4_8_16(l0[jl]);
+                const float lj1 = warp_sum_xor_4_8_16(l1[jl]);
+                const int slot = (warp * C::PJ + jt) * C::G;
+                if (lane < 4) {
+                    sm_m[slot + 2 * c4] = m0[jl];
+                    sm_m[slot + 2 * c4 + 1] = m1[jl];
+                    sm_l[slot + 2 * c4] = lj0;
+                    sm_l[slot + 2 * c4 + 1] = lj1;
+                }
+                float *uw = sm_u + (size_t)slot * C::UPAD;
 #pragma unroll
-                    for (int mt = 0; mt < C::MT; ++mt) {
-                        // accumulator rows -> head-dim index
-                        const int dA = FP8 ? mt * 16 + 2 * r8 : mt * 16 + r8;
-                        const int dB = FP8 ? dA + 1 : dA + 8;
-                        uw[(2 * c4) * C::UPAD + dA] = acc[mt][jl][0];
-                        uw[(2 * c4 + 1) * C::UPAD + dA] = acc[mt][jl][1];
-                        uw[(2 * c4) * C::UPAD + dB] = acc[mt][jl][2];
-                        uw[(2 * c4 + 1) * C::UPAD + dB] = acc[mt][jl][3];
-                    }
+                for (int mt = 0; mt < C::MT; ++mt) {
+                    // accumulator rows -> head-dim index
+                    const int dA = FP8 ? mt * 16 + 2 * r8 : mt * 16 + r8;
+                    const int dB = FP8 ? dA + 1 : dA + 8;
+                    uw[(2 * c4) * C::UPAD + dA] = acc[mt][jl][0];
+                    uw[(2 * c4 + 1) * C::UPAD + dA] = acc[mt][jl][1];
+                    uw[(2 * c4) * C::UPAD + dB] = acc[mt][jl][2];
+                    uw[(2 * c4 + 1) * C::UPAD + dB] = acc[mt][jl][3];
                 }
-                named_barrier_sync(1, C::NCW * 32);
-                if (ctid < C::G) {
-                    const int g = ctid;
-                    float M = -INFINITY;
-                    for (int w = ow; w < C::NCW; w += WPC) M = fmaxf(M, sm_m[w * C::G + g]);
-                    float Ls = 0.f;
-                    for (int w = ow; w < C::NCW; w += WPC) {
-                        const float mw = sm_m[w * C::G + g];
-                        const float wt = (mw == -INFINITY) ? 0.f : ex2(mw - M);
-                        sm_w[w * C::G + g] = wt;
-                        Ls += wt * sm_l[w * C::G + g];
-                    }
-                    // lse over the tokens; a request with a single split gets its
-                    // attention sink here (the combine adds it to the others)
-                    // (a NaN sum -- a NaN code in a row -- stays NaN rather than reading as empty)
-                    float lse_v = !(Ls <= 0.f) ? (M + log2f(Ls)) * kLn2 : -INFINITY, fac = 1.f;
-                    if (direct && p.sinks != nullptr) {
-                        const float tot = log_add_exp(lse_v, p.sinks[h * C::G + g]);
-                        fac = (lse_v == -INFINITY) ? 0.f : expf(lse_v - tot);
-                        lse_v = tot;
-                    }
-                    sm_fin[g] = !(Ls <= 0.f) ? vscale * fac / Ls : 0.f;  // out = u * this
-                    sm_fin[2 * C::G + g] = lse_v;
+            }
+            named_barrier_sync(1, C::NCW * 32);
+            if (ctid < C::ROWS && there(token_of(ctid))) {
+                const int g = head_of(ctid), at = (first_of(ctid) * C::PJ + tile_of(ctid)) * C::G + g;
+                float M = -INFINITY;
+                for (int k = 0; k < C::NG; ++k) M = fmaxf(M, sm_m[at + k * step]);
+                float Ls = 0.f;
+                for (int k = 0; k < C::NG; ++k) {
+                    const float mw = sm_m[at + k * step];
+                    const float wt = (mw == -INFINITY) ? 0.f : ex2(mw - M);
+                    sm_w[at + k * step] = wt;
+                    Ls += wt * sm_l[at + k * step];
                 }
-                named_barrier_sync(1, C::NCW * 32);
-                const size_t row0 = (size_t)jj * p.H_q + (size_t)h * C::G;  // row of head g = row0 + g
-                // four consecutive dims per thread and step
-                for (int idx = ctid; idx < C::G * (D / 4); idx += C::NCW * 32) {
-                    const int g = idx / (D / 4), d = (idx % (D / 4)) * 4;
-                    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+                // lse over the tokens; a request with a single split gets its
+                // attention sink here (the combine adds it to the others)
+                // (a NaN sum -- a NaN code in a row -- stays NaN rather than reading as empty)
+                float lse_v = !(Ls <= 0.f) ? (M + log2f(Ls)) * kLn2 : -INFINITY, fac = 1.f;
+                if (direct && p.sinks != nullptr) {
+                    const float tot = log_add_exp(lse_v, p.sinks[h * C::G + g]);
+                    fac = (lse_v == -INFINITY) ? 0.f : expf(lse_v - tot);
+                    lse_v = tot;
+                }
+                sm_fin[ctid] = !(Ls <= 0.f) ? vscale * fac / Ls : 0.f;  // out = u * this
+                sm_fin[C::ROWS + ctid] = lse_v;
+            }
+            named_barrier_sync(1, C::NCW * 32);
+            // four consecutive dims per thread and step
+            for (int idx = ctid; idx < C::ROWS * (D / 4); idx += C::NCW * 32) {
+                const int row = idx / (D / 4), d = (idx % (D / 4)) * 4;
+                const int jj = token_of(row), g = head_of(row);
+                if (!there(jj)) continue;
+                const int at = (first_of(row) * C::PJ + tile_of(row)) * C::G + g;
+                const float *w0 = sm_w + at, *u0 = sm_u + (size_t)at * C::UPAD + d;
+                float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int w = ow; w < C::NCW; w += WPC) {
-                        const float wt = sm_w[w * C::G + g];
-                        const float4 v = *reinterpret_cast<const float4 *>(sm_u + ((size_t)w * C::G + g) * C::UPAD + d);
-                        u.x += wt * v.x;
-                        u.y += wt * v.y;
-                        u.z += wt * v.z;
-                        u.w += wt * v.w;
-                    }
-                    const float f = sm_fin[g];
-                    const float4 o = make_float4(u.x * f, u.y * f, u.z * f, u.w * f);
-                    if (direct)
-                        *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) +
-                                                   ((size_t)sb * rows + row0 + g) * D + d) =
-                            make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-                    else if (p.cluster_merge)
-                        *reinterpret_cast<float4 *>(xo + (size_t)(jj * C::G + g) * D + d) = o;
-                    else if (split_ok)
-                        *reinterpret_cast<float4 *>(p.meta.o_part + ((size_t)split * rows + row0 + g) * D + d) = o;
+                for (int k = 0; k < C::NG; ++k) {
+                    const float wt = w0[k * step];
+                    const float4 v = *reinterpret_cast<const float4 *>(u0 + (size_t)k * step * C::UPAD);
+                    u.x += wt * v.x;
+                    u.y += wt * v.y;
+                    u.z += wt * v.z;
+                    u.w += wt * v.w;
                 }
-                if (ctid < C::G) {
-                    const int g = ctid;
-                    const float v = sm_fin[2 * C::G + g];
-                    if (direct)
-                        p.lse[(size_t)sb * rows + row0 + g] = v;
-                    else if (p.cluster_merge)
-                        xl[jj * C::G + g] = v;
-                    else if (split_ok)
-                        p.meta.lse_part[(size_t)split * rows + row0 + g] = v;
-                }
+                const float f = sm_fin[row];
+                const float4 o = make_float4(u.x * f, u.y * f, u.z * f, u.w * f);
+                const size_t out_row = (size_t)jj * p.H_q + (size_t)h * C::G + g;
+                if (direct)
+                    *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + ((size_t)sb * rows + out_row) * D +
+                                               d) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+                else if (p.cluster_merge)
+                    *reinterpret_cast<float4 *>(xo + (size_t)(jj * C::G + g) * D + d) = o;
+                else if (split_ok)
+                    *reinterpret_cast<float4 *>(p.meta.o_part + ((size_t)split * rows + out_row) * D + d) = o;
+            }
+            if (ctid < C::ROWS && there(token_of(ctid))) {
+                const int jj = token_of(ctid), g = head_of(ctid);
+                const size_t out_row = (size_t)jj * p.H_q + (size_t)h * C::G + g;
+                const float v = sm_fin[C::ROWS + ctid];
+                if (direct)
+                    p.lse[(size_t)sb * rows + out_row] = v;
+                else if (p.cluster_merge)
+                    xl[jj * C::G + g] = v;
+                else if (split_ok)
+                    p.meta.lse_part[(size_t)split * rows + out_row] = v;
             }
         }
         if (named_barrier_or(1, C::NCW * 32, *abort_flag != 0)) break;
