@@ -19,7 +19,7 @@ tokens and evict keeps the heaviest. Around the cache: fork_pages, reserve_pages
 free_pages, compact_pages and copy_pages keep pages that rows share. token_probs
 turns logits into the probabilities that verify_drafts takes. All of these but
 append_kv check every tensor's dtype, shape, strides and device and raise
-DecodeAttnError.
+DecodeAttnError; fwd and fwd_static_scratch do so for the scales of the block formats.
 """
 import ctypes
 import os
@@ -200,9 +200,25 @@ def sched_meta(desc: Desc, cache_seqlens, meta, stream=None, lib=None):
                                                  meta.numel() * meta.element_size(), _stream(stream)))
 
 
+def _block_scales(desc, k_scale, v_scale):
+    """Refuses scales that are not the block formats' (the per-head format's are far shorter: the kernel would read past
+    their end). None is left to the library's own check."""
+    import torch
+    dev, shape = _device(), (desc.num_pages, desc.H_kv, desc.page_size // 16)
+    n = shape[0] * shape[1] * shape[2]
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None and not (t.dtype is torch.float32 and t.get_device() == dev and t.is_contiguous() and t.numel() == n):
+            raise DecodeAttnError(f"{name}: want a contiguous torch.float32 tensor of shape {shape} on the current CUDA device, "
+                                  f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+
+
 def fwd(desc: Desc, q, k_pool, v_pool, k_scale, v_scale, block_table, cache_seqlens, meta, out, lse,
         stream=None, use_pdl=True, main_begin=None, main_end=None, sinks=None, indices=None, lib=None):
+    """Decode attention; see decode_attn_fwd in the header. Of the tensors only the scales of the block formats
+    are checked here."""
     lib = lib or load_library()
+    if desc.kv_dtype in (KV_FP8_BLOCK, KV_INT8_BLOCK):
+        _block_scales(desc, k_scale, v_scale)
     args = (ctypes.byref(desc), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
             _ptr(block_table), _ptr(cache_seqlens), _ptr(meta), meta.numel() * meta.element_size(),
             _ptr(out), _ptr(lse))
@@ -228,6 +244,8 @@ def fwd_static_scratch(desc: Desc, q, k_pool, v_pool, k_scale, v_scale, block_ta
     (fixed 16 MiB library buffer, first call per device before any capture,
     overlapping calls race)."""
     lib = load_library()
+    if desc.kv_dtype in (KV_FP8_BLOCK, KV_INT8_BLOCK):
+        _block_scales(desc, k_scale, v_scale)
     f = lib.decode_attn_fwd_static_scratch
     if f.restype is not ctypes.c_int:
         P = ctypes.c_void_p
