@@ -247,7 +247,7 @@ def fwd_static_scratch(desc: Desc, q, k_pool, v_pool, k_scale, v_scale, block_ta
     if desc.kv_dtype in (KV_FP8_BLOCK, KV_INT8_BLOCK):
         _block_scales(desc, k_scale, v_scale)
     f = lib.decode_attn_fwd_static_scratch
-    if f.restype is not ctypes.c_int:
+    if not f.argtypes:       # (without them a stream's handle would be cut to 32 bits)
         P = ctypes.c_void_p
         f.argtypes = [ctypes.POINTER(Desc), P, P, P, P, P, P, P, P, P, P]
         f.restype = ctypes.c_int
