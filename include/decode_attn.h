@@ -708,6 +708,12 @@ int decode_attn_debug_wait_limit(uint64_t ns);
  * completes: the wait runs out, DA_DEV_TIMEOUT is set and the CTAs return.
  * 0 turns it off. No counterpart on the pages. Always returns DA_OK. */
 int decode_attn_debug_stall(int32_t on);
+
+/* Test build only. The page operators and the token probabilities launch
+ * clusters of at most `ctas` CTAs (8 or 16; else DA_ERR_DIMS), as they do on a
+ * device that has no room for 16. 16 restores the product's choice. No
+ * counterpart on the pages. */
+int decode_attn_debug_max_cluster(int32_t ctas);
 #endif
 
 #ifdef __cplusplus

@@ -166,6 +166,8 @@ int check_pool_desc(const da_desc *d, int64_t *row_len) {
     }
 }
 
+int32_t g_max_cluster = 16;  // of the page operators and the token probabilities (lowered in the test build)
+
 // The sizes that the page operators read (those of the tables and counts)
 int check_pages(const da_desc *d) {
     if (!d) return DA_ERR_NULL;
@@ -186,6 +188,7 @@ PagesParams pages_params(const da_desc *d, int32_t *device_error) {
     p.page_size = d->page_size;
     p.max_pages = d->max_pages_per_seq;
     p.num_pages = d->num_pages;
+    p.max_cluster = g_max_cluster;
     return p;
 }
 
@@ -1067,6 +1070,7 @@ int decode_attn_token_probs(int32_t B, int32_t n_draft, int32_t vocab, int32_t l
     p.history_cols = r.history ? r.history_cols : 0;
     p.wait_limit_ns = g_wait_limit_ns ? g_wait_limit_ns : kWaitLimitNs;
     p.debug_stall = g_debug_stall;
+    p.max_cluster = g_max_cluster;
     p.n_bias = r.n_bias;
     p.B = B;
     p.K = n_draft;
@@ -1167,6 +1171,13 @@ extern "C" int decode_attn_debug_wait_limit(uint64_t ns) {
 // that wait runs out.
 extern "C" int decode_attn_debug_stall(int32_t on) {
     g_debug_stall = on;
+    return DA_OK;
+}
+
+// Test build only: clusters of `ctas` (8 or 16) at most in the page operators and the token probabilities.
+extern "C" int decode_attn_debug_max_cluster(int32_t ctas) {
+    if (ctas != 8 && ctas != 16) return DA_ERR_DIMS;
+    g_max_cluster = ctas;
     return DA_OK;
 }
 #endif

@@ -255,6 +255,7 @@ struct PagesParams {
     int32_t *error;                // may be null
     int32_t B, s_q, page_size, max_pages, num_pages;
     int32_t ctas, share_words;     // of a planning kernel's cluster; words of 32 pages to a CTA
+    int32_t max_cluster;           // CTAs of a cluster at most: 16 (the test build may lower it to 8)
 };
 struct CopyPagesParams {
     const int32_t *copies;         // [max_copies] pairs; a negative source: none
@@ -292,6 +293,7 @@ struct ProbsParams {
     uint64_t wait_limit_ns;
     int32_t debug_stall;           // test build only: the walkers first wait on a barrier nothing completes
     int32_t ctas, share;           // CTAs of a row; groups of eight values to a CTA
+    int32_t max_cluster;           // CTAs of a cluster at most: 16 (the test build may lower it to 8)
 };
 
 // Verification of drafted tokens (verify.cu).

@@ -652,7 +652,7 @@ cudaError_t launch(void (*kern)(Args...), int64_t grid, int threads, size_t smem
 cudaError_t plan(const void *kern, PagesParams &p) {
     int c = 1;
     while (c < 16 && (int64_t)c * kPagesPerCta < p.num_pages) c *= 2;
-    if (c == 16 && !wide_clusters()) c = 8;
+    if (c == 16 && (p.max_cluster < 16 || !wide_clusters())) c = 8;
     p.ctas = c;
     const int64_t words = ((int64_t)p.num_pages + 31) / 32;
     p.share_words = (int)((words + c - 1) / c);

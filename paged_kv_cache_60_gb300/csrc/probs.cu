@@ -36,6 +36,7 @@
 // by value.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cstdint>
 #include <type_traits>
@@ -49,7 +50,6 @@ namespace da {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 16;
 constexpr int kShareBytes = 256 << 10;          // of a CTA at most: 2^17 values
 // groups of a thread in a piece of a share that streams: 16 KB a piece
 template <typename T>
@@ -813,8 +813,41 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
     if (p.ctas > 1) cluster_wait_all();  // this CTA's pair stays until all have read it
 }
 
+// Whether the current device can hold a cluster of 16 CTAs of this kernel, asked once per device for CTAs of which two fit an SM and
+// for larger ones (by the most shared memory that such a one takes). cfg: of the launch, attr[0] its cluster.
 template <typename TI, int kG>
-cudaError_t launch_one(const ProbsParams &p, size_t smem, cudaStream_t stream, bool pdl) {
+bool wide_clusters(cudaLaunchConfig_t cfg, cudaLaunchAttribute *attr) {
+    static std::atomic<int> known[64][2];  // 1: no, 2: yes
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    const bool large = cfg.dynamicSmemBytes > (size_t)kSmemTwo;
+    int k = known[dev][large].load(std::memory_order_relaxed);
+    if (k == 0) {
+        cfg.gridDim = dim3(attr[0].val.clusterDim.x);
+        cfg.dynamicSmemBytes = large ? kSmemMax : kSmemTwo;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        const bool ok = cudaOccupancyMaxActiveClusters(&n, probs_kernel<TI, kG>, &cfg) == cudaSuccess && n >= 1;
+        if (!ok) cudaGetLastError();
+        k = ok ? 2 : 1;
+        known[dev][large].store(k, std::memory_order_relaxed);
+    }
+    return k == 2;
+}
+
+// How a row is divided: its CTAs, groups to each, the list's room, slots of the ring, shared memory of a CTA.
+struct Split {
+    int ctas, share, cap, slots;
+    size_t smem;
+};
+
+template <typename TI, int kG>
+cudaError_t launch_one(ProbsParams p, const Split &how, cudaStream_t stream, bool pdl, bool *no_room) {
+    p.ctas = how.ctas;
+    p.share = how.share;
+    p.cap = how.cap;
+    p.slots = how.slots;
     const auto kern = probs_kernel<TI, kG>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e == cudaSuccess && p.ctas > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -824,7 +857,7 @@ cudaError_t launch_one(const ProbsParams &p, size_t smem, cudaStream_t stream, b
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = how.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     int n = 0;
@@ -832,6 +865,10 @@ cudaError_t launch_one(const ProbsParams &p, size_t smem, cudaStream_t stream, b
         attr[n].id = cudaLaunchAttributeClusterDimension;
         attr[n].val.clusterDim = {(unsigned)p.ctas, 1, 1};
         ++n;
+    }
+    if (p.ctas > 8 && !wide_clusters<TI, kG>(cfg, attr)) {
+        *no_room = true;
+        return cudaSuccess;
     }
     if (pdl) {
         attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -843,46 +880,63 @@ cudaError_t launch_one(const ProbsParams &p, size_t smem, cudaStream_t stream, b
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// rows of [0, V) over clusters of at most `most` CTAs
 template <typename TI>
-cudaError_t launch_types(ProbsParams p, int num_sms, cudaStream_t stream, bool pdl) {
+Split split_rows(const ProbsParams &p, int num_sms, int most) {
     // groups of the longest row: the first of them may start before it
     const int head = p.logits_stride % 8 == 0 ? (int)(reinterpret_cast<uintptr_t>(p.logits) / sizeof(TI) & 7) : 7;
     const int groups = (p.V + head + 7) / 8;
     const int64_t rows = (int64_t)p.B * (p.K + 1);
-    // tokens that a list has room for: those of the history and drafts, and of the biases as many as a request has in earnest
-    // (n_bias is all requests'); a request with more counts for each token by itself
+    // tokens that a list has room for: those of the history (of all its columns: how many are used is known on the device
+    // alone) and drafts, and of the biases as many as a request has in earnest (n_bias is all requests'); a request with more counts
+    // for each token by itself
     const int64_t touches = (int64_t)p.history_cols + (p.drafts ? p.K : 0) + (p.bias_starts ? min(p.n_bias, kBiasRoom) : 0);
+    const int64_t piece = kPieceBytes;
+    Split how = {};
     const auto split = [&](int c) -> size_t {  // a row over c CTAs: the shared memory of one
-        p.ctas = c;
-        p.share = (groups + c - 1) / c;
-        const int64_t tokens = (int64_t)p.share * 8;
-        p.cap = (int)((touches < tokens ? touches : tokens) + 3) / 4 * 4;
+        how.ctas = c;
+        how.share = (groups + c - 1) / c;
+        const int64_t tokens = (int64_t)how.share * 8, words = words_of(how.share);
+        how.cap = (int)((touches < tokens ? touches : tokens) + 3) / 4 * 4;
         if (touches == 0) return 0;
-        return ((size_t)words_of(p.share) * 6 + (size_t)p.cap * 6 + 15) / 16 * 16;
+        // (reached by clusters of eight alone: sixteen have room for a list of their whole share)
+        const int64_t room = (kSmemMax - piece - words * 6) / 6 / 4 * 4;
+        if (c == most && how.cap > room) how.cap = (int)room;
+        return ((size_t)words * 6 + (size_t)how.cap * 6 + 15) / 16 * 16;
     };
     // As few CTAs as hold a row, with two slots beside what the listed tokens need, twice on an SM; where that leaves SMs
     // idle, more, down to eight values a thread: two or four as long as all have a place at once (64 rows of 128259: 18.0 us
     // with four, 28.0 with one), eight or sixteen for half the SMs at most (32 rows: 12.9 us with four, 15.2 with eight, as
     // clusters of eight do not fill the chip; one row: 9.1 with sixteen, 12.0 with four).
-    const int64_t piece = kPieceBytes;
     int c = 1;
-    while (c < kMaxCluster && ((int64_t)((groups + c - 1) / c) * 8 * (int)sizeof(TI) > kShareBytes || (int64_t)split(c) + 2 * piece > kSmemTwo)) c *= 2;
-    while (c < kMaxCluster && rows * c * 2 <= (c < 4 ? 2 * num_sms : num_sms / 2) && groups > c * kThreads) c *= 2;
-    size_t smem = split(c);
-    const int need = (p.share + kThreads - 1) / kThreads;
-    p.slots = 0;
-    if (need > 2) {
-        const int64_t all = ((int64_t)p.share * 8 * sizeof(TI) + piece - 1) / piece, given = (int64_t)smem + 2 * piece <= kSmemTwo ? kSmemTwo : kSmemMax;
-        const int64_t room = (given - (int64_t)smem) / piece;
-        p.slots = (int)(room < all ? room : all);
-        if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-        if (p.slots < 1) return cudaErrorInvalidConfiguration;
-        smem += (size_t)p.slots * piece;
+    while (c < most && ((int64_t)((groups + c - 1) / c) * 8 * (int)sizeof(TI) > kShareBytes || (int64_t)split(c) + 2 * piece > kSmemTwo)) c *= 2;
+    while (c < most && rows * c * 2 <= (c < 4 ? 2 * num_sms : num_sms / 2) && groups > c * kThreads) c *= 2;
+    how.smem = split(c);
+    how.slots = 0;
+    if (how.share > 2 * kThreads) {
+        const int64_t all = ((int64_t)how.share * 8 * sizeof(TI) + piece - 1) / piece;
+        const int64_t given = (int64_t)how.smem + 2 * piece <= kSmemTwo ? kSmemTwo : kSmemMax, room = (given - (int64_t)how.smem) / piece;
+        how.slots = (int)(room < all ? room : all);
+        if (how.slots > kMaxSlots) how.slots = kMaxSlots;
+        how.smem += (size_t)how.slots * piece;
     }
-    if (smem > (size_t)kSmemMax) return cudaErrorInvalidConfiguration;
-    return need <= 1   ? launch_one<TI, 1>(p, smem, stream, pdl)
-           : need <= 2 ? launch_one<TI, 2>(p, smem, stream, pdl)
-                       : launch_one<TI, 0>(p, smem, stream, pdl);
+    return how;
+}
+// the longest row over the fewest CTAs that a device may be limited to: a share that streams, with one slot at least
+static_assert((int64_t)(kMaxProbsVocab + 7) / 8 / 8 * 8 * 4 <= kShareBytes, "eight CTAs hold the longest row");
+
+template <typename TI>
+cudaError_t launch_types(const ProbsParams &p, int num_sms, cudaStream_t stream, bool pdl) {
+    bool no_room = false;
+    for (int most = p.max_cluster;; most = 8) {
+        const Split how = split_rows<TI>(p, num_sms, most);
+        if ((how.share > 2 * kThreads && how.slots < 1) || how.smem > (size_t)kSmemMax) return cudaErrorInvalidConfiguration;
+        no_room = false;
+        const cudaError_t e = how.share <= kThreads       ? launch_one<TI, 1>(p, how, stream, pdl, &no_room)
+                              : how.share <= 2 * kThreads ? launch_one<TI, 2>(p, how, stream, pdl, &no_room)
+                                                          : launch_one<TI, 0>(p, how, stream, pdl, &no_room);
+        if (!no_room) return e;
+    }
 }
 
 }  // namespace
