@@ -162,7 +162,7 @@ def _check(rc: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream, dev=None):
@@ -200,15 +200,15 @@ def sched_meta(desc: Desc, cache_seqlens, meta, stream=None, lib=None):
                                                  meta.numel() * meta.element_size(), _stream(stream)))
 
 
-def _block_scales(desc, k_scale, v_scale):
+def _block_scales(desc, dev, k_scale, v_scale):
     """Refuses scales that are not the block formats' (the per-head format's are far shorter: the kernel would read past
-    their end). None is left to the library's own check."""
+    their end) or not on device ``dev``, the pool's. None is left to the library's own check."""
     import torch
-    dev, shape = _device(), (desc.num_pages, desc.H_kv, desc.page_size // 16)
-    n = shape[0] * shape[1] * shape[2]
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is not None and not (t.dtype is torch.float32 and t.get_device() == dev and t.is_contiguous() and t.numel() == n):
-            raise DecodeAttnError(f"{name}: want a contiguous torch.float32 tensor of shape {shape} on the current CUDA device, "
+    f32, n = torch.float32, desc.num_pages * desc.H_kv * (desc.page_size // 16)
+    for t in (k_scale, v_scale):
+        if t is not None and not (t.dtype is f32 and t.numel() == n and t.get_device() == dev and t.is_contiguous()):
+            raise DecodeAttnError(f"scales of a block format: want contiguous {f32} tensors of shape "
+                                  f"{(desc.num_pages, desc.H_kv, desc.page_size // 16)} on the pool's device, "
                                   f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
 
@@ -218,7 +218,7 @@ def fwd(desc: Desc, q, k_pool, v_pool, k_scale, v_scale, block_table, cache_seql
     are checked here."""
     lib = lib or load_library()
     if desc.kv_dtype in (KV_FP8_BLOCK, KV_INT8_BLOCK):
-        _block_scales(desc, k_scale, v_scale)
+        _block_scales(desc, k_pool.get_device(), k_scale, v_scale)
     args = (ctypes.byref(desc), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
             _ptr(block_table), _ptr(cache_seqlens), _ptr(meta), meta.numel() * meta.element_size(),
             _ptr(out), _ptr(lse))
@@ -245,7 +245,7 @@ def fwd_static_scratch(desc: Desc, q, k_pool, v_pool, k_scale, v_scale, block_ta
     overlapping calls race)."""
     lib = load_library()
     if desc.kv_dtype in (KV_FP8_BLOCK, KV_INT8_BLOCK):
-        _block_scales(desc, k_scale, v_scale)
+        _block_scales(desc, k_pool.get_device(), k_scale, v_scale)
     f = lib.decode_attn_fwd_static_scratch
     if not f.argtypes:       # (without them a stream's handle would be cut to 32 bits)
         P = ctypes.c_void_p

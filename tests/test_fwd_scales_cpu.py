@@ -35,11 +35,6 @@ def _desc(**kw):
     return da.Desc.make(**{**base, **kw})
 
 
-@pytest.fixture(autouse=True)
-def _host_is_the_device(monkeypatch):
-    monkeypatch.setattr(da, "_device", lambda: -1)        # where host tensors are
-
-
 def _calls(monkeypatch):
     """Each attention call of the binding as f(desc, k_scale, v_scale), with the library that it reaches."""
     t = torch.zeros(8)
@@ -52,7 +47,7 @@ def _calls(monkeypatch):
 
 GOOD = torch.zeros(40, 2, 4)
 BAD = [torch.zeros(2), torch.zeros(40, 2, 3), torch.zeros(39, 2, 4), torch.zeros(40, 2, 4, dtype=torch.bfloat16),
-       torch.zeros(40, 2, 8)[:, :, ::2], torch.zeros(1, 2, 4).expand(40, 2, 4), torch.zeros(0)]
+       torch.zeros(40, 2, 8)[:, :, ::2], torch.zeros(1, 2, 4).expand(40, 2, 4), torch.zeros(0)]  # (another device: test_gpu_fwd_scales.py)
 
 
 @pytest.mark.parametrize("kv", [da.KV_FP8_BLOCK, da.KV_INT8_BLOCK])
