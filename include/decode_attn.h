@@ -582,9 +582,8 @@ typedef struct {
  *     likewise with probs_stride (0: V, else >= V; rows aligned to their type only). probs may
  *     be logits itself (same type and stride); else they must not overlap
  *     (DA_ERR_UNSUPPORTED).
- *   rules: NULL for none. Tokens outside [0, V) in any of its lists are ignored. A request's
- *     biases are searched through for every token that has one, and one with more than
- *     1024 of them, its history too: meant for hundreds, not for a bias on every token.
+ *   rules: NULL for none. Tokens outside [0, V) in any of its lists are ignored. A request
+ *     may have any number of biases, one on every token too.
  * x is fp32 in the order above, each step rounded; exponentials are the hardware's ex2 (2
  * ulp), sums fp32 in a fixed order; p is rounded once to its type. Launches one kernel on
  * `stream`. No allocation, no sync.

@@ -24,8 +24,11 @@
 // way: a bit per token of the share, a prefix sum over its words, and so a place for each
 // in a list, with its count (and marks: in the prompt, has a bias). They are left out
 // of the first walk; a thread per listed token then computes its x, which takes its
-// part in maximum and sum, and is written over what the second walk left there. Biases
-// are added in the list's order, so that a token that stands twice has one result.
+// part in maximum and sum, and is written over what the second walk left there. A token's
+// biases are added in their order, so that one that stands twice has one result. Where there are
+// many, a pass over them adds each to its token's x (looked through by every token that has one, as a
+// few are, a bias on each of 131072 tokens took 342 ms for one row, now 0.57); and where the list is too short
+// for a share's tokens, they are taken window by window.
 //
 // Sums: a thread's own in fp32, then warps, then the (largest, sum) pairs of the CTAs, in a
 // fixed order.
@@ -59,6 +62,9 @@ constexpr int kMaxSlots = 12;
 constexpr int kAhead = 8, kAbreast = 4;        // tokens of the history, listed tokens that a thread has under way
 constexpr int kSmemMax = 224 << 10, kSmemTwo = 112 << 10;  // of a CTA; where two fit an SM
 constexpr int kBiasRoom = 1024;
+// biases of a request that every token with one looks through; more are added to the list's x instead (two barriers more and a chain of
+// loads: one row of 32000 with up to 4 biases 8.6 instead of 7.3 us, 576 rows of 131072 with up to 300 125 instead of 225)
+constexpr int kFewBiases = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kPrompt = 0x80000000u, kBias = 0x40000000u, kCount = kBias - 1;
 
@@ -242,38 +248,243 @@ struct Run {
 // Words of a share's marks, a run of eight for each thread that has one: those of a share fit.
 static_assert(kShareBytes / 2 / 32 <= 8 * kThreads, "a run of eight words per thread");
 __host__ __device__ inline int words_of(int share) { return (share * 8 + 255) / 256 * 8; }
+__host__ __device__ inline int many_words(int cap) { return (cap + 127) / 128 * 4; }  // a bit per place of a list
 
-// What x becomes of a logit with a count and marks (kPrompt, kBias, kCount).
-__device__ __forceinline__ float adjusted(const ProbsParams &p, int t, float y, uint32_t c, float rep, float freq, float pres,
-                                          int blo, int bhi) {
+// What x becomes, but for its biases, of a logit with a count and marks (kPrompt, kCount).
+__device__ __forceinline__ float penalised(float y, uint32_t c, float rep, float freq, float pres) {
     const uint32_t n = c & kCount;
     if (n > 0 || (c & kPrompt)) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
     y = __fsub_rn(y, __fmul_rn(freq, (float)n));
-    if (n > 0) y = __fsub_rn(y, pres);
-    if (c & kBias)
-        for (int e = blo; e < bhi; ++e)
-            if (p.bias_tokens[e] == t) y = __fadd_rn(y, p.bias_values[e]);
-    return y;
-}
-// x of token t in row j of request b, counted by itself: for requests with more tokens than a list has room for. Out of line: the
-// walks' registers.
-__device__ __noinline__ float counted(const ProbsParams &p, int b, int j, int t, float logit) {
-    const int n_hist = p.history ? min(max(p.history_lens[b], 0), p.history_cols) : 0, prompt = p.prompt_lens ? p.prompt_lens[b] : 0;
-    const int32_t *hist = p.history + (int64_t)b * p.history_cols, *drafts = p.drafts + (int64_t)b * p.K;
-    uint32_t c = kBias;
-    for (int i = 0; i < n_hist; ++i)
-        if (hist[i] == t) c = i < prompt ? c | kPrompt : c + 1;
-    for (int i = 0; p.drafts != nullptr && i < j && drafts[i] >= 0; ++i) c += drafts[i] == t;
-    const int blo = p.bias_starts ? min(max(p.bias_starts[b], 0), p.n_bias) : 0;
-    const int bhi = p.bias_starts ? min(max(p.bias_starts[b + 1], 0), p.n_bias) : 0;
-    const float y = adjusted(p, t, logit, c, p.repetition ? p.repetition[b] : 1.f, p.frequency ? p.frequency[b] : 0.f,
-                             p.presence ? p.presence[b] : 0.f, blo, bhi);
-    const uint32_t *bits = p.allowed ? p.allowed + ((int64_t)b * (p.K + 1) + j) * p.allowed_stride : nullptr;
-    return !bits || (bits[t >> 5] >> (t & 31) & 1) ? y : -INFINITY;
+    return n > 0 ? __fsub_rn(y, pres) : y;
 }
 
-// kG: groups of eight values that a thread holds between the walks; 0: the share streams
-template <typename TI, int kG>
+// The list of the touched tokens in shared memory: those of [lowest, lowest + span), of which `before` of the share's stand in
+// front. From `mark` on there lie: a bit per token of the share (`words` of them); for each listed token (cap) its count and marks, then
+// its x; for each a bit, whether it has several biases; for each word the marks in the words before, without multiples of
+// 65536; the listed tokens, from t0 on, without 65536: they ascend, `upper` and up have it.
+struct List {
+    uint32_t *mark;
+    int words, cap;
+    int t0, lowest, span, before, upper;
+    __device__ __forceinline__ uint32_t *value() const { return mark + words; }
+    __device__ __forceinline__ uint32_t *many() const { return mark + words + cap; }
+    __device__ __forceinline__ uint16_t *place() const { return reinterpret_cast<uint16_t *>(mark + words + cap + many_words(cap)); }
+    __device__ __forceinline__ uint16_t *tokens() const { return place() + words; }
+    __device__ __forceinline__ int at(int i) const {  // token t0 + i, which is here
+        return (uint16_t)(place()[i / 32] + __popc(mark[i / 32] & ((1u << (i & 31)) - 1)) - before);
+    }
+    __device__ __forceinline__ int place_of(int token) const {  // -1: not here
+        return (unsigned)(token - lowest) < (unsigned)span ? at(token - t0) : -1;
+    }
+    __device__ __forceinline__ int token_at(int k) const { return t0 + tokens()[k] + (k >= upper ? 65536 : 0); }
+    __device__ __forceinline__ uint32_t *enlist(int i) const {  // token t0 + i
+        const int k = at(i);
+        tokens()[k] = (uint16_t)i;
+        return value() + k;
+    }
+    __device__ __forceinline__ void enlist_bias(int i) const {
+        uint32_t *v = enlist(i);
+        const int k = (int)(v - value());
+        if (atomicOr(v, kBias) & kBias) atomicOr(many() + k / 32, 1u << (k & 31));
+    }
+    __device__ __forceinline__ bool has_many(int k) const { return many()[k / 32] >> (k & 31) & 1; }
+};
+// f(token, its index) for the tokens [from, to) of an array, kAhead loads of a thread under way at once.
+template <typename F>
+__device__ __forceinline__ void each_token(const int32_t *tokens, int from, int to, F f) {
+    for (int i0 = from + (int)threadIdx.x; i0 < to; i0 += kAhead * kThreads) {
+        int tok[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) tok[k] = i0 + k * kThreads < to ? tokens[i0 + k * kThreads] : -1;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (tok[k] >= 0) f(tok[k], i0 + k * kThreads);
+    }
+}
+// The biases [lo, hi), added to the x of the list, each token's in their order: a token with one bias takes it from whichever thread
+// meets it; those with several, if there are any, from one warp that goes through the biases in order. All threads of the CTA;
+// the sums are there when it returns. (Inlined, as what follows: called out of line they made the walks around them spill.)
+__device__ __forceinline__ void add_biases(const ProbsParams &p, List l, int lo, int hi) {
+    bool later = false;
+    __syncthreads();
+    for (int i0 = lo + (int)threadIdx.x; i0 < hi; i0 += kAhead * kThreads) {
+        int tok[kAhead];
+        float v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k * kThreads;
+            tok[k] = i < hi ? p.bias_tokens[i] : -1;
+            v[k] = i < hi ? p.bias_values[i] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int at = l.place_of(tok[k]);
+            if (at < 0) continue;
+            if (l.has_many(at))
+                later = true;
+            else
+                l.value()[at] = __float_as_uint(__fadd_rn(__uint_as_float(l.value()[at]), v[k]));
+        }
+    }
+    if (!__syncthreads_or(later)) return;
+    if (threadIdx.x < 32) {
+        const int lane = (int)threadIdx.x;
+        for (int i0 = lo; i0 < hi; i0 += 32) {
+            int at = i0 + lane < hi ? l.place_of(p.bias_tokens[i0 + lane]) : -1;
+            if (at >= 0 && !l.has_many(at)) at = -1;
+            const float v = at >= 0 ? p.bias_values[i0 + lane] : 0.f;
+            // lanes with the same token: one behind the other
+            const unsigned here = __ballot_sync(0xFFFFFFFFu, at >= 0);
+            const int turn = at >= 0 ? __popc(__match_any_sync(here, at) & ((1u << lane) - 1)) : -1;
+            const int last = __reduce_max_sync(0xFFFFFFFFu, turn);
+            for (int k = 0; k <= last; ++k) {
+                if (k == turn) l.value()[at] = __float_as_uint(__fadd_rn(__uint_as_float(l.value()[at]), v));
+                __syncwarp();
+            }
+        }
+    }
+    __syncthreads();
+}
+// Draft `tid` of a chain, where it stands before row j and the chain has not ended before it; else -1.
+__device__ __forceinline__ int draft_before(const ProbsParams &p, int b, int j, int tid) {
+    if (p.drafts == nullptr || tid >= j) return -1;
+    const int32_t *drafts = p.drafts + (int64_t)b * p.K;
+    int signs = 0;
+    for (int i = 0; i < tid; ++i) signs |= drafts[i];
+    return signs < 0 ? -1 : drafts[tid];
+}
+
+// A row, and a CTA's share of it.
+template <typename TI>
+struct Place {
+    int row, rank, b, j;
+    const TI *in;        // the row's logits
+    int t0, groups;      // token of the share's first value; group g holds t0 + 8 g ..
+    const uint32_t *bits;
+    int n_hist, prompt, blo, bhi;
+    __device__ __forceinline__ Place(const ProbsParams &p) {
+        row = blockIdx.x / p.ctas, rank = blockIdx.x - row * p.ctas;
+        b = row / (p.K + 1), j = row - b * (p.K + 1);
+        in = static_cast<const TI *>(p.logits) + row * p.logits_stride;
+        t0 = rank * p.share * 8 - (int)(reinterpret_cast<uintptr_t>(in) / sizeof(TI) & 7);
+        groups = max(min(p.share, (p.V - t0 + 7) / 8), 0);
+        bits = p.allowed ? p.allowed + row * p.allowed_stride : nullptr;
+        n_hist = p.history ? min(max(p.history_lens[b], 0), p.history_cols) : 0;
+        prompt = p.prompt_lens ? p.prompt_lens[b] : 0;
+        blo = p.bias_starts ? min(max(p.bias_starts[b], 0), p.n_bias) : 0;
+        bhi = p.bias_starts ? min(max(p.bias_starts[b + 1], 0), p.n_bias) : 0;
+    }
+    __device__ __forceinline__ List list(const ProbsParams &p) const {
+        extern __shared__ uint4 smem_v[];
+        uint32_t *mark = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(smem_v) + (size_t)p.slots * kPieceBytes);
+        const int lowest = max(t0, 0);
+        return {mark, words_of(p.share), p.cap, t0, lowest, min(p.V - t0, groups * 8) - (lowest - t0), 0, INT32_MAX};
+    }
+};
+
+// x, biases and all, of the listed tokens, in place of their counts and marks.
+template <typename TI>
+__device__ __forceinline__ void settle(const ProbsParams &p, const Place<TI> &at, const List &l, int listed) {
+    const float rep = p.repetition ? p.repetition[at.b] : 1.f, freq = p.frequency ? p.frequency[at.b] : 0.f;
+    const float pres = p.presence ? p.presence[at.b] : 0.f;
+    for (int i = threadIdx.x; i < listed; i += kThreads)
+        l.value()[i] = __float_as_uint(penalised(static_cast<float>(at.in[l.token_at(i)]), l.value()[i], rep, freq, pres));
+    if (at.bhi > at.blo) add_biases(p, l, at.blo, at.bhi);
+}
+template <typename TI>
+__device__ __forceinline__ void settle_list(const ProbsParams &p, int listed) {
+    const Place<TI> at(p);
+    List l = at.list(p);
+    if (l.words > 65536 / 32) l.upper = l.place()[65536 / 32];
+    settle(p, at, l, listed);
+}
+
+// The touched tokens of a share that has more of them than the list has room for (p.cap), window by window: as many runs of 256 tokens as
+// the list holds, enlisted anew from history, drafts and biases. What each thread has met of them, (largest, sum) or (largest, its
+// token); or their probabilities are written. All threads of the CTA.
+enum class Crowd { kSum, kLargest, kWrite, kWriteZero, kWriteNan };
+template <typename TI>
+__device__ __forceinline__ float2 crowded_tokens(const ProbsParams &p, Crowd what, float scale, float from, float off) {
+    constexpr int kRunTokens = 256;
+    __shared__ int sums[kWarps + 1];
+    const Place<TI> at(p);
+    const List whole = at.list(p);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, runs = whole.words / 8;
+    Run run;
+    const int32_t *hist = p.history + (int64_t)at.b * p.history_cols;
+    const int draft = draft_before(p, at.b, at.j, tid);
+    const int out_size = p.prob_dtype == DA_PROB_F32 ? 4 : 2;
+    uint8_t *out = static_cast<uint8_t *>(p.probs) + at.row * p.probs_stride * out_size;
+    // marks up to the end of this thread's run
+    int end = 0;
+    for (int k = 0; k < 8 && tid < runs; ++k) end += __popc(whole.mark[tid * 8 + k]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, end, o);
+        if (lane >= o) end += u;
+    }
+    if (lane == 31) sums[warp] = end;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) end += sums[w];
+    for (int r0 = 0, base = 0; r0 < runs;) {
+        // (a run fits: a list that may be too short has room for 1024 tokens)
+        const int r1 = r0 + __syncthreads_count(tid >= r0 && tid < runs && end - base <= p.cap);
+        if (tid == r1 - 1) sums[kWarps] = end;
+        List l = whole;
+        for (int i = tid; i < p.cap; i += kThreads) l.value()[i] = 0u;
+        for (int i = tid; i < many_words(p.cap); i += kThreads) l.many()[i] = 0u;
+        __syncthreads();
+        const int n = sums[kWarps] - base;
+        l.lowest = max(whole.lowest, l.t0 + r0 * kRunTokens);
+        l.span = max(min(whole.lowest + whole.span, l.t0 + r1 * kRunTokens) - l.lowest, 0);
+        l.before = base;
+        l.upper = r0 * kRunTokens >= 65536 ? 0 : r1 * kRunTokens > 65536 ? (uint16_t)(l.place()[65536 / 32] - base) : INT32_MAX;
+        const auto here = [&](int token) -> bool { return (unsigned)(token - l.lowest) < (unsigned)l.span; };
+        each_token(hist, 0, at.n_hist, [&](int token, int i) {
+            if (!here(token)) return;
+            uint32_t *v = l.enlist(token - l.t0);
+            if (i < at.prompt)
+                atomicOr(v, kPrompt);
+            else
+                atomicAdd(v, 1u);
+        });
+        if (draft >= 0 && here(draft)) atomicAdd(l.enlist(draft - l.t0), 1u);
+        each_token(p.bias_tokens, at.blo, at.bhi, [&](int token, int) {
+            if (here(token)) l.enlist_bias(token - l.t0);
+        });
+        __syncthreads();
+        settle(p, at, l, n);
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+            const int t = l.token_at(i);
+            const float y = __uint_as_float(l.value()[i]);
+            const float v = !at.bits || (at.bits[t >> 5] >> (t & 31) & 1) ? y : -INFINITY;
+            if (what == Crowd::kSum) {
+                const float to = run.raise(v, scale);
+                run.sum += ex2((v - to) * scale);
+            } else if (what == Crowd::kLargest) {
+                run.take(v, t);
+            } else {
+                const float x = what == Crowd::kWrite ? Exps{from, scale, off}(v) : what == Crowd::kWriteZero ? 0.f : NAN;
+                if (p.prob_dtype == DA_PROB_F32)
+                    store1(reinterpret_cast<float *>(out) + t, x);
+                else if (p.prob_dtype == DA_PROB_BF16)
+                    store1(reinterpret_cast<__nv_bfloat16 *>(out) + t, x);
+                else
+                    store1(reinterpret_cast<__half *>(out) + t, x);
+            }
+        }
+        base += n;
+        r0 = r1;
+    }
+    __syncthreads();
+    return make_float2(run.m, what == Crowd::kLargest ? __int_as_float(run.at) : run.sum);
+}
+
+// kG: groups of eight values that a thread holds between the walks; 0: the share streams. kMany: built for requests that may have many
+// biases or more tokens than the list has room for (which costs the others: 1024 rows of 131072 with histories 200 instead of
+// 190 us, one row of 32000 7.5 instead of 7.0).
+template <typename TI, int kG, bool kMany>
 __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constant__ ProbsParams p) {
     extern __shared__ uint4 smem_v[];
     __shared__ float2 warp_pair[kWarps];
@@ -288,17 +499,15 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = blockIdx.x / p.ctas, rank = blockIdx.x - row * p.ctas;
-    const int b = row / (p.K + 1), j = row - b * (p.K + 1);
+    const Place<TI> here(p);
+    const int row = here.row, rank = here.rank, b = here.b, j = here.j;
     const int V = p.V;
-    const TI *in = static_cast<const TI *>(p.logits) + row * p.logits_stride;
+    const TI *in = here.in;
     const int out_size = p.prob_dtype == DA_PROB_F32 ? 4 : 2;
     uint8_t *out_at = static_cast<uint8_t *>(p.probs) + row * p.probs_stride * out_size;
-    const int head = (int)(reinterpret_cast<uintptr_t>(in) / sizeof(TI) & 7);
-    const bool vec = (int)(reinterpret_cast<uintptr_t>(out_at) / out_size & 7) == head;
-    const int t0 = rank * p.share * 8 - head;  // token of the share's first value; group g holds t0 + 8 g ..
-    const int groups = max(min(p.share, (V - t0 + 7) / 8), 0);
-    const uint32_t *bits = p.allowed ? p.allowed + row * p.allowed_stride : nullptr;
+    const bool vec = (int)(reinterpret_cast<uintptr_t>(out_at) / out_size & 7) == (int)(reinterpret_cast<uintptr_t>(in) / sizeof(TI) & 7);
+    const int t0 = here.t0, groups = here.groups;
+    const uint32_t *bits = here.bits;
     const int words = (V + 31) / 32;
 
     // the logits of a group, -infinity where there is none
@@ -330,18 +539,9 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
         bulk_load(reinterpret_cast<uint8_t *>(smem_v) + (size_t)slot * kPieceBytes, in + t0 + g * 8, bytes, &full[slot]);
     };
     // what the lists and the walks wait for, read ahead of the rest
-    const int n_hist = p.history ? min(max(p.history_lens[b], 0), p.history_cols) : 0;
-    const int blo = p.bias_starts ? min(max(p.bias_starts[b], 0), p.n_bias) : 0;
-    const int bhi = p.bias_starts ? min(max(p.bias_starts[b + 1], 0), p.n_bias) : 0;
-    const int prompt = p.prompt_lens ? p.prompt_lens[b] : 0;
+    const int n_hist = here.n_hist, blo = here.blo, bhi = here.bhi, prompt = here.prompt;
     const float T = p.temperature ? p.temperature[b] : 1.f;
-    int draft = -1;  // draft tid, where it stands before this row and the chain has not ended before it
-    if (p.drafts != nullptr && tid < j) {
-        const int32_t *drafts = p.drafts + (int64_t)b * p.K;
-        int signs = 0;
-        for (int i = 0; i < tid; ++i) signs |= drafts[i];
-        draft = signs < 0 ? -1 : drafts[tid];
-    }
+    const int draft = draft_before(p, b, j, tid);
     if (kG == 0 && tid == 0) {
         for (int k = 0; k < slots; ++k) {
             mbar_init(&full[k], 1);
@@ -414,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
                                                   (kG == 0 ? (size_t)slots * kPieceBytes : 0));  // a bit per token of the share
     // of each listed token: count and marks, then x
     uint32_t *value = mark + share_words;
-    uint16_t *place = reinterpret_cast<uint16_t *>(value + p.cap);  // marks in the words before
+    uint16_t *place = reinterpret_cast<uint16_t *>(value + p.cap + many_words(p.cap));  // marks in the words before
     uint16_t *list = place + share_words;  // the listed tokens, from t0 on, without 65536: they ascend, `upper` and up have it
     int upper = INT32_MAX;
     const auto token_at = [&](int i) -> int { return t0 + list[i] + (i >= upper ? 65536 : 0); };
@@ -426,6 +626,8 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
         const int cap = (min(p.cap, n_hist + j + bhi - blo) + 3) / 4;
         for (int i = tid; i < share_words / 4; i += kThreads) reinterpret_cast<uint4 *>(mark)[i] = make_uint4(0u, 0u, 0u, 0u);
         for (int i = tid; i < cap; i += kThreads) reinterpret_cast<uint4 *>(value)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (kMany && bhi - blo > kFewBiases)
+            for (int i = tid; i < many_words(4 * cap); i += kThreads) value[p.cap + i] = 0u;
         __syncthreads();
         const int lowest = max(t0, 0), span = min(V - t0, groups * 8) - (lowest - t0);
         // f(token's place in the share) for every token of the history in [from, to)
@@ -493,12 +695,16 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
             list[at] = (uint16_t)i;
             return value + at;
         };
-        crowded = listed > p.cap;
+        crowded = kMany && listed > p.cap;
         if (!crowded) {
             each(0, min(prompt, n_hist), [&](int i) { atomicOr(enlist(i), kPrompt); });
             each(max(prompt, 0), n_hist, [&](int i) { atomicAdd(enlist(i), 1u); });
             drafted([&](int i) { atomicAdd(enlist(i), 1u); });
-            biased([&](int i) { atomicOr(enlist(i), kBias); });
+            biased([&](int i) {
+                uint32_t *v = enlist(i);
+                if (const uint32_t was = atomicOr(v, kBias); kMany && bhi - blo > kFewBiases && (was & kBias))
+                    atomicOr(value + p.cap + (v - value) / 32, 1u << ((v - value) & 31));
+            });
         }
         __syncthreads();
     }
@@ -610,22 +816,23 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
             }
         }
     }
-    // the listed tokens; or, where they are too many for that, the marked ones
-    if (crowded) {
-        for (int w = tid; w < share_words; w += kThreads)
-            for (uint32_t m = mark[w]; m; m &= m - 1) {
-                const int t = t0 + w * 32 + __ffs(m) - 1;
-                const float v = counted(p, b, j, t, static_cast<float>(in[t]));
-                if (warm) {
-                    const float from = run.raise(v, scale);
-                    run.sum += ex2((v - from) * scale);
-                } else {
-                    run.take(v, t);
-                }
-            }
+    // the listed tokens
+    if (kMany && crowded) {
+        const float2 met = crowded_tokens<TI>(p, warm ? Crowd::kSum : Crowd::kLargest, scale, 0.f, 0.f);
+        if (warm) {
+            const float from = run.raise(met.x, scale);
+            run.sum += met.y * ex2((met.x - from) * scale);  // (none: 0 times 0)
+        } else {
+            run.take(met.x, __float_as_int(met.y));
+        }
     } else if (listed > 0) {
         const float rep = p.repetition ? p.repetition[b] : 1.f, freq = p.frequency ? p.frequency[b] : 0.f;
         const float pres = p.presence ? p.presence[b] : 0.f;
+        const bool summed = kMany && bhi - blo > kFewBiases;  // x stands in the list then, biases and all
+        if (summed) {
+            settle_list<TI>(p, listed);
+            __syncthreads();
+        }
         for (int i0 = tid; i0 < listed; i0 += kAbreast * kThreads) {
             int t[kAbreast];
             float v[kAbreast];
@@ -633,14 +840,20 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
             for (int k = 0; k < kAbreast; ++k) {
                 const int i = i0 + k * kThreads;
                 t[k] = i < listed ? token_at(i) : 0;
-                v[k] = i < listed ? static_cast<float>(in[t[k]]) : -INFINITY;
+                v[k] = i >= listed ? -INFINITY : summed ? __uint_as_float(value[i]) : static_cast<float>(in[t[k]]);
             }
             float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kAbreast; ++k) {
                 const int i = i0 + k * kThreads;
                 if (i >= listed) continue;
-                const float y = adjusted(p, t[k], v[k], value[i], rep, freq, pres, blo, bhi);
+                float y = v[k];
+                if (!summed) {
+                    y = penalised(y, value[i], rep, freq, pres);
+                    if (value[i] & kBias)
+                        for (int e = blo; e < bhi; ++e)
+                            if (p.bias_tokens[e] == t[k]) y = __fadd_rn(y, p.bias_values[e]);
+                }
                 v[k] = !bits || (bits[t[k] >> 5] >> (t[k] & 31) & 1) ? y : -INFINITY;
                 value[i] = __float_as_uint(v[k]);
                 if (!warm) run.take(v[k], t[k]);
@@ -722,15 +935,6 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
             probabilities(g, r, v);
             store_group(row, t0 + g * 8, V, vec, written(g), v);
         };
-        if (crowded && warm) {  // ahead of the walk: it may write over the logits
-            for (int w = tid; w < share_words; w += kThreads)
-                for (uint32_t m = mark[w]; m; m &= m - 1) {
-                    const int t = t0 + w * 32 + __ffs(m) - 1;
-                    const float v = exps(counted(p, b, j, t, static_cast<float>(in[t])));
-                    store1(row + t, bad ? NAN : nothing ? 0.f : v);
-                }
-            __syncthreads();
-        }
         if constexpr (kG > 0) {
 #pragma unroll
             for (int k = 0; k < kG; ++k)
@@ -799,6 +1003,8 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
             }
         }
     };
+    if (kMany && crowded && warm)  // ahead of the walk: it may write over the logits
+        crowded_tokens<TI>(p, bad ? Crowd::kWriteNan : nothing ? Crowd::kWriteZero : Crowd::kWrite, scale, from, off);
     if (p.prob_dtype == DA_PROB_F32)
         second(reinterpret_cast<float *>(out_at));
     else if (p.prob_dtype == DA_PROB_BF16)
@@ -815,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
 
 // Whether the current device can hold a cluster of 16 CTAs of this kernel, asked once per device for CTAs of which two fit an SM and
 // for larger ones (by the most shared memory that such a one takes). cfg: of the launch, attr[0] its cluster.
-template <typename TI, int kG>
+template <typename TI, int kG, bool kMany>
 bool wide_clusters(cudaLaunchConfig_t cfg, cudaLaunchAttribute *attr) {
     static std::atomic<int> known[64][2];  // 1: no, 2: yes
     int dev = 0;
@@ -828,7 +1034,7 @@ bool wide_clusters(cudaLaunchConfig_t cfg, cudaLaunchAttribute *attr) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        const bool ok = cudaOccupancyMaxActiveClusters(&n, probs_kernel<TI, kG>, &cfg) == cudaSuccess && n >= 1;
+        const bool ok = cudaOccupancyMaxActiveClusters(&n, probs_kernel<TI, kG, kMany>, &cfg) == cudaSuccess && n >= 1;
         if (!ok) cudaGetLastError();
         k = ok ? 2 : 1;
         known[dev][large].store(k, std::memory_order_relaxed);
@@ -839,16 +1045,17 @@ bool wide_clusters(cudaLaunchConfig_t cfg, cudaLaunchAttribute *attr) {
 // How a row is divided: its CTAs, groups to each, the list's room, slots of the ring, shared memory of a CTA.
 struct Split {
     int ctas, share, cap, slots;
+    bool many;
     size_t smem;
 };
 
-template <typename TI, int kG>
+template <typename TI, int kG, bool kMany>
 cudaError_t launch_one(ProbsParams p, const Split &how, cudaStream_t stream, bool pdl, bool *no_room) {
     p.ctas = how.ctas;
     p.share = how.share;
     p.cap = how.cap;
     p.slots = how.slots;
-    const auto kern = probs_kernel<TI, kG>;
+    const auto kern = probs_kernel<TI, kG, kMany>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e == cudaSuccess && p.ctas > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
@@ -866,7 +1073,7 @@ cudaError_t launch_one(ProbsParams p, const Split &how, cudaStream_t stream, boo
         attr[n].val.clusterDim = {(unsigned)p.ctas, 1, 1};
         ++n;
     }
-    if (p.ctas > 8 && !wide_clusters<TI, kG>(cfg, attr)) {
+    if (p.ctas > 8 && !wide_clusters<TI, kG, kMany>(cfg, attr)) {
         *no_room = true;
         return cudaSuccess;
     }
@@ -880,6 +1087,13 @@ cudaError_t launch_one(ProbsParams p, const Split &how, cudaStream_t stream, boo
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+template <typename TI, bool kMany>
+cudaError_t launch_held(const ProbsParams &p, const Split &how, cudaStream_t stream, bool pdl, bool *no_room) {
+    return how.share <= kThreads       ? launch_one<TI, 1, kMany>(p, how, stream, pdl, no_room)
+           : how.share <= 2 * kThreads ? launch_one<TI, 2, kMany>(p, how, stream, pdl, no_room)
+                                       : launch_one<TI, 0, kMany>(p, how, stream, pdl, no_room);
+}
+
 // rows of [0, V) over clusters of at most `most` CTAs
 template <typename TI>
 Split split_rows(const ProbsParams &p, int num_sms, int most) {
@@ -888,8 +1102,8 @@ Split split_rows(const ProbsParams &p, int num_sms, int most) {
     const int groups = (p.V + head + 7) / 8;
     const int64_t rows = (int64_t)p.B * (p.K + 1);
     // tokens that a list has room for: those of the history (of all its columns: how many are used is known on the device
-    // alone) and drafts, and of the biases as many as a request has in earnest (n_bias is all requests'); a request with more counts
-    // for each token by itself
+    // alone) and drafts, and of the biases as many as a request has in earnest (n_bias is all requests'); a share with more takes
+    // them window by window
     const int64_t touches = (int64_t)p.history_cols + (p.drafts ? p.K : 0) + (p.bias_starts ? min(p.n_bias, kBiasRoom) : 0);
     const int64_t piece = kPieceBytes;
     Split how = {};
@@ -900,9 +1114,10 @@ Split split_rows(const ProbsParams &p, int num_sms, int most) {
         how.cap = (int)((touches < tokens ? touches : tokens) + 3) / 4 * 4;
         if (touches == 0) return 0;
         // (reached by clusters of eight alone: sixteen have room for a list of their whole share)
-        const int64_t room = (kSmemMax - piece - words * 6) / 6 / 4 * 4;
-        if (c == most && how.cap > room) how.cap = (int)room;
-        return ((size_t)words * 6 + (size_t)how.cap * 6 + 15) / 16 * 16;
+        const int64_t room = (kSmemMax - piece - words * 6) * 8 / 49 / 128 * 128;
+        how.many = p.bias_starts && p.n_bias > kFewBiases;
+        if (c == most && how.cap > room) how.cap = (int)room, how.many = true;
+        return ((size_t)words * 6 + (size_t)how.cap * 6 + (size_t)many_words(how.cap) * 4 + 15) / 16 * 16;
     };
     // As few CTAs as hold a row, with two slots beside what the listed tokens need, twice on an SM; where that leaves SMs
     // idle, more, down to eight values a thread: two or four as long as all have a place at once (64 rows of 128259: 18.0 us
@@ -932,9 +1147,7 @@ cudaError_t launch_types(const ProbsParams &p, int num_sms, cudaStream_t stream,
         const Split how = split_rows<TI>(p, num_sms, most);
         if ((how.share > 2 * kThreads && how.slots < 1) || how.smem > (size_t)kSmemMax) return cudaErrorInvalidConfiguration;
         no_room = false;
-        const cudaError_t e = how.share <= kThreads       ? launch_one<TI, 1>(p, how, stream, pdl, &no_room)
-                              : how.share <= 2 * kThreads ? launch_one<TI, 2>(p, how, stream, pdl, &no_room)
-                                                          : launch_one<TI, 0>(p, how, stream, pdl, &no_room);
+        const cudaError_t e = how.many ? launch_held<TI, true>(p, how, stream, pdl, &no_room) : launch_held<TI, false>(p, how, stream, pdl, &no_room);
         if (!no_room) return e;
     }
 }
