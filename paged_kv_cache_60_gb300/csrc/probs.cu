@@ -61,6 +61,10 @@ constexpr int kPieceBytes = 16 << 10;
 constexpr int kMaxSlots = 12;
 constexpr int kAhead = 8, kAbreast = 4;        // tokens of the history, listed tokens that a thread has under way
 constexpr int kSmemMax = 224 << 10, kSmemTwo = 112 << 10;  // of a CTA; where two fit an SM
+// Tokens that a list has room for at most, beside the marks of a share of 2^17 and two pieces: where two CTAs fit an SM, and else
+constexpr int kListRoomTwo = 9344, kListRoom = 27904;
+static_assert(2 * kPieceBytes + kShareBytes / 2 / 32 * 6 + kListRoomTwo * 6 + kListRoomTwo / 8 <= kSmemTwo, "two CTAs an SM");
+static_assert(2 * kPieceBytes + kShareBytes / 2 / 32 * 6 + kListRoom * 6 + kListRoom / 8 <= kSmemMax, "one");
 constexpr int kBiasRoom = 1024;
 // biases of a request that every token with one looks through; more are added to the list's x instead (two barriers more and a chain of
 // loads: one row of 32000 with up to 4 biases 8.6 instead of 7.3 us, 576 rows of 131072 with up to 300 125 instead of 225)
@@ -1101,43 +1105,39 @@ Split split_rows(const ProbsParams &p, int num_sms, int most) {
     const int head = p.logits_stride % 8 == 0 ? (int)(reinterpret_cast<uintptr_t>(p.logits) / sizeof(TI) & 7) : 7;
     const int groups = (p.V + head + 7) / 8;
     const int64_t rows = (int64_t)p.B * (p.K + 1);
-    // tokens that a list has room for: those of the history (of all its columns: how many are used is known on the device
-    // alone) and drafts, and of the biases as many as a request has in earnest (n_bias is all requests'); a share with more takes
-    // them window by window
+    // tokens that a list may need room for: those of the history and drafts, and of the biases as many as a request has in
+    // earnest (n_bias is all requests'). How much of the history's columns is used is known on the device alone: a buffer as wide as
+    // the longest text does not decide how rows are divided, the list stays as short as two CTAs an SM allow it where CTAs wait
+    // for SMs, and a share with more takes them window by window. (With room for all columns, by clusters of up to 16: 1024 rows of
+    // 131072 with up to 64 tokens in 131072 columns 775 us instead of 154, with 8192 to 16384 tokens 1250 instead of 430, with 65536
+    // to 131072 4360 instead of 3190.)
     const int64_t touches = (int64_t)p.history_cols + (p.drafts ? p.K : 0) + (p.bias_starts ? min(p.n_bias, kBiasRoom) : 0);
     const int64_t piece = kPieceBytes;
-    Split how = {};
-    const auto split = [&](int c) -> size_t {  // a row over c CTAs: the shared memory of one
-        how.ctas = c;
-        how.share = (groups + c - 1) / c;
-        const int64_t tokens = (int64_t)how.share * 8, words = words_of(how.share);
-        how.cap = (int)((touches < tokens ? touches : tokens) + 3) / 4 * 4;
-        if (touches == 0) return 0;
-        // (reached by clusters of eight alone: sixteen have room for a list of their whole share)
-        const int64_t room = (kSmemMax - piece - words * 6) * 8 / 49 / 128 * 128;
-        how.many = p.bias_starts && p.n_bias > kFewBiases;
-        if (c == most && how.cap > room) how.cap = (int)room, how.many = true;
-        return ((size_t)words * 6 + (size_t)how.cap * 6 + (size_t)many_words(how.cap) * 4 + 15) / 16 * 16;
-    };
-    // As few CTAs as hold a row, with two slots beside what the listed tokens need, twice on an SM; where that leaves SMs
-    // idle, more, down to eight values a thread: two or four as long as all have a place at once (64 rows of 128259: 18.0 us
-    // with four, 28.0 with one), eight or sixteen for half the SMs at most (32 rows: 12.9 us with four, 15.2 with eight, as
-    // clusters of eight do not fill the chip; one row: 9.1 with sixteen, 12.0 with four).
+    // As few CTAs as hold a row; where that leaves SMs idle, more, down to eight values a thread: two or four as long as all
+    // have a place at once (64 rows of 128259: 18.0 us with four, 28.0 with one), eight or sixteen for half the SMs at most (32
+    // rows: 12.9 us with four, 15.2 with eight, as clusters of eight do not fill the chip; one row: 9.1 with sixteen, 12.0
+    // with four).
     int c = 1;
-    while (c < most && ((int64_t)((groups + c - 1) / c) * 8 * (int)sizeof(TI) > kShareBytes || (int64_t)split(c) + 2 * piece > kSmemTwo)) c *= 2;
+    while (c < most && (int64_t)((groups + c - 1) / c) * 8 * (int)sizeof(TI) > kShareBytes) c *= 2;
     while (c < most && rows * c * 2 <= (c < 4 ? 2 * num_sms : num_sms / 2) && groups > c * kThreads) c *= 2;
-    how.smem = split(c);
-    how.slots = 0;
+    Split how = {};
+    how.ctas = c;
+    how.share = (groups + c - 1) / c;
+    const int64_t need = touches < (int64_t)how.share * 8 ? touches : (int64_t)how.share * 8;
+    const int64_t most_listed = rows * c <= num_sms ? kListRoom : kListRoomTwo;
+    how.cap = (int)(need < most_listed ? need + 3 : most_listed) / 4 * 4;
+    how.many = (p.bias_starts && p.n_bias > kFewBiases) || need > most_listed;
+    how.smem = touches == 0 ? 0 : ((size_t)words_of(how.share) * 6 + (size_t)how.cap * 6 + (size_t)many_words(how.cap) * 4 + 15) / 16 * 16;
     if (how.share > 2 * kThreads) {
         const int64_t all = ((int64_t)how.share * 8 * sizeof(TI) + piece - 1) / piece;
-        const int64_t given = (int64_t)how.smem + 2 * piece <= kSmemTwo ? kSmemTwo : kSmemMax, room = (given - (int64_t)how.smem) / piece;
+        const int64_t room = ((how.cap > kListRoomTwo ? kSmemMax : kSmemTwo) - (int64_t)how.smem) / piece;
         how.slots = (int)(room < all ? room : all);
         if (how.slots > kMaxSlots) how.slots = kMaxSlots;
         how.smem += (size_t)how.slots * piece;
     }
     return how;
 }
-// the longest row over the fewest CTAs that a device may be limited to: a share that streams, with one slot at least
+// the longest row over the fewest CTAs that a device may be limited to
 static_assert((int64_t)(kMaxProbsVocab + 7) / 8 / 8 * 8 * 4 <= kShareBytes, "eight CTAs hold the longest row");
 
 template <typename TI>
@@ -1145,7 +1145,7 @@ cudaError_t launch_types(const ProbsParams &p, int num_sms, cudaStream_t stream,
     bool no_room = false;
     for (int most = p.max_cluster;; most = 8) {
         const Split how = split_rows<TI>(p, num_sms, most);
-        if ((how.share > 2 * kThreads && how.slots < 1) || how.smem > (size_t)kSmemMax) return cudaErrorInvalidConfiguration;
+        if ((how.share > 2 * kThreads && how.slots < 2) || how.smem > (size_t)kSmemMax) return cudaErrorInvalidConfiguration;
         no_room = false;
         const cudaError_t e = how.many ? launch_held<TI, true>(p, how, stream, pdl, &no_room) : launch_held<TI, false>(p, how, stream, pdl, &no_room);
         if (!no_room) return e;

@@ -1,6 +1,6 @@
 """Token probabilities of rows whose shares stream: in place, where pieces are
 loaded again from rows that are being written; into rows that are aligned
-otherwise than the logits; through a ring of a single slot."""
+otherwise than the logits; with lists as long as there is room for."""
 import pytest
 import torch
 
@@ -108,8 +108,8 @@ def test_rows_loaded_again_in_place_and_unaligned(dtype, B, V, pad):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("cols", [32768, 50000])
-def test_a_ring_of_one_slot(dtype, cols):
-    """Lists that leave room for one piece beside them: 16 CTAs a row, each with a share of 32768 tokens."""
+def test_long_lists_beside_a_short_ring(dtype, cols):
+    """16 CTAs a row, each with a share of 32768 tokens and a list that leaves room for few pieces, or is too short itself."""
     B, V = 3, (1 << 19) - 7
     x = (torch.randn(B, 1, V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(cols)) * 2.5).to(dtype)
     r = _rules(B, V, cols, cols)
@@ -128,7 +128,7 @@ def test_a_ring_of_one_slot(dtype, cols):
 
 
 def test_a_history_buffer_far_wider_than_what_is_used():
-    """The buffer's row length decides how a row is divided, not the result: the same probabilities but for the order of sums."""
+    """The same probabilities, but for the order of sums."""
     B, V = 170, 131072
     x = (torch.randn(B, 1, V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)) * 2.5).to(BF16)
     narrow = _rules(B, V, 64, 5, masks=False)
@@ -138,3 +138,24 @@ def test_a_history_buffer_far_wider_than_what_is_used():
         out = torch.empty(B, 1, V, device="cuda")
         da.token_probs(x, out, **r)
         _close(out[:, 0], want, F32, 2, V)
+
+
+@pytest.mark.parametrize("dtype,B,V,cols", [(BF16, 200, 130999, 20000), (F32, 160, 131072, 40000), (BF16, 320, 65000, 65000), (BF16, 70, 131072, 131072)])
+def test_histories_longer_than_a_list(dtype, B, V, cols):
+    """Shares whose touched tokens take one window (short texts in a wide buffer), two, or many; in place; again and again the
+    same."""
+    x = (torch.randn(B, 1, V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(B)) * 2.5).to(dtype)
+    r = _rules(B, V, cols, B)
+    r["history_lens"][0], r["history_lens"][1], r["history_lens"][2] = cols, 0, 9345
+    out = torch.empty_like(x)
+    da.token_probs(x, out, **r)
+    for lo in range(0, B, 40):
+        s = {k: t[lo:lo + 40] for k, t in r.items()}
+        # a token stands there 1 time in the mean at most: 14 times or more with a chance below 1e-11, of 1e7 tokens
+        _close(out[lo:lo + 40, 0], _want(x[lo:lo + 40, 0], s, V), dtype, 14, V)
+    for _ in range(5):
+        same = torch.full_like(x, 7.0)
+        da.token_probs(x, same, **r)
+        assert torch.equal(same, out)
+    da.token_probs(x, x, **r)
+    assert torch.equal(x, out)
