@@ -583,7 +583,7 @@ typedef struct {
  *     be logits itself (same type and stride); else they must not overlap
  *     (DA_ERR_UNSUPPORTED).
  *   rules: NULL for none. Tokens outside [0, V) in any of its lists are ignored. A request
- *     may have any number of biases, one on every token too.
+ *     may have any number of biases, one on every token too (n_bias: 2^30 at most).
  * x is fp32 in the order above, each step rounded; exponentials are the hardware's ex2 (2
  * ulp), sums fp32 in a fixed order; p is rounded once to its type. Launches one kernel on
  * `stream`. No allocation, no sync.

@@ -1026,7 +1026,7 @@ int decode_attn_token_probs(int32_t B, int32_t n_draft, int32_t vocab, int32_t l
     const da_token_rules &r = rules ? *rules : kNone;
     const int64_t words = (vocab + 31) / 32, allowed_stride = r.allowed_stride ? r.allowed_stride : words;
     if (r.history && (r.history_cols < 1 || r.history_cols > (1 << 28))) return DA_ERR_DIMS;
-    if (r.bias_starts && r.n_bias < 0) return DA_ERR_DIMS;
+    if (r.bias_starts && (r.n_bias < 0 || r.n_bias > (1 << 30))) return DA_ERR_DIMS;  // (indexes run past the last by some thousands)
     if (r.allowed && (allowed_stride < words || allowed_stride > ((int64_t)1 << 34))) return DA_ERR_DIMS;
     if (!logits || !probs) return DA_ERR_NULL;
     if (r.history && !r.history_lens) return DA_ERR_NULL;
