@@ -584,6 +584,7 @@ typedef struct {
  *     (DA_ERR_UNSUPPORTED).
  *   rules: NULL for none. Tokens outside [0, V) in any of its lists are ignored. A request
  *     may have any number of biases, one on every token too (n_bias: 2^30 at most).
+ *     history_cols may be as wide as the longest text (2^28 at most): the tokens used cost, not the columns.
  * x is fp32 in the order above, each step rounded; exponentials are the hardware's ex2 (2
  * ulp), sums fp32 in a fixed order; p is rounded once to its type. Launches one kernel on
  * `stream`. No allocation, no sync.

@@ -15,10 +15,11 @@
 // through a ring of 16 KB pieces in shared memory (bulk copies, issued by one thread as the
 // slots come free); what the ring holds at the first walk's end is written first, the rest
 // comes again, out of L2 for the most part: two CTAs an SM with shares of at most 256 KB.
-// Measured on 1024 rows of 131072 bf16 logits to bf16: 131 us without a history (4.1
-// TB/s; instruction issue is the limit, 19 instructions a value for both walks), 191 with
-// histories of 1024 to 8192 tokens, 238 with masks too. (Rows held in registers throughout, by clusters of eight:
-// 308 and 476 us; 128 warps a row, whose fixed work was more than the values'.)
+// Measured on 1024 rows of 131072 bf16 logits to bf16: 109 us without a history (4.9
+// TB/s, 0.73 of the measured copy rate), 190 with histories of 1024 to 8192 tokens (30
+// instructions a value, 60 % of the issue slots; the rest are loads waited for, the lists in front of each row, and a
+// fourth wave of CTAs that is a third full), 232 with masks too. (Rows held in registers throughout, by clusters of
+// eight: 308 and 476 us; 128 warps a row, whose fixed work was more than the values'.)
 //
 // The tokens that the history, the drafts and the biases touch are few, and go their own
 // way: a bit per token of the share, a prefix sum over its words, and so a place for each
