@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const __grid_constan
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
             const int second = at + __popc(m[k]);
-            const uint32_t both = (uint32_t)at | (uint32_t)second << 16;
+            const uint32_t both = ((uint32_t)at & 0xFFFFu) | (uint32_t)second << 16;  // (a share may have more than 65535)
             at = second + __popc(m[k + 1]);
             m[k / 2] = both;  // (read by now)
         }

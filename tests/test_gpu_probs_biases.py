@@ -115,6 +115,40 @@ def test_several_on_a_token_in_their_order(V):
     _check(x, [tokens], [values])
 
 
+@pytest.mark.parametrize("V,B,in_place", [(131072, 180, False), (131072, 160, True), (250043, 104, True)])
+def test_shares_with_more_touched_tokens_than_16_bits_count(V, B, in_place):
+    """One or two CTAs a row; a few requests with a bias on nearly every token, beside some with few and none."""
+    g = torch.Generator(device="cuda").manual_seed(V + B)
+    x = (torch.randn(B, 1, V, device="cuda", generator=g) * 2.5).to(BF16)
+    n = [V + 30000 if b in (0, 7, B - 1) else (0, 5, 300)[b % 3] for b in range(B)]
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(n)]).astype(np.int32), device="cuda")
+    tokens = torch.randint(0, V, (sum(n),), device="cuda", generator=g, dtype=torch.int32)
+    values = torch.randn(sum(n), device="cuda", generator=g)
+    tokens[:V] = torch.randperm(V, device="cuda", generator=g).int()       # all of them in the first
+    request = torch.repeat_interleave(torch.arange(B, device="cuda"), torch.tensor(n, device="cuda"))
+    allowed = torch.randint(-2 ** 31, 2 ** 31, (B, 1, -(-V // 32)), device="cuda", generator=g, dtype=torch.int64).to(torch.int32)
+    v = torch.arange(V, device="cuda")
+    wants, most = [], 0
+    for b in range(B):
+        mine = request == b
+        y = x[b, 0].double().index_put_((tokens[mine].long(),), values[mine].double(), accumulate=True)
+        most = max(most, int(torch.bincount(tokens[mine], minlength=1).max())) if n[b] else most
+        wants.append(torch.softmax(torch.where((allowed[b, 0][v // 32] >> (v % 32)) & 1 == 1, y, -torch.inf), -1))
+    out = x if in_place else torch.full((B, 1, V), 7.0, device="cuda")
+    keep = x.clone()
+    da.token_probs(x, out, bias=(starts, tokens, values), allowed=allowed)
+    # x: `most` sums of magnitudes up to 30 (logits of 2.5 sigma, each sum of normal biases), for the token, the largest and the total;
+    # the exponent's four; ex2 three times; a thread's values one behind the other, then 13
+    u = 2.0 ** -24
+    rel, eps = u * (3 * most * 30 + 8 * 30 + 12 + V // 512 + 16), {True: 2.0 ** -8, False: u}[in_place]
+    for b in range(B):
+        assert ((out[b, 0].double() - wants[b]).abs() <= wants[b] * ((1 + rel) * (1 + eps) - 1) + 2.0 ** -126).all(), b
+    for _ in range(3):
+        again = torch.full_like(out, 9.0)
+        da.token_probs(keep, again, bias=(starts, tokens, values), allowed=allowed)
+        assert torch.equal(again, out)
+
+
 def test_one_token_tens_of_thousands_of_times():
     g = np.random.RandomState(1)
     V, n = 3001, 60000
