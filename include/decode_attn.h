@@ -294,7 +294,8 @@ int decode_attn_append_kv(const da_desc *desc, const void *k_new, const void *v_
  *     two), ties to even. e4m3: saturating at +-448, NaN ->
  *     0x7F. int8: saturating at +-127, NaN -> 0.
  * Where a block's scale grows, the codes of its earlier tokens are rounded to the new
- * scale (from their values, not from what was appended). A value that is appended with
+ * scale (from their values code * scale, in fp32: exact where the old scale is a power of
+ * two; not from what was appended). A value that is appended with
  * its whole block is off by at most half a step; one whose block grew later, by less
  * than a step of the final scale in int8 (halves add up), and in e4m3 by its own
  * rounding only, as long as its code stays normal (|value| >= scale / 64). The
